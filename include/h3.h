@@ -293,6 +293,165 @@ h3_status h3_adaln_modulate(const void* d_x, void* d_y, const int32_t* d_timeste
                             const int32_t* d_token_tag, const float* d_table, int32_t n_entries, int64_t n_rows,
                             int32_t hidden, int64_t x_row_stride, int64_t y_row_stride, float eps, void* stream);
 
+/* Element types of the calls that take more than bf16. */
+enum { H3_DTYPE_BF16 = 0, H3_DTYPE_F16 = 1, H3_DTYPE_F32 = 2 };
+
+/*
+ * h3_mmrope_rotate -- the rotation of h3_mmrope_qk for Q and K with their own
+ * head counts and row strides (grouped heads), and its gradient.
+ *
+ *   d_q, d_q_out       device bf16 [n_rows][n_heads][128], strides q_stride,
+ *                      q_out_stride (elements); d_q_out may be d_q
+ *   d_k, d_k_out       device bf16 [n_rows][n_kv_heads][128], k_stride, k_out_stride
+ *                      either tensor may be absent (NULL, 0 heads)
+ *   inverse            0: rotate by the rows' angles a (as h3_mmrope_qk, same
+ *                      values); 1: rotate by -a.  A rotation's transpose is its
+ *                      inverse, so this maps the gradients of the rotated Q and
+ *                      K to those of the unrotated ones.
+ * Arithmetic, other arguments and errors as h3_mmrope_qk.
+ */
+h3_status h3_mmrope_rotate(const void* d_q, const void* d_k, void* d_q_out, void* d_k_out, const float* d_coords,
+                           int64_t n_rows, int32_t n_heads, int32_t n_kv_heads, int64_t q_stride, int64_t k_stride,
+                           int64_t q_out_stride, int64_t k_out_stride, const h3_rope_cfg* cfg, int32_t inverse,
+                           void* stream);
+
+/* Masks of h3_build_key_ranges. */
+enum { H3_MASK_DOCUMENT = 0, H3_MASK_PREFIX_CAUSAL = 1, H3_MASK_PREFIX_BLOCK = 2 };
+
+/*
+ * h3_build_key_ranges -- documents packed into one sequence -> the interval of
+ * keys that each row attends to.
+ *
+ *   d_doc_starts   device int32[n_docs + 1], ascending inside [0, n_rows]: document
+ *                  d holds the rows [starts[d], starts[d + 1]) and may be empty
+ *   d_prefix       device int32[n_docs], rows of each document's prefix (at most
+ *                  its length counts), or NULL for none; ignored by
+ *                  H3_MASK_DOCUMENT
+ *   mode           H3_MASK_DOCUMENT: every row of a document attends to all of it.
+ *                  H3_MASK_PREFIX_CAUSAL: to the prefix and to rows up to itself.
+ *                  H3_MASK_PREFIX_BLOCK: prefix rows to the prefix, the others to
+ *                  the whole document (the K and V of reference rows put first
+ *                  then hold for every sample that shares them).
+ *   d_ranges       device int32[n_rows][2], 8-byte aligned, written: [lo, hi); rows
+ *                  in no document get (0, 0)
+ * A table that does not ascend inside [0, n_rows], or a negative prefix, raises
+ * H3_ERR_DEVICE_INPUT; the intervals stay inside [0, n_rows].
+ * Errors: H3_ERR_INVALID_ARG (sizes, mode, NULL pointers); H3_ERR_UNSUPPORTED
+ * (misaligned d_ranges).
+ */
+h3_status h3_build_key_ranges(const int32_t* d_doc_starts, const int32_t* d_prefix, int32_t n_docs, int64_t n_rows,
+                              int32_t mode, int32_t* d_ranges, void* stream);
+
+/* A masked attention problem: n_q query rows and n_k key rows per batch entry,
+ * n_heads query heads sharing n_kv_heads (a divisor of n_heads) K/V heads: head h
+ * reads K/V head h / (n_heads / n_kv_heads). */
+typedef struct {
+  int64_t n_q;
+  int64_t n_k;
+  int32_t batch;
+  int32_t n_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;      /* must be 128 */
+  float softmax_scale;   /* > 0, or <= 0 for 1/sqrt(head_dim) */
+} h3_attn_shape;
+
+/*
+ * h3_masked_attention -- softmax attention in which query row i attends to the
+ * keys [lo_i, hi_i) only:  O_i = sum_j P_ij V_j over those j,
+ * P_ij = exp(scale q_i.k_j - lse_i).
+ *
+ *   d_q, d_o       device bf16 [batch][n_q][n_heads][128], row strides q_stride,
+ *                  o_stride, batch strides n_q times those
+ *   d_k, d_v       device bf16 [batch][n_k][n_kv_heads][128], k_stride, v_stride
+ *   d_lse          device float[batch][n_heads][n_q], or NULL
+ *   d_ranges       device int32[batch][n_q][2], 8-byte aligned: the intervals, from
+ *                  h3_build_key_ranges or any others (cut to [0, n_k); lo >= hi is
+ *                  empty).  n_q may differ from n_k: fresh rows against reused keys.
+ * A row with an empty interval gets O = 0 and lse = -inf.  What lies outside a
+ * row's interval does not change it, inf and NaN included.  A row that attends to
+ * a key whose V holds inf or NaN becomes non-finite (at least in the columns
+ * concerned, in a tile at an interval's edge in all of them).
+ * Arithmetic and bounded waits as h3_packed_attention.
+ * Errors: H3_ERR_INVALID_ARG (sizes, heads, strides, NULL pointers);
+ * H3_ERR_UNSUPPORTED (head_dim != 128, misaligned pointer or stride).
+ */
+h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v, void* d_o, float* d_lse,
+                              const int32_t* d_ranges, const h3_attn_shape* shape, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int64_t o_stride, void* stream);
+
+/*
+ * h3_layernorm -- y = xhat * weight + bias, xhat = (x - mean(x)) * rstd,
+ * rstd = 1 / sqrt(var(x) + eps) (biased variance), per row.
+ *
+ *   d_x, d_y           device [n_rows][hidden] of `dtype`, row strides in elements;
+ *                      any hidden from 1 to 16384, stride and alignment (rows that
+ *                      are 16-byte aligned and a multiple of 8 long go in 16-byte
+ *                      pieces); d_y may be d_x
+ *   d_weight, d_bias   device [hidden] of `param_dtype` (dtype or H3_DTYPE_F32);
+ *                      NULL = ones, zeros
+ *   d_mean, d_rstd     device float[n_rows], the rows' statistics for
+ *                      h3_layernorm_backward, or NULL
+ * Arithmetic: fp32, y rounded once.
+ * Errors: H3_ERR_INVALID_ARG (sizes, strides, dtypes, NULL d_x or d_y, eps < 0);
+ * H3_ERR_UNSUPPORTED (hidden > 16384, another param_dtype).
+ */
+h3_status h3_layernorm(const void* d_x, void* d_y, const void* d_weight, const void* d_bias, float* d_mean,
+                       float* d_rstd, int64_t n_rows, int32_t hidden, int64_t x_row_stride, int64_t y_row_stride,
+                       int32_t dtype, int32_t param_dtype, float eps, void* stream);
+
+/*
+ * h3_layernorm_backward -- gradients of h3_layernorm.  With g = dy * weight:
+ *   dx = rstd * (g - mean(g) - xhat * mean(g * xhat)),
+ *   dweight = sum over rows of dy * xhat, dbias = sum over rows of dy.
+ *
+ *   d_dy, d_x, d_dx    device [n_rows][hidden] of `dtype`, own row strides; d_dx
+ *                      may be d_dy or d_x
+ *   d_mean, d_rstd     device float[n_rows] from h3_layernorm
+ *   d_weight           as h3_layernorm (NULL = ones)
+ *   d_dweight, d_dbias device [hidden] of `param_dtype`, overwritten; either may be
+ *                      NULL; zeros when n_rows is 0
+ *   d_work             h3_layernorm_backward_workspace_bytes() bytes, 256-byte
+ *                      aligned, contents undefined before and after; calls that may
+ *                      overlap in time need their own (NULL when neither parameter
+ *                      gradient is wanted)
+ * Column sums are fp32, added in an order that depends on the sizes alone.
+ * Errors: as h3_layernorm; H3_ERR_INVALID_ARG for a missing workspace.
+ */
+uint64_t h3_layernorm_backward_workspace_bytes(int64_t n_rows, int32_t hidden);
+h3_status h3_layernorm_backward(const void* d_dy, const void* d_x, const float* d_mean, const float* d_rstd,
+                                const void* d_weight, void* d_dx, void* d_dweight, void* d_dbias, void* d_work,
+                                int64_t n_rows, int32_t hidden, int64_t dy_row_stride, int64_t x_row_stride,
+                                int64_t dx_row_stride, int32_t dtype, int32_t param_dtype, void* stream);
+
+/*
+ * h3_adaln_modulate_backward -- gradients of h3_adaln_modulate:  dx of the
+ * rows, and of the table's entries
+ *   dshift[e] = sum over the rows of entry e of dy,
+ *   dscale[e] = sum over the rows of entry e of dy * LayerNorm(x).
+ *
+ *   d_dy, d_x, d_dx    device bf16 [n_rows][hidden], own row strides; d_dx may be
+ *                      d_dy or d_x
+ *   d_dtable           device float[n_entries][2][hidden], overwritten in full:
+ *                      [e][0] = dshift, [e][1] = dscale; zeros for an entry without
+ *                      rows
+ *   d_work             h3_adaln_backward_workspace_bytes() bytes, 256-byte aligned,
+ *                      contents undefined before and after; calls that may overlap
+ *                      in time need their own
+ *   others             as h3_adaln_modulate, with the same eps; the rows' statistics
+ *                      are computed again from x
+ * A row whose e falls outside [0, n_entries) gets a dx of NaN, adds to no entry and
+ * raises H3_ERR_DEVICE_INPUT.  Sums are fp32, in an order that depends on the sizes
+ * and indices alone.
+ * Errors: as h3_adaln_modulate; H3_ERR_INVALID_ARG for a missing workspace or
+ * n_rows >= 2^31; H3_ERR_UNSUPPORTED for n_entries > 8192.
+ */
+uint64_t h3_adaln_backward_workspace_bytes(int64_t n_rows, int32_t hidden, int32_t n_entries);
+h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const int32_t* d_timestep_index,
+                                     const int32_t* d_token_tag, const float* d_table, void* d_dx, float* d_dtable,
+                                     void* d_work, int32_t n_entries, int64_t n_rows, int32_t hidden,
+                                     int64_t dy_row_stride, int64_t x_row_stride, int64_t dx_row_stride, float eps,
+                                     void* stream);
+
 /*
  * Device workspace, in bytes, that h3_packed_mmrope_attention_host needs for
  * n_rows x n_heads (Q, K, V, O copies, coordinates and the permutation,

@@ -8,6 +8,9 @@ step of the path runs in the library's CUDA kernels:
 * ``h3_mmrope_qk``        three-axis rotary rotation of bf16 Q and K
 * ``h3_rope_cos_sin``     the per-row rotary (cos, sin) table of the fused Q rotation
 * ``h3_packed_attention`` full softmax attention over the packed rows
+* ``h3_masked_attention`` the same under one key interval per row (documents, prefixes), grouped heads
+* ``h3_mmrope_rotate``, ``h3_layernorm``, ``h3_adaln_modulate_backward`` and the other backward calls:
+  the training direction of the block
 
 The library is loaded on first use (``load()``, or any call below) and a
 missing or stale ``libh3.so`` raises there; there is no CPU or eager-PyTorch
@@ -22,7 +25,10 @@ from ._lib import (H3Error, H3_OK, H3_ERR_INVALID_ARG, H3_ERR_UNSUPPORTED, H3_ER
                    h3_build_coords, h3_check_device_error, h3_init, h3_shutdown,
                    h3_host_workspace_bytes, h3_mmrope_qk, h3_packed_attention, h3_packed_mmrope_attention_host,
                    h3_rope_cos_sin,
-                   h3_set_wait_limit_ns, rope_cfg, status_str)
+                   h3_set_wait_limit_ns, rope_cfg, status_str,
+                   h3_adaln_backward_workspace_bytes, h3_adaln_modulate_backward, h3_attn_shape,
+                   h3_build_key_ranges, h3_layernorm, h3_layernorm_backward, h3_layernorm_backward_workspace_bytes,
+                   h3_masked_attention, h3_mmrope_rotate)
 
 load = _lib.load
 
@@ -252,3 +258,264 @@ def adaln_modulate(x, timestep_index, token_tag, table, out=None, eps: float = 1
     h3_adaln_modulate(x.data_ptr(), out.data_ptr(), timestep_index.data_ptr(), token_tag.data_ptr(),
                       table.data_ptr(), table.shape[0], n, c, x.stride(0), out.stride(0), eps, _stream(stream))
     return out
+
+
+# ------------------------------------------------ masks, grouped heads, training --
+
+MASK_MODES = {"document": _lib.H3_MASK_DOCUMENT, "prefix_causal": _lib.H3_MASK_PREFIX_CAUSAL,
+              "prefix_block": _lib.H3_MASK_PREFIX_BLOCK}
+
+
+def _allocate_on(stream):
+    """Context in which tensors are allocated for use on ``stream`` (None: the current one)."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def mmrope_rotate(q, k, coords, q_out=None, k_out=None, inverse: bool = False, theta=10000.0,
+                  sections=(32, 48, 48), pair_layout=0, freq_rule=0, stream=None):
+    """Rotate Q [.., N, H, 128] and K [.., N, Hkv, 128]; returns (q_out, k_out).
+
+    The head counts may differ, each tensor has its own row stride, and either
+    may be None.  ``inverse`` rotates back: it maps the gradients of the rotated
+    Q and K to those of the unrotated ones.  Pass q_out=q, k_out=k for in place.
+    """
+    import torch
+    rows = None
+    ptr, heads, stride, out_stride, outs = [0, 0], [0, 0], [0, 0], [0, 0], [None, None]
+    for i, (x, out) in enumerate(((q, q_out), (k, k_out))):
+        if x is None:
+            if out is not None:
+                raise ValueError("an output without its input")
+            continue
+        b, n, heads[i], stride[i] = _row_layout(x)
+        if rows is not None and rows != (b, n):
+            raise ValueError("q and k differ in their rows")
+        rows = (b, n)
+        if out is None:
+            with _allocate_on(stream):
+                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        ob, on, oh, out_stride[i] = _row_layout(out)
+        if (ob, on, oh) != (b, n, heads[i]):
+            raise ValueError("outputs must have the inputs' shape")
+        ptr[i], outs[i] = x.data_ptr(), out
+    if rows is None:
+        raise ValueError("neither q nor k given")
+    n = rows[0] * rows[1]
+    if coords.dtype != torch.float32 or coords.numel() != 3 * n or not coords.is_contiguous():
+        raise ValueError("coords must be contiguous fp32 [rows, 3]")
+    _on_device(coords, "coords")
+    h3_mmrope_rotate(ptr[0], ptr[1], outs[0].data_ptr() if outs[0] is not None else 0,
+                     outs[1].data_ptr() if outs[1] is not None else 0, coords.data_ptr(), n, heads[0], heads[1],
+                     stride[0], stride[1], out_stride[0], out_stride[1],
+                     rope_cfg(theta, 128, sections, pair_layout, freq_rule), inverse, _stream(stream))
+    return outs[0], outs[1]
+
+
+def build_key_ranges(doc_starts, n_rows: int, mode: str = "document", prefix=None, out=None, stream=None):
+    """int32 [n_rows, 2]: the keys [lo, hi) that each row of documents packed into one sequence attends to.
+
+    doc_starts: CUDA int32 [D + 1], document d = rows doc_starts[d] .. doc_starts[d + 1] - 1 (may be
+    empty); prefix: CUDA int32 [D], rows of each document's prefix.  mode: "document" (all of the
+    document), "prefix_causal" (the prefix, then rows up to itself) or "prefix_block" (prefix rows
+    attend to the prefix, the others to the whole document).  Rows in no document get (0, 0).
+    """
+    import torch
+    if mode not in MASK_MODES:
+        raise ValueError(f"mode must be one of {sorted(MASK_MODES)}")
+    if doc_starts.dtype != torch.int32 or doc_starts.dim() != 1 or doc_starts.numel() < 1 \
+            or not doc_starts.is_contiguous():
+        raise ValueError("doc_starts must be a contiguous int32 [documents + 1] tensor")
+    _on_device(doc_starts, "doc_starts")
+    n_docs = doc_starts.numel() - 1
+    if prefix is not None:
+        _exact(prefix, torch.int32, (n_docs,), "prefix")
+        _on_device(prefix, "prefix")
+    if out is None:
+        with _allocate_on(stream):
+            out = torch.empty((n_rows, 2), dtype=torch.int32, device=doc_starts.device)
+    _exact(out, torch.int32, (n_rows, 2), "out")
+    _on_device(out, "out")
+    h3_build_key_ranges(doc_starts.data_ptr(), prefix.data_ptr() if prefix is not None else 0, n_docs, n_rows,
+                        MASK_MODES[mode], out.data_ptr(), _stream(stream))
+    return out
+
+
+def _masked_shape(q, k, v, key_ranges, softmax_scale):
+    """(shape struct, strides of q, k, v) of a masked attention problem, its tensors checked."""
+    import torch
+    b, n, h, qs = _row_layout(q)
+    kb, nk, hk, ks = _row_layout(k)
+    vb, nv, hv, vs = _row_layout(v)
+    if (vb, nv, hv) != (kb, nk, hk) or kb != b:
+        raise ValueError("k and v must have one shape and q's batch")
+    if h < 1 or hk < 1 or h % hk:
+        raise ValueError("the query heads must be a multiple of the K/V heads")
+    if key_ranges.dtype != torch.int32 or key_ranges.numel() != 2 * b * n or not key_ranges.is_contiguous() \
+            or key_ranges.shape[-1] != 2:
+        raise ValueError("key_ranges must be contiguous int32 [rows, 2]")
+    _on_device(key_ranges, "key_ranges")
+    return h3_attn_shape(n, nk, b, h, hk, 128, softmax_scale), qs, ks, vs
+
+
+def masked_attention(q, k, v, key_ranges, out=None, lse=None, softmax_scale: float = 0.0, stream=None):
+    """O = softmax(Q K^T * scale) V where row i attends to the keys key_ranges[i] = [lo, hi) only.
+
+    q: [Nq, H, 128] or [B, Nq, H, 128]; k, v: [.., Nk, Hkv, 128], H a multiple of Hkv (head h reads
+    K/V head h // (H / Hkv)); key_ranges: int32 [.., Nq, 2] from ``build_key_ranges`` or any other
+    intervals.  Rows that attend to nothing give O = 0 and lse = -inf.  lse: fp32 [B, H, Nq], written
+    if given (``masked_attention_backward`` needs it).
+    """
+    import torch
+    shape, qs, ks, vs = _masked_shape(q, k, v, key_ranges, softmax_scale)
+    if out is None:
+        with _allocate_on(stream):
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    b, n, h, os_ = _row_layout(out)
+    if (b, n, h) != (shape.batch, shape.n_q, shape.n_heads):
+        raise ValueError("output must have q's shape")
+    lp = 0
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.numel() != b * h * n or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous fp32 [B, H, Nq]")
+        _on_device(lse, "lse")
+        lp = lse.data_ptr()
+    h3_masked_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, key_ranges.data_ptr(), shape,
+                        qs, ks, vs, os_, _stream(stream))
+    return out
+
+
+def _dtype_code(t, what: str) -> int:
+    import torch
+    codes = {torch.bfloat16: _lib.H3_DTYPE_BF16, torch.float16: _lib.H3_DTYPE_F16, torch.float32: _lib.H3_DTYPE_F32}
+    if t.dtype not in codes:
+        raise ValueError(f"{what} must be bf16, fp16 or fp32")
+    return codes[t.dtype]
+
+
+def _norm_rows(t, n: int, c: int, dtype, what: str) -> int:
+    """Row stride of an [n, c] tensor with unit inner stride."""
+    if t.dtype != dtype or tuple(t.shape) != (n, c) or (c > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < c):
+        raise ValueError(f"{what} must be a {dtype} [{n}, {c}] tensor with unit inner stride")
+    _on_device(t, what)
+    return t.stride(0) if n > 1 else max(c, t.stride(0))
+
+
+def _workspace(workspace, need: int, device, stream):
+    import torch
+    if workspace is None:
+        with _allocate_on(stream):
+            return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes")
+    _on_device(workspace, "workspace")
+    return workspace
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None, stream=None):
+    """(y, mean, rstd): y = (x - mean) * rstd * weight + bias per row of x [N, C].
+
+    x, y: bf16, fp16 or fp32; weight, bias: [C] of x's type or fp32 (both alike), or None; mean, rstd:
+    fp32 [N], the input of ``layer_norm_backward``.  Pass out=x for in place.
+    """
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [N, C]")
+    n, c = x.shape
+    dt = _dtype_code(x, "x")
+    xs = _norm_rows(x, n, c, x.dtype, "x")
+    pdt = dt
+    for t, what in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            pdt = _dtype_code(t, what)
+            _exact(t, (weight if weight is not None else bias).dtype, (c,), what)
+            _on_device(t, what)
+    with _allocate_on(stream):
+        out = torch.empty((n, c), dtype=x.dtype, device=x.device) if out is None else out
+        mean = torch.empty(n, dtype=torch.float32, device=x.device) if mean is None else mean
+        rstd = torch.empty(n, dtype=torch.float32, device=x.device) if rstd is None else rstd
+    ys = _norm_rows(out, n, c, x.dtype, "out")
+    for t, what in ((mean, "mean"), (rstd, "rstd")):
+        _exact(t, torch.float32, (n,), what)
+        _on_device(t, what)
+    h3_layernorm(x.data_ptr(), out.data_ptr(), weight.data_ptr() if weight is not None else 0,
+                 bias.data_ptr() if bias is not None else 0, mean.data_ptr(), rstd.data_ptr(), n, c, xs, ys, dt, pdt,
+                 eps, _stream(stream))
+    return out, mean, rstd
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, param_dtype=None, dx=None, workspace=None,
+                        param_grads: bool = True, stream=None):
+    """(dx, dweight, dbias) of ``layer_norm``; dweight and dbias are None without ``param_grads``.
+
+    The parameter gradients have the weight's type (``param_dtype``, or fp32, without a weight).
+    """
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [N, C]")
+    n, c = x.shape
+    dt = _dtype_code(x, "x")
+    xs, dys = _norm_rows(x, n, c, x.dtype, "x"), _norm_rows(dy, n, c, x.dtype, "dy")
+    for t, what in ((mean, "mean"), (rstd, "rstd")):
+        _exact(t, torch.float32, (n,), what)
+        _on_device(t, what)
+    if weight is not None:
+        _exact(weight, weight.dtype, (c,), "weight")
+        _on_device(weight, "weight")
+        param_dtype = weight.dtype
+    else:
+        param_dtype = param_dtype or torch.float32
+    dw = db = None
+    with _allocate_on(stream):
+        dx = torch.empty((n, c), dtype=x.dtype, device=x.device) if dx is None else dx
+        if param_grads:
+            dw = torch.empty(c, dtype=param_dtype, device=x.device)
+            db = torch.empty(c, dtype=param_dtype, device=x.device)
+            pdt = _dtype_code(dw, "weight")
+            workspace = _workspace(workspace, h3_layernorm_backward_workspace_bytes(n, c), x.device, stream)
+        else:
+            pdt = _dtype_code(weight, "weight") if weight is not None else dt
+    dxs = _norm_rows(dx, n, c, x.dtype, "dx")
+    h3_layernorm_backward(dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                          weight.data_ptr() if weight is not None else 0, dx.data_ptr(),
+                          dw.data_ptr() if param_grads else 0, db.data_ptr() if param_grads else 0,
+                          workspace.data_ptr() if param_grads else 0, n, c, dys, xs, dxs, dt, pdt, _stream(stream))
+    return dx, dw, db
+
+
+def adaln_modulate_backward(dy, x, timestep_index, token_tag, table, eps: float = 1e-6, dx=None, dtable=None,
+                            workspace=None, stream=None):
+    """(dx, dtable) of ``adaln_modulate``: dx bf16 [N, C], dtable fp32 [E, 2, C] (dshift, dscale).
+
+    Takes what the forward call took, with the same eps; the rows' statistics are
+    computed again from x.  Pass dx=dy (or x) for in place.
+    """
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [N, C]")
+    n, c = x.shape
+    xs, dys = _norm_rows(x, n, c, torch.bfloat16, "x"), _norm_rows(dy, n, c, torch.bfloat16, "dy")
+    for t in (timestep_index, token_tag):
+        if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+            raise ValueError("indices must be contiguous CUDA int32 [N]")
+        _on_device(t, "indices")
+    if table.dim() != 3:
+        raise ValueError("table must be [E, 2, C]")
+    e = table.shape[0]
+    _exact(table, torch.float32, (e, 2, c), "table")
+    _on_device(table, "table")
+    need = h3_adaln_backward_workspace_bytes(n, c, e)
+    if need == 0:
+        raise ValueError("hidden must be a multiple of 8 up to 8192, with 1 to 8192 table entries")
+    with _allocate_on(stream):
+        dx = torch.empty((n, c), dtype=x.dtype, device=x.device) if dx is None else dx
+        dtable = torch.empty((e, 2, c), dtype=torch.float32, device=x.device) if dtable is None else dtable
+    _exact(dtable, torch.float32, (e, 2, c), "dtable")
+    _on_device(dtable, "dtable")
+    workspace = _workspace(workspace, need, x.device, stream)
+    dxs = _norm_rows(dx, n, c, torch.bfloat16, "dx")
+    h3_adaln_modulate_backward(dy.data_ptr(), x.data_ptr(), timestep_index.data_ptr(), token_tag.data_ptr(),
+                               table.data_ptr(), dx.data_ptr(), dtable.data_ptr(), workspace.data_ptr(), e, n, c,
+                               dys, xs, dxs, eps, _stream(stream))
+    return dx, dtable

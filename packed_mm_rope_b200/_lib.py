@@ -22,7 +22,12 @@ H3_MAX_SEGMENTS = 64
 EXPORTED = ("h3_status_str", "h3_version", "h3_build_coords", "h3_mmrope_qk", "h3_rope_cos_sin",
             "h3_packed_attention", "h3_check_device_error", "h3_set_wait_limit_ns",
             "h3_host_workspace_bytes", "h3_packed_mmrope_attention_host",
-            "h3_packed_mmrope_attention_host_noalloc", "h3_adaln_modulate", "h3_init", "h3_shutdown")
+            "h3_packed_mmrope_attention_host_noalloc", "h3_adaln_modulate", "h3_init", "h3_shutdown",
+            "h3_mmrope_rotate", "h3_build_key_ranges", "h3_masked_attention",
+            "h3_layernorm", "h3_layernorm_backward_workspace_bytes", "h3_layernorm_backward",
+            "h3_adaln_backward_workspace_bytes", "h3_adaln_modulate_backward")
+H3_DTYPE_BF16, H3_DTYPE_F16, H3_DTYPE_F32 = 0, 1, 2
+H3_MASK_DOCUMENT, H3_MASK_PREFIX_CAUSAL, H3_MASK_PREFIX_BLOCK = 0, 1, 2
 
 
 class h3_segment(ctypes.Structure):
@@ -34,6 +39,12 @@ class h3_rope_cfg(ctypes.Structure):
     _fields_ = [("theta", ctypes.c_double), ("head_dim", ctypes.c_int32), ("sec_t", ctypes.c_int32),
                 ("sec_h", ctypes.c_int32), ("sec_w", ctypes.c_int32), ("pair_layout", ctypes.c_int32),
                 ("freq_rule", ctypes.c_int32)]
+
+
+class h3_attn_shape(ctypes.Structure):
+    _fields_ = [("n_q", ctypes.c_int64), ("n_k", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float)]
 
 
 class H3Error(RuntimeError):
@@ -86,6 +97,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.h3_shutdown.argtypes = []
     lib.h3_adaln_modulate.restype = I32
     lib.h3_adaln_modulate.argtypes = [P, P, P, P, P, I32, I64, I32, I64, I64, F32, P]
+    lib.h3_mmrope_rotate.restype = I32
+    lib.h3_mmrope_rotate.argtypes = [P, P, P, P, P, I64, I32, I32, I64, I64, I64, I64, ctypes.POINTER(h3_rope_cfg),
+                                     I32, P]
+    lib.h3_build_key_ranges.restype = I32
+    lib.h3_build_key_ranges.argtypes = [P, P, I32, I64, I32, P, P]
+    lib.h3_masked_attention.restype = I32
+    lib.h3_masked_attention.argtypes = [P, P, P, P, P, P, ctypes.POINTER(h3_attn_shape), I64, I64, I64, I64, P]
+    lib.h3_layernorm.restype = I32
+    lib.h3_layernorm.argtypes = [P, P, P, P, P, P, I64, I32, I64, I64, I32, I32, F32, P]
+    lib.h3_layernorm_backward_workspace_bytes.restype = U64
+    lib.h3_layernorm_backward_workspace_bytes.argtypes = [I64, I32]
+    lib.h3_layernorm_backward.restype = I32
+    lib.h3_layernorm_backward.argtypes = [P, P, P, P, P, P, P, P, P, I64, I32, I64, I64, I64, I32, I32, P]
+    lib.h3_adaln_backward_workspace_bytes.restype = U64
+    lib.h3_adaln_backward_workspace_bytes.argtypes = [I64, I32, I32]
+    lib.h3_adaln_modulate_backward.restype = I32
+    lib.h3_adaln_modulate_backward.argtypes = [P, P, P, P, P, P, P, P, I32, I64, I32, I64, I64, I64, F32, P]
     _lib = lib
     return lib
 
@@ -169,6 +197,61 @@ def h3_adaln_modulate(d_x: int, d_y: int, d_ts: int, d_tags: int, d_table: int, 
     _check(load().h3_adaln_modulate(d_x or None, d_y or None, d_ts or None, d_tags or None, d_table or None,
                                     n_entries, n_rows, hidden, x_row_stride, y_row_stride, eps, stream or None),
            "h3_adaln_modulate")
+
+
+def h3_mmrope_rotate(d_q: int, d_k: int, d_q_out: int, d_k_out: int, d_coords: int, n_rows: int, n_heads: int,
+                     n_kv_heads: int, q_stride: int, k_stride: int, q_out_stride: int, k_out_stride: int,
+                     cfg: h3_rope_cfg, inverse: bool = False, stream: int = 0) -> None:
+    _check(load().h3_mmrope_rotate(d_q or None, d_k or None, d_q_out or None, d_k_out or None, d_coords or None,
+                                   n_rows, n_heads, n_kv_heads, q_stride, k_stride, q_out_stride, k_out_stride,
+                                   ctypes.byref(cfg), int(inverse), stream or None), "h3_mmrope_rotate")
+
+
+def h3_build_key_ranges(d_doc_starts: int, d_prefix: int, n_docs: int, n_rows: int, mode: int, d_ranges: int,
+                        stream: int = 0) -> None:
+    _check(load().h3_build_key_ranges(d_doc_starts or None, d_prefix or None, n_docs, n_rows, mode, d_ranges or None,
+                                      stream or None), "h3_build_key_ranges")
+
+
+def h3_masked_attention(d_q: int, d_k: int, d_v: int, d_o: int, d_lse: int, d_ranges: int, shape: h3_attn_shape,
+                        q_stride: int, k_stride: int, v_stride: int, o_stride: int, stream: int = 0) -> None:
+    _check(load().h3_masked_attention(d_q or None, d_k or None, d_v or None, d_o or None, d_lse or None,
+                                      d_ranges or None, ctypes.byref(shape), q_stride, k_stride, v_stride, o_stride,
+                                      stream or None), "h3_masked_attention")
+
+
+def h3_layernorm(d_x: int, d_y: int, d_weight: int, d_bias: int, d_mean: int, d_rstd: int, n_rows: int, hidden: int,
+                 x_row_stride: int, y_row_stride: int, dtype: int = 0, param_dtype: int = 2, eps: float = 1e-5,
+                 stream: int = 0) -> None:
+    _check(load().h3_layernorm(d_x or None, d_y or None, d_weight or None, d_bias or None, d_mean or None,
+                               d_rstd or None, n_rows, hidden, x_row_stride, y_row_stride, dtype, param_dtype, eps,
+                               stream or None), "h3_layernorm")
+
+
+def h3_layernorm_backward_workspace_bytes(n_rows: int, hidden: int) -> int:
+    return int(load().h3_layernorm_backward_workspace_bytes(n_rows, hidden))
+
+
+def h3_layernorm_backward(d_dy: int, d_x: int, d_mean: int, d_rstd: int, d_weight: int, d_dx: int, d_dweight: int,
+                          d_dbias: int, d_work: int, n_rows: int, hidden: int, dy_row_stride: int, x_row_stride: int,
+                          dx_row_stride: int, dtype: int = 0, param_dtype: int = 2, stream: int = 0) -> None:
+    _check(load().h3_layernorm_backward(d_dy or None, d_x or None, d_mean or None, d_rstd or None, d_weight or None,
+                                        d_dx or None, d_dweight or None, d_dbias or None, d_work or None, n_rows,
+                                        hidden, dy_row_stride, x_row_stride, dx_row_stride, dtype, param_dtype,
+                                        stream or None), "h3_layernorm_backward")
+
+
+def h3_adaln_backward_workspace_bytes(n_rows: int, hidden: int, n_entries: int) -> int:
+    return int(load().h3_adaln_backward_workspace_bytes(n_rows, hidden, n_entries))
+
+
+def h3_adaln_modulate_backward(d_dy: int, d_x: int, d_ts: int, d_tags: int, d_table: int, d_dx: int, d_dtable: int,
+                               d_work: int, n_entries: int, n_rows: int, hidden: int, dy_row_stride: int,
+                               x_row_stride: int, dx_row_stride: int, eps: float = 1e-6, stream: int = 0) -> None:
+    _check(load().h3_adaln_modulate_backward(d_dy or None, d_x or None, d_ts or None, d_tags or None, d_table or None,
+                                             d_dx or None, d_dtable or None, d_work or None, n_entries, n_rows,
+                                             hidden, dy_row_stride, x_row_stride, dx_row_stride, eps,
+                                             stream or None), "h3_adaln_modulate_backward")
 
 
 def h3_check_device_error(stream: int = 0) -> int:

@@ -55,6 +55,18 @@
 // Every mbarrier wait is bounded (global-time limit); a thread that gives up
 // raises an abort flag that all other waits observe, the producer and the
 // issuer drain what they already started, and TMEM is freed before exit.
+//
+// MASKED: query row i attends to the keys [lo_i, hi_i) of `ranges` only (keys
+// and queries may differ in number, and groups of query heads may share a K/V
+// head).  The CTA visits the key tiles of the hull of its rows' intervals.  A
+// tile inside every row's interval runs as above; in the others logits outside
+// a row's interval become -inf, so their P is 0.  A 0 does not hide a V row
+// that holds inf or NaN (0 x inf = NaN on the tensor core), so in those tiles
+// the softmax warps first set the non-finite elements of V to 0 in shared
+// memory, and rows that do attend to such a key get a NaN logit there: masked
+// places cannot change a row, and what a row attends to is never hidden.  A row
+// takes its reference m from its first 64-key half with a visible key; a row
+// without one ends with l = 0, O = 0 and a log-sum-exp of -inf.
 #pragma once
 
 #include "common.cuh"
@@ -80,9 +92,11 @@ constexpr uint32_t SMEM_BAR = SMEM_KV + KV_STAGES * TILE_BYTES;
 // barriers: q_full[2], kv_full[S], kv_empty[S], s_full[2], p_full[2][2] (halves),
 //           pva_done[2] (first half of PV landed), o_full[2], mma_done,
 //           q_ready[2] (Q tile rotated in place, fused RoPE only)
-constexpr int NUM_BARS = 2 + 2 * KV_STAGES + 2 + 4 + 2 + 2 + 1 + 2;
-constexpr uint32_t SMEM_MISC = SMEM_BAR + NUM_BARS * 8;   // tmem base, abort flag
-constexpr uint32_t SMEM_BYTES = SMEM_MISC + 16 + 1024;    // + alignment slack
+//           v_clean (masked: the V tile holds no inf or NaN any more)
+constexpr int NUM_BARS = 2 + 2 * KV_STAGES + 2 + 4 + 2 + 2 + 1 + 2 + 1;
+constexpr uint32_t SMEM_MISC = SMEM_BAR + NUM_BARS * 8;   // tmem base, abort flag, hull; two 16-byte key sets
+constexpr uint32_t SMEM_BYTES = SMEM_MISC + 32 + 32 + 1024;   // + alignment slack
+static_assert(SMEM_MISC % 16 == 0, "the key sets are read 16 bytes at a time");
 
 constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, BN, false, false);   // Q, K both K-major
 constexpr uint32_t IDESC_O = idesc_bf16_f32(BM, HD, false, true);    // P from TMEM, V MN-major
@@ -120,8 +134,45 @@ struct Params {
   // fused RoPE on Q (rope_cs == null: Q arrives rotated)
   const float2* rope_cs;          // [B][N][64] (cos, sin) per rotary pair
   int rope_layout;                // 0 adjacent pairs, 1 half-split
+  // MASKED only
+  const int2* ranges;             // [B][n_rows] key interval [lo, hi) of each query row
+  int n_keys;
+  int group;                      // query heads per K/V head
 };
 
+// Keys of the row's interval that exist: an empty interval is (0, 0).
+__device__ __forceinline__ int2 clamp_range(int2 r, int n_keys) {
+  r.x = max(r.x, 0);
+  r.y = min(r.y, n_keys);
+  return r.x < r.y ? r : make_int2(0, 0);
+}
+
+// Sets the inf and NaN elements of rows 8 part .. 8 part + 7 of a swizzled
+// 128 x 128 bf16 tile (two halves of 64 columns) to 0 and returns those rows'
+// bits (one warp; the swizzle moves 16-byte pieces within their row only).
+__device__ __forceinline__ uint32_t clean_rows(uint8_t* tile, int part, int lane) {
+  uint32_t rows = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int piece = (i & 1) * 32 + lane;         // 64 pieces of 16 bytes: 8 rows of one half
+    uint4* p = reinterpret_cast<uint4*>(tile + (i >> 1) * HALF_BYTES + part * 1024 + piece * 16);
+    const uint4 u = *p;
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    bool found = false;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if ((w[m] & 0x7f80u) == 0x7f80u) w[m] &= 0xffff0000u, found = true;
+      if ((w[m] & 0x7f800000u) == 0x7f800000u) w[m] &= 0xffffu, found = true;
+    }
+    if (found) {
+      *p = make_uint4(w[0], w[1], w[2], w[3]);
+      rows |= 1u << (piece >> 3);
+    }
+  }
+  return __reduce_or_sync(0xffffffffu, rows);
+}
+
+template <bool MASKED>
 __global__ void __launch_bounds__(THREADS, 1)
 attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const Params p) {
@@ -140,7 +191,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   auto bar_o_full = [&](int i) { return bar0 + 8u * (10 + 2 * KV_STAGES + i); };
   const uint32_t bar_mma_done = bar0 + 8u * (12 + 2 * KV_STAGES);
   auto bar_q_ready = [&](int i) { return bar0 + 8u * (13 + 2 * KV_STAGES + i); };
-  const bool fused_rope = p.rope_cs != nullptr;
+  const uint32_t bar_v_clean = bar0 + 8u * (15 + 2 * KV_STAGES);
+  const bool fused_rope = !MASKED && p.rope_cs != nullptr;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC);
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 4);
 
@@ -148,8 +200,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const int lane = threadIdx.x & 31;
   const int head = blockIdx.y;
   const int batch = blockIdx.z;
-  const int q_row0 = blockIdx.x * (2 * BM);
-  const int nkv = p.n_kv_tiles;
+  // masked: the last rows first, since under a causal mask they see the most keys
+  const int q_row0 = (MASKED ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * (2 * BM);
   const uint64_t limit = p.wait_limit_ns;
   const int eslot = p.err_slot;
 
@@ -169,8 +221,60 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     mbar_init(bar_mma_done, 1);
     mbar_init(bar_q_ready(0), 8);
     mbar_init(bar_q_ready(1), 8);
+    if (MASKED) mbar_init(bar_v_clean, SOFTMAX_WARPS);
     *abort_flag = 0u;
     mbar_fence_init();
+  }
+  int nkv = p.n_kv_tiles;
+  int tile0 = 0;                     // first key tile of this CTA
+  int full_lo = 0, full_hi = 0;      // masked: keys [full_lo, full_hi) are seen by every row of the CTA
+  if constexpr (MASKED) {
+    // hull of the rows' intervals, and the keys that all of them see
+    int* const hull = reinterpret_cast<int*>(gbase + SMEM_MISC + 8);
+    if (threadIdx.x == 0) {
+      hull[0] = hull[2] = 0x7fffffff;
+      hull[1] = hull[3] = 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2 * BM) {
+      const int row = q_row0 + threadIdx.x;
+      int2 r = make_int2(0x7fffffff, 0);           // rows past the end: no say in the hull
+      int all_lo = 0, all_hi = 0x7fffffff;
+      if (row < p.n_rows) {
+        r = clamp_range(p.ranges[static_cast<long long>(batch) * p.n_rows + row], p.n_keys);
+        all_lo = r.x;
+        all_hi = r.y;
+        if (r.x >= r.y) r = make_int2(0x7fffffff, 0);
+      }
+      const int lo = __reduce_min_sync(0xffffffffu, r.x), hi = __reduce_max_sync(0xffffffffu, r.y);
+      all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+      all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+      if (lane == 0) {
+        atomicMin(&hull[0], lo);
+        atomicMax(&hull[1], hi);
+        atomicMin(&hull[2], all_hi);
+        atomicMax(&hull[3], all_lo);
+      }
+    }
+    __syncthreads();
+    full_hi = hull[2];
+    full_lo = hull[3];
+    nkv = 0;
+    if (hull[0] < hull[1]) {
+      tile0 = hull[0] / BN;
+      nkv = (hull[1] + BN - 1) / BN - tile0;
+    }
+    if (nkv == 0) {                                // no row attends to anything
+      for (int i = threadIdx.x; i < 2 * BM * (HD / 8); i += THREADS) {
+        const int row = q_row0 + i / (HD / 8);
+        if (row < p.n_rows)
+          *reinterpret_cast<uint4*>(p.o + batch * p.o_batch_stride + static_cast<long long>(row) * p.o_row_stride +
+                                    head * HD + 8 * (i % (HD / 8))) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (p.lse != nullptr && threadIdx.x < 2 * BM && q_row0 + threadIdx.x < p.n_rows)
+        p.lse[(static_cast<long long>(batch) * p.n_heads + head) * p.n_rows + q_row0 + threadIdx.x] = -INFINITY;
+      return;
+    }
   }
   if (warp == W_MMA) {
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
@@ -190,6 +294,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // ------------------------------------------------------------ TMA ----
     if (lane == 0) {
       const int col0 = head * HD;
+      const int kv_col0 = MASKED ? head / p.group * HD : col0;
       for (int i = 0; i < 2; ++i) {
         const uint32_t dst = base + SMEM_Q + i * TILE_BYTES;
         mbar_arrive_expect_tx(bar_q_full(i), TILE_BYTES);
@@ -202,11 +307,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int use = idx / KV_STAGES;
         if (use > 0 && !mbar_wait_bounded(bar_kv_empty(s), (use - 1) & 1, abort_flag, limit, eslot)) break;
         const CUtensorMap* tm = (idx & 1) ? &tm_v : &tm_k;
-        const int row = (idx >> 1) * BN;
+        const int row = (tile0 + (idx >> 1)) * BN;
         const uint32_t dst = base + SMEM_KV + s * TILE_BYTES;
         mbar_arrive_expect_tx(bar_kv_full(s), TILE_BYTES);
-        tma_load_3d(dst, tm, bar_kv_full(s), col0, row, batch);
-        tma_load_3d(dst + HALF_BYTES, tm, bar_kv_full(s), col0 + 64, row, batch);
+        tma_load_3d(dst, tm, bar_kv_full(s), kv_col0, row, batch);
+        tma_load_3d(dst + HALF_BYTES, tm, bar_kv_full(s), kv_col0 + 64, row, batch);
         issued = idx + 1;
       }
       // Drain: every load this thread started must land before the CTA exits.
@@ -326,6 +431,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int tail = p.n_rows - (nkv - 1) * BN;    // valid keys in the last tile (1..128)
     const int row_a = q_row0 + wg * BM + lane16 + t1;
     const int row_b = row_a + 8;
+    int2 rng_a = make_int2(0, 0), rng_b = make_int2(0, 0);   // masked: the rows' key intervals
+    if constexpr (MASKED) {
+      const int2* rg = p.ranges + static_cast<long long>(batch) * p.n_rows;
+      if (row_a < p.n_rows) rng_a = clamp_range(rg[row_a], p.n_keys);
+      if (row_b < p.n_rows) rng_b = clamp_range(rg[row_b], p.n_keys);
+    }
+    uint4* const unclean = reinterpret_cast<uint4*>(gbase + SMEM_MISC + 32);   // [2]: keys of V with inf or NaN
+    int cleaned = 0;                               // masked: tiles cleaned so far
     float m_a = -INFINITY, m_b = -INFINITY;        // log2 units, identical in a row's 4 threads
     float l_a = 0.f, l_b = 0.f;                    // this thread's share of the row sums
     bool ok = true;
@@ -342,11 +455,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       return x != 0;
     };
     // logits of 64 keys starting at key c0 of the tile (registers as loaded);
-    // keys past the end -> -inf
+    // keys past the end -> -inf; masked: keys outside the row's interval -> -inf
     auto to_logits = [&](const uint32_t (&r)[32], int c0, bool last, float (&x)[32]) {
 #pragma unroll
       for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r[e]);
-      if (last && tail < BN) {
+      if (!MASKED && last && tail < BN) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int key = c0 + 8 * (e >> 2) + 2 * t0 + (e & 1);
@@ -354,11 +467,36 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
       }
     };
+    auto mask_logits = [&](int key0, uint32_t bad_lo, uint32_t bad_hi, float (&x)[32]) {
+      const unsigned len_a = rng_a.y - rng_a.x, len_b = rng_b.y - rng_b.x;
+      const int off_a = key0 + 2 * t0 - rng_a.x, off_b = key0 + 2 * t0 - rng_b.x;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const int k = 8 * (e >> 2) + (e & 1);
+        const bool seen = ((e >> 1) & 1) ? static_cast<unsigned>(off_b + k) < len_b
+                                         : static_cast<unsigned>(off_a + k) < len_a;
+        if (!seen) x[e] = -INFINITY;
+      }
+      if ((bad_lo | bad_hi) != 0u) {               // a key of this half has inf or NaN in V
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int k = 8 * (e >> 2) + (e & 1);
+          const bool seen = ((e >> 1) & 1) ? static_cast<unsigned>(off_b + k) < len_b
+                                           : static_cast<unsigned>(off_a + k) < len_a;
+          const uint32_t bit = (k < 32 ? bad_lo : bad_hi) >> ((k & 31) + 2 * t0) & 1u;
+          if (bit && seen) x[e] = __int_as_float(0x7fc00000);
+        }
+      }
+    };
+    // whether row r sees a key of [key0, key0 + 64)
+    auto sees = [](int2 r, int key0) { return r.x < key0 + 64 && r.y > key0; };
     // numerators of the 16 keys of each row: bf16 pairs (register order of the
     // 16x128b store) and this thread's sums
     auto exps = [&](const float (&x)[32], uint32_t (&pk)[16], float& sa, float& sb) {
       const float2 c2 = make_float2(sl2, sl2);
-      const float2 ma = make_float2(-m_a, -m_a), mb = make_float2(-m_b, -m_b);
+      // masked: a row that has seen no key yet has no reference (its numerators are 0 or found again)
+      const float ra = MASKED && m_a == -INFINITY ? 0.f : -m_a, rb = MASKED && m_b == -INFINITY ? 0.f : -m_b;
+      const float2 ma = make_float2(ra, ra), mb = make_float2(rb, rb);
       float2 acc_a = make_float2(0.f, 0.f), acc_b = make_float2(0.f, 0.f);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
@@ -389,9 +527,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     };
     // the rare path: raise the reference of the rows whose shares need it
     // (all rows on the first half of the first tile); returns (fa, fb)
-    auto new_reference = [&](const float (&x)[32], bool first, float sa, float sb, float& fa, float& fb) {
-      const bool na = quad_or(first || !(sa <= PART_LIMIT));
-      const bool nb = quad_or(first || !(sb <= PART_LIMIT));
+    auto new_reference = [&](const float (&x)[32], bool first_a, bool first_b, float sa, float sb, float& fa,
+                             float& fb) {
+      const bool na = quad_or(first_a || !(sa <= PART_LIMIT));
+      const bool nb = quad_or(first_b || !(sb <= PART_LIMIT));
       float xa = -INFINITY, xb = -INFINITY;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
@@ -404,13 +543,13 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       fb = 1.f;
       if (na) {
         const float mn = fmaxf(m_a, xa * sl2);
-        fa = first ? 0.f : ex2_approx(m_a - mn);
+        fa = first_a ? 0.f : ex2_approx(m_a - mn);
         m_a = mn;
         l_a *= fa;
       }
       if (nb) {
         const float mn = fmaxf(m_b, xb * sl2);
-        fb = first ? 0.f : ex2_approx(m_b - mn);
+        fb = first_b ? 0.f : ex2_approx(m_b - mn);
         m_b = mn;
         l_b *= fb;
       }
@@ -473,6 +612,25 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
 
     for (int j = 0; ok && j < nkv; ++j) {
+      const int key0 = (tile0 + j) * BN;
+      bool partial = false;                         // masked: some row does not see all of the tile
+      uint4 bad = make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (MASKED) {
+        partial = key0 < full_lo || key0 + BN > full_hi;
+        if (partial) {
+          // all softmax warps clean V(j) together; PV(j) waits for P(j), hence for them
+          const int vidx = 2 * j + 1, vs = vidx % KV_STAGES;
+          if (!warp_wait(bar_kv_full(vs), (vidx / KV_STAGES) & 1, abort_flag, limit, eslot)) { ok = false; break; }
+          const uint32_t rows = clean_rows(gbase + SMEM_KV + vs * TILE_BYTES, warp, lane);
+          if (rows != 0u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (lane == 0) reinterpret_cast<volatile uint8_t*>(&unclean[cleaned & 1])[warp] = static_cast<uint8_t>(rows);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_v_clean);
+          if (!warp_wait(bar_v_clean, cleaned & 1, abort_flag, limit, eslot)) { ok = false; break; }
+          bad = unclean[cleaned & 1];
+          ++cleaned;
+        }
+      }
       if (!warp_wait(bar_s_full(wg), j & 1, abort_flag, limit, eslot)) { ok = false; break; }
       tc_fence_after();
       const bool last = j == nkv - 1;
@@ -483,13 +641,16 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tmem_wait_ld(r);
         float x[32];
         to_logits(r, 0, last, x);
+        if (MASKED && partial) mask_logits(key0, bad.x, bad.y, x);
         uint32_t pk[16];
         float sa, sb;
         exps(x, pk, sa, sb);                        // speculative against the references
-        const bool need = (j == 0) || !(sa <= PART_LIMIT) || !(sb <= PART_LIMIT);
+        const bool first_a = MASKED ? m_a == -INFINITY && sees(rng_a, key0) : j == 0;
+        const bool first_b = MASKED ? m_b == -INFINITY && sees(rng_b, key0) : j == 0;
+        const bool need = first_a || first_b || !(sa <= PART_LIMIT) || !(sb <= PART_LIMIT);
         if (__any_sync(0xffffffffu, need)) {
           float fa, fb;
-          new_reference(x, j == 0, sa, sb, fa, fb);
+          new_reference(x, first_a, first_b, sa, sb, fa, fb);
           __syncwarp();
           if (j > 0) rescale_o(fa, fb);   // O holds PV(j-1); PV(j) has not started
           exps(x, pk, sa, sb);
@@ -506,17 +667,20 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tmem_wait_ld(r);
         float x[32];
         to_logits(r, 64, last, x);
+        if (MASKED && partial) mask_logits(key0 + 64, bad.z, bad.w, x);
         uint32_t pk[16];
         float sa, sb;
         exps(x, pk, sa, sb);
-        const bool need = !(sa <= PART_LIMIT) || !(sb <= PART_LIMIT);
+        const bool first_a = MASKED && m_a == -INFINITY && sees(rng_a, key0 + 64);
+        const bool first_b = MASKED && m_b == -INFINITY && sees(rng_b, key0 + 64);
+        const bool need = first_a || first_b || !(sa <= PART_LIMIT) || !(sb <= PART_LIMIT);
         if (__any_sync(0xffffffffu, need)) {
           // the first half of PV(j) may be in flight: let it land, then rescale
           // O (which now includes it) together with the running sums
           if (!warp_wait(bar_pva_done(wg), j & 1, abort_flag, limit, eslot)) { ok = false; break; }
           tc_fence_after();
           float fa, fb;
-          new_reference(x, false, sa, sb, fa, fb);
+          new_reference(x, first_a, first_b, sa, sb, fa, fb);
           __syncwarp();
           rescale_o(fa, fb);
           exps(x, pk, sa, sb);
@@ -535,7 +699,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
       l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
       l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
-      const float inv_a = 1.f / l_a, inv_b = 1.f / l_b;
+      // masked: a row without keys has l = 0 and O = 0
+      const float inv_a = MASKED && l_a == 0.f ? 0.f : 1.f / l_a, inv_b = MASKED && l_b == 0.f ? 0.f : 1.f / l_b;
       __nv_bfloat16* orow_a = p.o + batch * p.o_batch_stride + static_cast<long long>(row_a) * p.o_row_stride + head * HD;
       __nv_bfloat16* orow_b = orow_a + 8 * p.o_row_stride;
 #pragma unroll 1

@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "common.cuh"
@@ -17,6 +18,8 @@
 #include "rope.cuh"
 #include "attention.cuh"
 #include "adaln.cuh"
+#include "norm.cuh"
+#include "ranges.cuh"
 
 namespace {
 
@@ -45,7 +48,9 @@ const DeviceState* device_state() {
   std::lock_guard<std::mutex> lock(g_state_mu);
   DeviceState& st = g_states[dev];
   if (!st.ready) {
-    if (cudaFuncSetAttribute(h3::attn::attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(h3::attn::attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(h3::attn::SMEM_BYTES)) != cudaSuccess ||
+        cudaFuncSetAttribute(h3::attn::attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(h3::attn::SMEM_BYTES)) != cudaSuccess)
       return nullptr;
     int n = 0;
@@ -315,7 +320,7 @@ h3_status h3_packed_attention(const void* d_q, const void* d_k, const void* d_v,
   p.rope_layout = d_rope_cs ? cfg->pair_layout : 0;
   const dim3 grid(static_cast<unsigned>((n_rows + 2 * h3::attn::BM - 1) / (2 * h3::attn::BM)),
                   static_cast<unsigned>(n_heads), static_cast<unsigned>(batch));
-  h3::attn::attention_kernel<<<grid, h3::attn::THREADS, h3::attn::SMEM_BYTES, as_stream(stream)>>>(tq, tk, tv,
+  h3::attn::attention_kernel<false><<<grid, h3::attn::THREADS, h3::attn::SMEM_BYTES, as_stream(stream)>>>(tq, tk, tv,
                                                                                                   p);
   return cudaGetLastError() == cudaSuccess ? H3_OK : H3_ERR_CUDA;
 }
@@ -660,7 +665,7 @@ h3_status h3_init(int32_t device) {
   DeviceGuard guard;
   if (cudaSetDevice(device) != cudaSuccess) return H3_ERR_CUDA;
   cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, h3::attn::attention_kernel) != cudaSuccess) return H3_ERR_UNSUPPORTED;
+  if (cudaFuncGetAttributes(&fa, h3::attn::attention_kernel<false>) != cudaSuccess) return H3_ERR_UNSUPPORTED;
   if (encode_tiled() == nullptr || device_state() == nullptr || host_pipe() == nullptr ||
       noalloc_scratch() == nullptr)
     return H3_ERR_CUDA;
@@ -689,3 +694,5 @@ void h3_shutdown(void) {
 }
 
 }  // extern "C"
+
+#include "train_api.cuh"

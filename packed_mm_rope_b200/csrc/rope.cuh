@@ -153,4 +153,72 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS_PER_SM) rope_kernel(
   }
 }
 
+// Q and K with head counts and strides of their own, either of which may be
+// absent (0 heads).
+struct GroupedRope {
+  const uint4* src[2];        // q, k
+  uint4* dst[2];
+  long long src_stride[2];    // row strides in 16-byte chunks
+  long long dst_stride[2];
+  int heads[2];
+};
+
+// As rope_kernel, over the heads of Q followed by those of K: the items of a
+// row are those of both tensors in a row, so a lane still meets the same pairs
+// in every item.  The rotation back (the gradient) is the same kernel with a
+// table of negated frequencies.
+template <int LAYOUT>
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS_PER_SM) rope_grouped_kernel(
+    const GroupedRope p, const float* __restrict__ coords, long long n_rows, const RopeTable tab) {
+  constexpr int IPH = LAYOUT == 0 ? 16 : 8;        // work items per head
+  constexpr int PPI = LAYOUT == 0 ? 4 : 8;         // rotary pairs per item
+  constexpr int B = LAYOUT == 0 ? 14 : 8;          // items per lane in flight
+  const int lane = threadIdx.x & 31;
+  const int sub = lane % IPH;                      // item index within the head
+  const long long gw = (static_cast<long long>(blockIdx.x) * ROPE_THREADS + threadIdx.x) >> 5;
+  const long long nw = (static_cast<long long>(gridDim.x) * ROPE_THREADS) >> 5;
+  const int q_items = p.heads[0] * IPH;
+  const int items = q_items + p.heads[1] * IPH;
+  for (long long r = gw; r < n_rows; r += nw) {
+    const uint4* const qs = p.src[0] + r * p.src_stride[0] + sub;
+    const uint4* const ks = p.src[1] + r * p.src_stride[1] + sub;
+    uint4* const qd = p.dst[0] + r * p.dst_stride[0] + sub;
+    uint4* const kd = p.dst[1] + r * p.dst_stride[1] + sub;
+    float2 cs[PPI];
+    bool first = true;
+    for (int i0 = lane; i0 < items; i0 += 32 * B) {
+      uint4 a[B], b[B];
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        const int item = i0 + 32 * u;
+        if (item < items) {
+          const uint4* s = item < q_items ? qs + (item / IPH) * 16 : ks + ((item - q_items) / IPH) * 16;
+          a[u] = __ldcs(s);
+          if (LAYOUT == 1) b[u] = __ldcs(s + 8);
+        }
+      }
+      if (first) {
+        const float* crd = coords + 3 * r;
+#pragma unroll
+        for (int m = 0; m < PPI; ++m) cs[m] = rope_cos_sin(tab, crd, PPI * sub + m);
+        first = false;
+      }
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        const int item = i0 + 32 * u;
+        if (item < items) {
+          uint4* d = item < q_items ? qd + (item / IPH) * 16 : kd + ((item - q_items) / IPH) * 16;
+          if (LAYOUT == 0) {
+            __stcs(d, rotate_adjacent(a[u], cs));
+          } else {
+            rotate_half(a[u], b[u], cs);
+            __stcs(d, a[u]);
+            __stcs(d + 8, b[u]);
+          }
+        }
+      }
+    }
+  }
+}
+
 }  // namespace h3

@@ -1,0 +1,369 @@
+// train_api.cuh -- host side of the training-direction calls and of the
+// masked attention (declared in include/h3.h): argument checks, workspace
+// layout and launches.  Included by h3.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+h3_status launched() { return cudaGetLastError() == cudaSuccess ? H3_OK : H3_ERR_CUDA; }
+
+inline uint64_t up256(uint64_t b) { return (b + 255u) & ~uint64_t(255u); }
+
+inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+int dtype_size(int32_t dtype) { return dtype == H3_DTYPE_F32 ? 4 : 2; }
+
+bool valid_dtype(int32_t dtype) { return dtype == H3_DTYPE_BF16 || dtype == H3_DTYPE_F16 || dtype == H3_DTYPE_F32; }
+
+// Whether rows of `stride` elements starting at p can be read 16 bytes at a time.
+bool vector_rows(const void* p, int64_t stride, int32_t dtype) {
+  return aligned16(p) && (stride * dtype_size(dtype)) % 16 == 0;
+}
+
+template <typename T>
+struct TypeTag {
+  using type = T;
+};
+
+// Calls f with the types of (x dtype, parameter dtype); the parameters share
+// x's type or are fp32.
+template <typename F>
+h3_status with_types(int32_t dtype, int32_t param_dtype, F f) {
+  if (dtype == H3_DTYPE_F32) return f(TypeTag<float>{}, TypeTag<float>{});
+  if (dtype == H3_DTYPE_BF16)
+    return param_dtype == H3_DTYPE_F32 ? f(TypeTag<__nv_bfloat16>{}, TypeTag<float>{})
+                                       : f(TypeTag<__nv_bfloat16>{}, TypeTag<__nv_bfloat16>{});
+  return param_dtype == H3_DTYPE_F32 ? f(TypeTag<__half>{}, TypeTag<float>{})
+                                     : f(TypeTag<__half>{}, TypeTag<__half>{});
+}
+
+// ---- layer norm ----
+
+// Threads per row and chunks of 8 elements per thread, by the row's length.
+template <int G_, int CH_>
+struct RowShape {
+  static constexpr int G = G_, CH = CH_;
+  static constexpr int BLOCK = G > h3::norm::THREADS ? G : h3::norm::THREADS;
+  static constexpr int GROUPS = BLOCK / G;
+};
+
+// Forward: a warp per row up to 1,024 elements, else 128 or 256 threads with
+// up to 8 chunks each.
+template <typename F>
+h3_status with_forward_shape(int hidden, F f) {
+  const int chunks = (hidden + 7) / 8;
+  if (chunks <= 32) return f(RowShape<32, 1>{});
+  if (chunks <= 128) return f(RowShape<32, 4>{});
+  if (chunks <= 512) return f(RowShape<128, 4>{});
+  if (chunks <= 1024) return f(RowShape<128, 8>{});
+  return f(RowShape<256, 8>{});
+}
+
+// Backward: a thread also holds 16 fp32 column sums per chunk, hence more
+// threads per row with fewer chunks each.
+template <typename F>
+h3_status with_backward_shape(int hidden, F f) {
+  const int chunks = (hidden + 7) / 8;
+  if (chunks <= 32) return f(RowShape<32, 1>{});
+  if (chunks <= 128) return f(RowShape<32, 4>{});
+  if (chunks <= 512) return f(RowShape<256, 2>{});
+  if (chunks <= 768) return f(RowShape<256, 3>{});
+  if (chunks <= 1024) return f(RowShape<256, 4>{});
+  return f(RowShape<512, 4>{});
+}
+
+constexpr int kBackwardBlocks = 296;   // two blocks per SM of a B200: every partial row is read once more
+
+// Blocks of the backward row kernels (a partial row per group of each).
+template <typename S>
+long long backward_blocks(int64_t n_rows) {
+  return std::min<long long>(kBackwardBlocks, (n_rows + S::GROUPS - 1) / S::GROUPS);
+}
+
+long long backward_groups(int64_t n_rows, int hidden) {
+  long long groups = 0;
+  with_backward_shape(hidden, [&](auto shape) {
+    using S = decltype(shape);
+    groups = backward_blocks<S>(n_rows) * S::GROUPS;
+    return H3_OK;
+  });
+  return groups;
+}
+
+// ---- AdaLN backward: workspace ----
+
+struct AdalnWork {
+  long long groups, per;               // row groups, sorted positions per group
+  int blocks;                          // sorting blocks
+  uint64_t order, starts, hist, partials, bytes;   // offsets and total size
+};
+
+AdalnWork adaln_work(int64_t n_rows, int hidden, int32_t n_entries) {
+  AdalnWork w;
+  w.groups = std::max<long long>(1, backward_groups(n_rows, hidden));
+  w.per = std::max<long long>(1, (n_rows + w.groups - 1) / w.groups);
+  w.blocks = static_cast<int>((n_rows + h3::norm::SORT_ROWS - 1) / h3::norm::SORT_ROWS);
+  w.order = 0;
+  w.starts = up256(static_cast<uint64_t>(n_rows) * 8u);
+  w.hist = w.starts + up256((static_cast<uint64_t>(n_entries) + 2u) * 4u);
+  w.partials = w.hist + up256(static_cast<uint64_t>(w.blocks) * (static_cast<uint64_t>(n_entries) + 1u) * 4u);
+  w.bytes = w.partials + up256((static_cast<uint64_t>(w.groups) + n_entries) * 2u * hidden * 4u);
+  return w;
+}
+
+// ---- masked attention ----
+
+// Sizes and strides of a masked attention problem; the strides of tensors that
+// a call does not take are left out of `strides`.
+h3_status check_attention(const h3_attn_shape* a, std::initializer_list<int64_t> q_strides,
+                          std::initializer_list<int64_t> kv_strides) {
+  if (a == nullptr || a->batch < 1 || a->n_heads < 1 || a->n_kv_heads < 1 || a->n_heads % a->n_kv_heads != 0 ||
+      a->n_q < 0 || a->n_k < 0 || a->n_q >= (1ll << 31) || a->n_k >= (1ll << 31) || a->batch > 65535 ||
+      a->n_heads > 65535 || !std::isfinite(a->softmax_scale))
+    return H3_ERR_INVALID_ARG;
+  if (a->head_dim != 128) return H3_ERR_UNSUPPORTED;
+  h3_status st = H3_OK;
+  auto check = [&](int64_t stride, int32_t heads) {
+    if (stride < static_cast<int64_t>(heads) * 128) st = H3_ERR_INVALID_ARG;
+    else if (stride % 8 != 0 && st == H3_OK) st = H3_ERR_UNSUPPORTED;
+  };
+  for (int64_t s : q_strides) check(s, a->n_heads);
+  for (int64_t s : kv_strides) check(s, a->n_kv_heads);
+  return st;
+}
+
+float attention_scale(const h3_attn_shape* a) {
+  return a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / std::sqrt(128.0f);
+}
+
+}  // namespace
+
+extern "C" {
+
+h3_status h3_build_key_ranges(const int32_t* d_doc_starts, const int32_t* d_prefix, int32_t n_docs, int64_t n_rows,
+                              int32_t mode, int32_t* d_ranges, void* stream) {
+  if (n_docs < 0 || n_rows < 0 || n_rows >= (1ll << 31) ||
+      (mode != H3_MASK_DOCUMENT && mode != H3_MASK_PREFIX_CAUSAL && mode != H3_MASK_PREFIX_BLOCK))
+    return H3_ERR_INVALID_ARG;
+  if (!d_doc_starts || (n_rows > 0 && !d_ranges)) return H3_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(d_ranges) & 7u) return H3_ERR_UNSUPPORTED;
+  const long long need = (std::max<long long>(n_rows, n_docs + 1LL) + 255) / 256;
+  const int grid = static_cast<int>(std::min<long long>(need, 8LL * sm_count()));
+  h3::key_ranges_kernel<<<grid, 256, 0, as_stream(stream)>>>(d_doc_starts, d_prefix, n_docs, static_cast<int>(n_rows),
+                                                             mode, reinterpret_cast<int2*>(d_ranges),
+                                                             error_slot(stream));
+  return launched();
+}
+
+h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v, void* d_o, float* d_lse,
+                              const int32_t* d_ranges, const h3_attn_shape* a, int64_t q_stride, int64_t k_stride,
+                              int64_t v_stride, int64_t o_stride, void* stream) {
+  const h3_status st = check_attention(a, {q_stride, o_stride}, {k_stride, v_stride});
+  if (st != H3_OK || a->n_q == 0) return st;
+  if (!d_q || !d_o || !d_ranges || (a->n_k > 0 && (!d_k || !d_v))) return H3_ERR_INVALID_ARG;
+  if (!aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) || !aligned16(d_o) ||
+      (reinterpret_cast<uintptr_t>(d_ranges) & 7u))
+    return H3_ERR_UNSUPPORTED;
+  CUtensorMap tq, tk, tv;
+  if (!make_qkv_map(&tq, d_q, a->batch, a->n_q, a->n_heads, q_stride, 128)) return H3_ERR_CUDA;
+  tk = tv = tq;                          // without keys every row is empty and K, V are never read
+  if (a->n_k > 0 && (!make_qkv_map(&tk, d_k, a->batch, a->n_k, a->n_kv_heads, k_stride, 128) ||
+                     !make_qkv_map(&tv, d_v, a->batch, a->n_k, a->n_kv_heads, v_stride, 128)))
+    return H3_ERR_CUDA;
+  if (device_state() == nullptr) return H3_ERR_CUDA;
+  h3::attn::Params p{};
+  p.n_rows = static_cast<int>(a->n_q);
+  p.n_heads = a->n_heads;
+  p.n_keys = static_cast<int>(a->n_k);
+  p.group = a->n_heads / a->n_kv_heads;
+  p.ranges = reinterpret_cast<const int2*>(d_ranges);
+  p.scale_log2 = attention_scale(a) * 1.4426950408889634f;
+  p.o = static_cast<__nv_bfloat16*>(d_o);
+  p.o_row_stride = o_stride;
+  p.o_batch_stride = o_stride * a->n_q;
+  p.lse = d_lse;
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  p.drain_limit_ns = kDrainLimitNs;
+  p.err_slot = error_slot(stream);
+  const dim3 grid(static_cast<unsigned>((a->n_q + 2 * h3::attn::BM - 1) / (2 * h3::attn::BM)),
+                  static_cast<unsigned>(a->n_heads), static_cast<unsigned>(a->batch));
+  h3::attn::attention_kernel<true><<<grid, h3::attn::THREADS, h3::attn::SMEM_BYTES, as_stream(stream)>>>(tq, tk, tv, p);
+  return launched();
+}
+
+h3_status h3_mmrope_rotate(const void* d_q, const void* d_k, void* d_q_out, void* d_k_out, const float* d_coords,
+                           int64_t n_rows, int32_t n_heads, int32_t n_kv_heads, int64_t q_stride, int64_t k_stride,
+                           int64_t q_out_stride, int64_t k_out_stride, const h3_rope_cfg* cfg, int32_t inverse,
+                           void* stream) {
+  if (n_rows < 0 || n_heads < 0 || n_kv_heads < 0 || n_heads + static_cast<int64_t>(n_kv_heads) < 1 ||
+      n_heads > 65535 || n_kv_heads > 65535 || !valid_rope_cfg(cfg) || (inverse != 0 && inverse != 1))
+    return H3_ERR_INVALID_ARG;
+  if (cfg->head_dim != 128) return H3_ERR_UNSUPPORTED;
+  const int64_t q_row = static_cast<int64_t>(n_heads) * 128, k_row = static_cast<int64_t>(n_kv_heads) * 128;
+  if (q_stride < q_row || q_out_stride < q_row || k_stride < k_row || k_out_stride < k_row) return H3_ERR_INVALID_ARG;
+  if (n_rows == 0) return H3_OK;
+  if ((n_heads > 0 && (!d_q || !d_q_out)) || (n_kv_heads > 0 && (!d_k || !d_k_out)) || !d_coords)
+    return H3_ERR_INVALID_ARG;
+  if ((q_stride | k_stride | q_out_stride | k_out_stride) % 8 != 0 || !aligned16(d_q) || !aligned16(d_k) ||
+      !aligned16(d_q_out) || !aligned16(d_k_out))
+    return H3_ERR_UNSUPPORTED;
+  h3::RopeTable tab = make_rope_table(cfg);
+  if (inverse)   // the rotation by -a: cos is even and sin odd, exactly
+    for (double& f : tab.inv_freq) f = -f;
+  h3::GroupedRope p;
+  p.src[0] = static_cast<const uint4*>(d_q);
+  p.src[1] = static_cast<const uint4*>(d_k);
+  p.dst[0] = static_cast<uint4*>(d_q_out);
+  p.dst[1] = static_cast<uint4*>(d_k_out);
+  p.src_stride[0] = q_stride / 8;
+  p.src_stride[1] = k_stride / 8;
+  p.dst_stride[0] = q_out_stride / 8;
+  p.dst_stride[1] = k_out_stride / 8;
+  p.heads[0] = n_heads;
+  p.heads[1] = n_kv_heads;
+  const long long warps_per_cta = h3::ROPE_THREADS / 32;
+  const long long nblk = (n_rows + warps_per_cta - 1) / warps_per_cta;
+  const long long cap = 2LL * h3::ROPE_CTAS_PER_SM * sm_count();
+  const int grid = static_cast<int>(nblk < cap ? nblk : cap);
+  if (cfg->pair_layout == 0)
+    h3::rope_grouped_kernel<0><<<grid, h3::ROPE_THREADS, 0, as_stream(stream)>>>(p, d_coords, n_rows, tab);
+  else
+    h3::rope_grouped_kernel<1><<<grid, h3::ROPE_THREADS, 0, as_stream(stream)>>>(p, d_coords, n_rows, tab);
+  return launched();
+}
+
+h3_status h3_layernorm(const void* d_x, void* d_y, const void* d_weight, const void* d_bias, float* d_mean,
+                       float* d_rstd, int64_t n_rows, int32_t hidden, int64_t x_row_stride, int64_t y_row_stride,
+                       int32_t dtype, int32_t param_dtype, float eps, void* stream) {
+  if (n_rows < 0 || hidden < 1 || !(eps >= 0.f) || !std::isfinite(eps) || !valid_dtype(dtype) ||
+      !valid_dtype(param_dtype))
+    return H3_ERR_INVALID_ARG;
+  if (x_row_stride < hidden || y_row_stride < hidden) return H3_ERR_INVALID_ARG;
+  if (hidden > h3::norm::MAX_HIDDEN || (param_dtype != dtype && param_dtype != H3_DTYPE_F32)) return H3_ERR_UNSUPPORTED;
+  if (n_rows == 0) return H3_OK;
+  if (!d_x || !d_y) return H3_ERR_INVALID_ARG;
+  const bool vec = hidden % 8 == 0 && vector_rows(d_x, x_row_stride, dtype) && vector_rows(d_y, y_row_stride, dtype) &&
+                   aligned16(d_weight) && aligned16(d_bias);
+  const int sms = sm_count();
+  return with_types(dtype, param_dtype, [&](auto tt, auto pt) {
+    using T = typename decltype(tt)::type;
+    using P = typename decltype(pt)::type;
+    return with_forward_shape(hidden, [&](auto shape) {
+      using S = decltype(shape);
+      const long long grid = std::min<long long>((n_rows + S::GROUPS - 1) / S::GROUPS, 16LL * sms);
+      auto go = [&](auto kernel) {
+        kernel<<<static_cast<int>(grid), S::BLOCK, 0, as_stream(stream)>>>(
+            static_cast<const T*>(d_x), static_cast<T*>(d_y), static_cast<const P*>(d_weight),
+            static_cast<const P*>(d_bias), d_mean, d_rstd, static_cast<long long>(n_rows), hidden, x_row_stride,
+            y_row_stride, eps);
+        return launched();
+      };
+      return vec ? go(h3::norm::layernorm_kernel<T, P, true, S::G, S::CH>)
+                 : go(h3::norm::layernorm_kernel<T, P, false, S::G, S::CH>);
+    });
+  });
+}
+
+uint64_t h3_layernorm_backward_workspace_bytes(int64_t n_rows, int32_t hidden) {
+  if (n_rows < 0 || hidden < 1 || hidden > h3::norm::MAX_HIDDEN) return 0;
+  return std::max<uint64_t>(256u, up256(static_cast<uint64_t>(backward_groups(n_rows, hidden)) * 2u * hidden * 4u));
+}
+
+h3_status h3_layernorm_backward(const void* d_dy, const void* d_x, const float* d_mean, const float* d_rstd,
+                                const void* d_weight, void* d_dx, void* d_dweight, void* d_dbias, void* d_work,
+                                int64_t n_rows, int32_t hidden, int64_t dy_row_stride, int64_t x_row_stride,
+                                int64_t dx_row_stride, int32_t dtype, int32_t param_dtype, void* stream) {
+  if (n_rows < 0 || hidden < 1 || !valid_dtype(dtype) || !valid_dtype(param_dtype)) return H3_ERR_INVALID_ARG;
+  if (dy_row_stride < hidden || x_row_stride < hidden || dx_row_stride < hidden) return H3_ERR_INVALID_ARG;
+  if (hidden > h3::norm::MAX_HIDDEN || (param_dtype != dtype && param_dtype != H3_DTYPE_F32)) return H3_ERR_UNSUPPORTED;
+  const bool params = d_dweight != nullptr || d_dbias != nullptr;
+  if (params && (d_work == nullptr || !aligned256(d_work))) return H3_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!d_dy || !d_x || !d_mean || !d_rstd || !d_dx)) return H3_ERR_INVALID_ARG;
+  const bool vec = hidden % 8 == 0 && vector_rows(d_dy, dy_row_stride, dtype) && vector_rows(d_x, x_row_stride, dtype) &&
+                   vector_rows(d_dx, dx_row_stride, dtype) && aligned16(d_weight);
+  float* partials = params ? static_cast<float*>(d_work) : nullptr;
+  return with_types(dtype, param_dtype, [&](auto tt, auto pt) {
+    using T = typename decltype(tt)::type;
+    using P = typename decltype(pt)::type;
+    return with_backward_shape(hidden, [&](auto shape) {
+      using S = decltype(shape);
+      const long long grid = backward_blocks<S>(n_rows);
+      if (grid > 0) {
+        auto go = [&](auto kernel) {
+          kernel<<<static_cast<int>(grid), S::BLOCK, 0, as_stream(stream)>>>(
+              static_cast<const T*>(d_dy), static_cast<const T*>(d_x), d_mean, d_rstd, static_cast<const P*>(d_weight),
+              static_cast<T*>(d_dx), partials, static_cast<long long>(n_rows), hidden, dy_row_stride, x_row_stride,
+              dx_row_stride);
+          return launched();
+        };
+        const h3_status st = vec ? go(h3::norm::layernorm_backward_kernel<T, P, true, S::G, S::CH>)
+                                 : go(h3::norm::layernorm_backward_kernel<T, P, false, S::G, S::CH>);
+        if (st != H3_OK) return st;
+      }
+      if (!params) return H3_OK;
+      const dim3 rgrid((hidden + 31) / 32, 2);
+      h3::norm::norm_reduce_kernel<P><<<rgrid, 32 * h3::norm::REDUCE_ROWS, 0, as_stream(stream)>>>(
+          partials, static_cast<int>(grid * S::GROUPS), hidden, static_cast<P*>(d_dweight), static_cast<P*>(d_dbias));
+      return launched();
+    });
+  });
+}
+
+uint64_t h3_adaln_backward_workspace_bytes(int64_t n_rows, int32_t hidden, int32_t n_entries) {
+  if (n_rows < 0 || n_rows >= (1ll << 31) || hidden < 8 || hidden % 8 != 0 || hidden > h3::ADALN_MAX_HIDDEN ||
+      n_entries < 1 || n_entries > h3::norm::MAX_ENTRIES)
+    return 0;
+  return adaln_work(n_rows, hidden, n_entries).bytes;
+}
+
+h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const int32_t* d_timestep_index,
+                                     const int32_t* d_token_tag, const float* d_table, void* d_dx, float* d_dtable,
+                                     void* d_work, int32_t n_entries, int64_t n_rows, int32_t hidden,
+                                     int64_t dy_row_stride, int64_t x_row_stride, int64_t dx_row_stride, float eps,
+                                     void* stream) {
+  if (n_rows < 0 || n_rows >= (1ll << 31) || hidden < 8 || n_entries < 1 || !(eps >= 0.f) || !std::isfinite(eps))
+    return H3_ERR_INVALID_ARG;
+  if (hidden % 8 != 0 || hidden > h3::ADALN_MAX_HIDDEN || n_entries > h3::norm::MAX_ENTRIES) return H3_ERR_UNSUPPORTED;
+  if (dy_row_stride < hidden || x_row_stride < hidden || dx_row_stride < hidden) return H3_ERR_INVALID_ARG;
+  if (!d_dtable || !d_work || !aligned256(d_work)) return H3_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!d_dy || !d_x || !d_timestep_index || !d_token_tag || !d_table || !d_dx)) return H3_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!vector_rows(d_dy, dy_row_stride, H3_DTYPE_BF16) || !vector_rows(d_x, x_row_stride, H3_DTYPE_BF16) ||
+                     !vector_rows(d_dx, dx_row_stride, H3_DTYPE_BF16) || !aligned16(d_table)))
+    return H3_ERR_UNSUPPORTED;
+  cudaStream_t s = as_stream(stream);
+  if (n_rows == 0)
+    return cudaMemsetAsync(d_dtable, 0, static_cast<size_t>(n_entries) * 2u * hidden * 4u, s) == cudaSuccess
+               ? H3_OK
+               : H3_ERR_CUDA;
+  const AdalnWork w = adaln_work(n_rows, hidden, n_entries);
+  uint8_t* base = static_cast<uint8_t*>(d_work);
+  int2* order = reinterpret_cast<int2*>(base + w.order);
+  int* starts = reinterpret_cast<int*>(base + w.starts);
+  int* hist = reinterpret_cast<int*>(base + w.hist);
+  float* partials = reinterpret_cast<float*>(base + w.partials);
+  const size_t smem = (static_cast<size_t>(n_entries) + 1u) * sizeof(int);
+  h3::norm::adaln_count_kernel<<<w.blocks, h3::norm::SORT_ROWS, smem, s>>>(d_timestep_index, d_token_tag, n_entries,
+                                                                           n_rows, hist, error_slot(stream));
+  h3::norm::adaln_place_kernel<<<w.blocks, h3::norm::SORT_ROWS, smem, s>>>(d_timestep_index, d_token_tag, n_entries,
+                                                                           n_rows, hist, w.blocks, order, starts);
+  h3_status st = launched();
+  if (st != H3_OK) return st;
+  st = with_backward_shape(hidden, [&](auto shape) {
+    using S = decltype(shape);
+    if constexpr (S::G <= 256) {   // up to ADALN_MAX_HIDDEN
+      h3::norm::adaln_backward_kernel<S::G, S::CH><<<static_cast<int>(w.groups / S::GROUPS), S::BLOCK, 0, s>>>(
+          static_cast<const __nv_bfloat16*>(d_dy), static_cast<const __nv_bfloat16*>(d_x), d_table, order,
+          static_cast<__nv_bfloat16*>(d_dx), partials, n_entries, n_rows, w.per, hidden, dy_row_stride, x_row_stride,
+          dx_row_stride, eps);
+      return launched();
+    } else {
+      return H3_ERR_UNSUPPORTED;
+    }
+  });
+  if (st != H3_OK) return st;
+  const dim3 rgrid((hidden + 31) / 32, 2 * n_entries);
+  h3::norm::adaln_reduce_kernel<<<rgrid, 32 * h3::norm::REDUCE_ROWS, 0, s>>>(partials, starts, w.per, hidden, d_dtable);
+  return launched();
+}
+
+}  // extern "C"

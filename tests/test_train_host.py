@@ -1,0 +1,127 @@
+"""Host-side refusals of the masked-attention and training-direction calls: nothing is launched, no GPU needed."""
+import ctypes
+
+import pytest
+
+import packed_mm_rope_b200 as h3
+from packed_mm_rope_b200 import _lib
+
+P = 0x10000
+INV, UNS = h3.H3_ERR_INVALID_ARG, h3.H3_ERR_UNSUPPORTED
+
+
+def _err(fn, *a, **kw):
+    with pytest.raises(h3.H3Error) as e:
+        fn(*a, **kw)
+    return e.value.status
+
+
+def test_attn_shape_layout():
+    assert ctypes.sizeof(h3.h3_attn_shape) == 40
+
+
+def test_rotate():
+    R, cfg = h3.h3_mmrope_rotate, h3.rope_cfg()
+    ok = (P, P, P, P, P, 4, 2, 1, 256, 128, 256, 128, cfg)
+    R(0, 0, 0, 0, 0, 0, 2, 1, 256, 128, 256, 128, cfg)                     # no rows: no-op
+
+    def but(**kw):
+        a = list(ok)
+        for i, v in kw.items():
+            a[int(i[1:])] = v
+        return a
+
+    for a in (but(_5=-1), but(_6=-1), but(_6=0, _7=0), but(_0=0), but(_2=0), but(_1=0), but(_3=0), but(_4=0),
+              but(_8=248), but(_9=120), but(_10=248), but(_11=0), but(_12=h3.rope_cfg(theta=1.0))):
+        assert _err(R, *a) == INV
+    assert _err(R, *ok, 2) == INV
+    for a in (but(_0=P + 8), but(_3=P + 2), but(_8=260), but(_11=132),
+              but(_12=h3.rope_cfg(head_dim=256, sections=(64, 96, 96)))):
+        assert _err(R, *a) == UNS
+
+
+def test_key_ranges():
+    B = h3.h3_build_key_ranges
+    assert _err(B, P, 0, -1, 4, 0, P) == INV
+    assert _err(B, P, 0, 1, -1, 0, P) == INV
+    assert _err(B, P, 0, 1, 1 << 31, 0, P) == INV
+    assert _err(B, P, 0, 1, 4, 3, P) == INV
+    assert _err(B, 0, 0, 1, 4, 0, P) == INV
+    assert _err(B, P, 0, 1, 4, 0, 0) == INV
+    assert _err(B, P, 0, 1, 4, 0, P + 4) == UNS
+
+
+def _shape(**kw):
+    d = dict(n_q=4, n_k=4, batch=1, n_heads=4, n_kv_heads=2, head_dim=128, softmax_scale=0.0)
+    d.update(kw)
+    return h3.h3_attn_shape(**d)
+
+
+def test_masked_attention():
+    A = h3.h3_masked_attention
+    strides = (512, 256, 256, 512)
+    A(0, 0, 0, 0, 0, 0, _shape(n_q=0), *strides)                            # no rows: no-op
+    for kw in (dict(batch=0), dict(batch=65536), dict(n_heads=0), dict(n_kv_heads=0), dict(n_heads=5), dict(n_q=-1),
+               dict(n_k=-1), dict(n_q=1 << 31), dict(n_k=1 << 31), dict(softmax_scale=float("inf"))):
+        assert _err(A, P, P, P, P, 0, P, _shape(**kw), *strides) == INV, kw
+    assert _err(A, P, P, P, P, 0, P, _shape(head_dim=64), *strides) == UNS
+    for i in range(4):
+        s = list(strides)
+        s[i] -= 8
+        assert _err(A, P, P, P, P, 0, P, _shape(), *s) == INV
+        s[i] += 12
+        assert _err(A, P, P, P, P, 0, P, _shape(), *s) == UNS
+        ptrs = [P, P, P, P]
+        ptrs[i] = 0
+        assert _err(A, *ptrs, 0, P, _shape(), *strides) == INV
+        ptrs[i] = P + 8
+        assert _err(A, *ptrs, 0, P, _shape(), *strides) == UNS
+    assert _err(A, P, P, P, P, 0, 0, _shape(), *strides) == INV
+    assert _err(A, P, P, P, P, 0, P + 4, _shape(), *strides) == UNS
+
+
+def test_layernorm():
+    L, B, W = h3.h3_layernorm, h3.h3_layernorm_backward, h3.h3_layernorm_backward_workspace_bytes
+    L(0, 0, 0, 0, 0, 0, 0, 64, 64, 64)                                       # no rows: no-op
+    assert _err(L, P, P, 0, 0, 0, 0, -1, 64, 64, 64) == INV
+    assert _err(L, P, P, 0, 0, 0, 0, 4, 0, 64, 64) == INV
+    assert _err(L, P, P, 0, 0, 0, 0, 4, 64, 63, 64) == INV
+    assert _err(L, P, P, 0, 0, 0, 0, 4, 64, 64, 63) == INV
+    assert _err(L, P, 0, 0, 0, 0, 0, 4, 64, 64, 64) == INV
+    assert _err(L, P, P, 0, 0, 0, 0, 4, 64, 64, 64, 3) == INV
+    assert _err(L, P, P, 0, 0, 0, 0, 4, 64, 64, 64, 0, 2, -1.0) == INV
+    assert _err(L, P, P, 0, 0, 0, 0, 4, 64, 64, 64, 0, 2, float("nan")) == INV
+    assert _err(L, P, P, 0, 0, 0, 0, 4, 64, 64, 64, 0, 1) == UNS            # fp16 parameters of bf16 rows
+    assert _err(L, P, P, 0, 0, 0, 0, 4, 16385, 16385, 16385) == UNS
+    assert W(-1, 64) == 0 and W(4, 0) == 0 and W(4, 16385) == 0
+    assert W(0, 64) >= 256 and W(28196, 5376) >= 2 * 5376 * 4 and W(10 ** 9, 5376) == W(10 ** 6, 5376)
+    ok = [P, P, P, P, 0, P, P, P, P, 4, 64, 64, 64, 64]
+    for i in (0, 1, 2, 3, 5, 8):
+        a = list(ok)
+        a[i] = 0
+        assert _err(B, *a) == INV
+    assert _err(B, *(ok[:8] + [P + 128] + ok[9:])) == INV                    # workspace not 256-byte aligned
+    for i in (11, 12, 13):
+        a = list(ok)
+        a[i] = 63
+        assert _err(B, *a) == INV
+    assert _err(B, *ok, 0, 1) == UNS
+
+
+def test_adaln_backward():
+    B, W = h3.h3_adaln_modulate_backward, h3.h3_adaln_backward_workspace_bytes
+    assert W(4, 60, 3) == 0 and W(4, 8200, 3) == 0 and W(4, 64, 0) == 0 and W(4, 64, 8193) == 0 and W(-1, 64, 3) == 0
+    assert W(1 << 31, 64, 3) == 0 and W(0, 64, 3) > 0
+    ok = [P, P, P, P, P, P, P, P, 3, 4, 64, 64, 64, 64]
+    for i in range(8):
+        a = list(ok)
+        a[i] = 0
+        assert _err(B, *a) == INV
+    for i, v, want in ((8, 0, INV), (8, 8193, UNS), (9, -1, INV), (9, 1 << 31, INV), (10, 60, UNS), (10, 4, INV),
+                       (10, 8200, UNS), (11, 56, INV), (12, 56, INV), (13, 56, INV), (11, 68, UNS), (12, 68, UNS),
+                       (13, 68, UNS), (0, P + 8, UNS), (1, P + 8, UNS), (4, P + 8, UNS), (5, P + 8, UNS),
+                       (7, P + 128, INV)):
+        a = list(ok)
+        a[i] = v
+        assert _err(B, *a) == want, (i, v)
+    assert _err(B, *ok, -1.0) == INV
