@@ -379,6 +379,39 @@ h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v,
                               const int32_t* d_ranges, const h3_attn_shape* shape, int64_t q_stride,
                               int64_t k_stride, int64_t v_stride, int64_t o_stride, void* stream);
 
+/* Row strides, in elements, of the tensors of h3_masked_attention_backward (each
+ * batch stride is the rows times it). */
+typedef struct {
+  int64_t q, k, v, o, dout, dq, dk, dv;
+} h3_attn_strides;
+
+/*
+ * h3_masked_attention_backward -- gradients of h3_masked_attention for the
+ * gradient dO of its output:
+ *   D_i = dO_i.O_i,  dS_ij = P_ij (dO_i.V_j - D_i),  dV_j = sum_i P_ij dO_i,
+ *   dQ_i = scale sum_j dS_ij K_j,  dK_j = scale sum_i dS_ij Q_i,
+ * the query heads of a K/V head added up in its dK and dV.
+ *
+ *   d_do, d_dq         device bf16, shaped as d_q
+ *   d_dk, d_dv         device bf16, shaped as d_k
+ *   d_o, d_lse         the forward call's results; others as there
+ *   d_work             h3_masked_attention_backward_workspace_bytes() bytes,
+ *                      256-byte aligned, contents undefined before and after; calls
+ *                      that may overlap in time need their own
+ * Every row of the outputs is written: queries with an empty interval and keys
+ * that no row sees get 0.  What lies outside a row's interval changes no gradient
+ * through it, inf and NaN included.
+ * Arithmetic: bf16 tensor-core products with fp32 accumulation, P and dS rounded
+ * to bf16 as operands, P and dS themselves fp32, outputs rounded to bf16; the
+ * same values on every run.  Bounded waits as h3_packed_attention.
+ * Errors: as h3_masked_attention; H3_ERR_INVALID_ARG for a missing workspace.
+ */
+uint64_t h3_masked_attention_backward_workspace_bytes(const h3_attn_shape* shape);
+h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const void* d_k, const void* d_v,
+                                       const void* d_o, const float* d_lse, const int32_t* d_ranges, void* d_dq,
+                                       void* d_dk, void* d_dv, void* d_work, const h3_attn_shape* shape,
+                                       const h3_attn_strides* strides, void* stream);
+
 /*
  * h3_layernorm -- y = xhat * weight + bias, xhat = (x - mean(x)) * rstd,
  * rstd = 1 / sqrt(var(x) + eps) (biased variance), per row.

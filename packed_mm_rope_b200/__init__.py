@@ -28,7 +28,8 @@ from ._lib import (H3Error, H3_OK, H3_ERR_INVALID_ARG, H3_ERR_UNSUPPORTED, H3_ER
                    h3_set_wait_limit_ns, rope_cfg, status_str,
                    h3_adaln_backward_workspace_bytes, h3_adaln_modulate_backward, h3_attn_shape,
                    h3_build_key_ranges, h3_layernorm, h3_layernorm_backward, h3_layernorm_backward_workspace_bytes,
-                   h3_masked_attention, h3_mmrope_rotate)
+                   h3_attn_strides, h3_masked_attention, h3_masked_attention_backward,
+                   h3_masked_attention_backward_workspace_bytes, h3_mmrope_rotate)
 
 load = _lib.load
 
@@ -384,6 +385,36 @@ def masked_attention(q, k, v, key_ranges, out=None, lse=None, softmax_scale: flo
     h3_masked_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, key_ranges.data_ptr(), shape,
                         qs, ks, vs, os_, _stream(stream))
     return out
+
+
+def masked_attention_backward(dout, q, k, v, out, lse, key_ranges, dq=None, dk=None, dv=None,
+                              softmax_scale: float = 0.0, workspace=None, stream=None):
+    """(dq, dk, dv) of ``masked_attention`` for the gradient ``dout`` of its output.
+
+    out, lse: what the forward call gave for the same q, k, v, key_ranges and scale.  workspace: uint8,
+    ``h3_masked_attention_backward_workspace_bytes`` bytes, one per call that may overlap in time.
+    """
+    import torch
+    shape, qs, ks, vs = _masked_shape(q, k, v, key_ranges, softmax_scale)
+    with _allocate_on(stream):
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+        dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
+    strides = {"q": qs, "k": ks, "v": vs}
+    for name, t, n, h in (("o", out, shape.n_q, shape.n_heads), ("dout", dout, shape.n_q, shape.n_heads),
+                          ("dq", dq, shape.n_q, shape.n_heads), ("dk", dk, shape.n_k, shape.n_kv_heads),
+                          ("dv", dv, shape.n_k, shape.n_kv_heads)):
+        b, rows, heads, strides[name] = _row_layout(t)
+        if (b, rows, heads) != (shape.batch, n, h):
+            raise ValueError(f"{name} must be shaped as the tensor it belongs to")
+    if lse.dtype != torch.float32 or lse.numel() != shape.batch * shape.n_heads * shape.n_q or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [B, H, Nq]")
+    _on_device(lse, "lse")
+    workspace = _workspace(workspace, h3_masked_attention_backward_workspace_bytes(shape), q.device, stream)
+    h3_masked_attention_backward(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                 lse.data_ptr(), key_ranges.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                 workspace.data_ptr(), shape, h3_attn_strides(**strides), _stream(stream))
+    return dq, dk, dv
 
 
 def _dtype_code(t, what: str) -> int:

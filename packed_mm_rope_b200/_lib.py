@@ -24,6 +24,7 @@ EXPORTED = ("h3_status_str", "h3_version", "h3_build_coords", "h3_mmrope_qk", "h
             "h3_host_workspace_bytes", "h3_packed_mmrope_attention_host",
             "h3_packed_mmrope_attention_host_noalloc", "h3_adaln_modulate", "h3_init", "h3_shutdown",
             "h3_mmrope_rotate", "h3_build_key_ranges", "h3_masked_attention",
+            "h3_masked_attention_backward_workspace_bytes", "h3_masked_attention_backward",
             "h3_layernorm", "h3_layernorm_backward_workspace_bytes", "h3_layernorm_backward",
             "h3_adaln_backward_workspace_bytes", "h3_adaln_modulate_backward")
 H3_DTYPE_BF16, H3_DTYPE_F16, H3_DTYPE_F32 = 0, 1, 2
@@ -45,6 +46,10 @@ class h3_attn_shape(ctypes.Structure):
     _fields_ = [("n_q", ctypes.c_int64), ("n_k", ctypes.c_int64), ("batch", ctypes.c_int32),
                 ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("softmax_scale", ctypes.c_float)]
+
+
+class h3_attn_strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")]
 
 
 class H3Error(RuntimeError):
@@ -104,6 +109,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.h3_build_key_ranges.argtypes = [P, P, I32, I64, I32, P, P]
     lib.h3_masked_attention.restype = I32
     lib.h3_masked_attention.argtypes = [P, P, P, P, P, P, ctypes.POINTER(h3_attn_shape), I64, I64, I64, I64, P]
+    lib.h3_masked_attention_backward_workspace_bytes.restype = U64
+    lib.h3_masked_attention_backward_workspace_bytes.argtypes = [ctypes.POINTER(h3_attn_shape)]
+    lib.h3_masked_attention_backward.restype = I32
+    lib.h3_masked_attention_backward.argtypes = [P] * 11 + [ctypes.POINTER(h3_attn_shape),
+                                                            ctypes.POINTER(h3_attn_strides), P]
     lib.h3_layernorm.restype = I32
     lib.h3_layernorm.argtypes = [P, P, P, P, P, P, I64, I32, I64, I64, I32, I32, F32, P]
     lib.h3_layernorm_backward_workspace_bytes.restype = U64
@@ -218,6 +228,19 @@ def h3_masked_attention(d_q: int, d_k: int, d_v: int, d_o: int, d_lse: int, d_ra
     _check(load().h3_masked_attention(d_q or None, d_k or None, d_v or None, d_o or None, d_lse or None,
                                       d_ranges or None, ctypes.byref(shape), q_stride, k_stride, v_stride, o_stride,
                                       stream or None), "h3_masked_attention")
+
+
+def h3_masked_attention_backward_workspace_bytes(shape: h3_attn_shape) -> int:
+    return int(load().h3_masked_attention_backward_workspace_bytes(ctypes.byref(shape)))
+
+
+def h3_masked_attention_backward(d_do: int, d_q: int, d_k: int, d_v: int, d_o: int, d_lse: int, d_ranges: int,
+                                 d_dq: int, d_dk: int, d_dv: int, d_work: int, shape: h3_attn_shape,
+                                 strides: h3_attn_strides, stream: int = 0) -> None:
+    _check(load().h3_masked_attention_backward(d_do or None, d_q or None, d_k or None, d_v or None, d_o or None,
+                                               d_lse or None, d_ranges or None, d_dq or None, d_dk or None,
+                                               d_dv or None, d_work or None, ctypes.byref(shape),
+                                               ctypes.byref(strides), stream or None), "h3_masked_attention_backward")
 
 
 def h3_layernorm(d_x: int, d_y: int, d_weight: int, d_bias: int, d_mean: int, d_rstd: int, n_rows: int, hidden: int,

@@ -1,0 +1,733 @@
+// attention_bwd.cuh -- gradients of the masked attention (sm_100a).
+//
+// With P_ij = exp(scale q_i.k_j - lse_i) for the keys that row i sees (else 0)
+// and D_i = dO_i . O_i:
+//   dV_j = sum_i P_ij dO_i         dP_ij = dO_i . v_j    dS_ij = P_ij (dP_ij - D_i)
+//   dQ_i = scale sum_j dS_ij k_j   dK_j  = scale sum_i dS_ij q_i
+// and the query heads that share a K/V head add up in its dK and dV.
+//
+// Three kernels.  `prep` forms D (one pass over O and dO) and lays the rows'
+// (lse, D), intervals and their hulls per 128-row tile out in the workspace,
+// padded to whole tiles.  `dkdv` owns 128 keys of a K/V head and walks the query
+// tiles that see them, over all heads of the group; `dq` owns 128 query rows of
+// a head and walks their key tiles.  Both recompute S and dP, 7 products of
+// 128 x 128 x 128 per pair of tiles where a single kernel would need 5: the price
+// of sums that stay in tensor memory, need no atomics and come out the same on
+// every run.
+//
+// dkdv works on S^T = K Q^T and dP^T = V dO^T (keys on the 128 TMEM lanes), so
+// that P^T and dS^T are, rounded to bf16 in place, the A operands of
+// dV += P^T dO and dK += dS^T Q straight from tensor memory; dq works on S and dP
+// (queries on the lanes) for dQ += dS K alike.  The four or three 128-column fp32
+// accumulators fill tensor memory (512 columns).  P and dS are rounded to bf16 as
+// MMA operands; every sum is fp32.
+//
+// Warps 0-15 do the element-wise part, warp w on the 16 lanes
+// 32 (w % 4) + 16 ((w / 4) % 2) and the columns 64 (w / 8): with the 16x256b shape
+// thread (t0 = lane % 4, t1 = lane / 4) holds lanes t1, t1 + 8 and columns
+// 8 r + 2 t0, + 1.  Warp 16 loads by TMA, warp 17 issues the MMAs.  The issuing
+// thread orders its work so that the tensor core runs two products while the
+// other warps run one element-wise phase:
+//   dkdv: .. dV(i) S(i+1) | dK(i) dP(i+1) ..   against   dS(i) | P(i+1)
+//   dq:   S(j+1) | dP(j+1) dQ(j)               against   dS(j) | P(j+1)
+//
+// Masked places (see attention.cuh): P and dS are set to 0 there by the rows'
+// intervals, never by a product, and the tiles that are B operands of a product
+// with such zeros (dO and Q in dkdv, K in dq) are freed of inf and NaN first; a
+// pair that is seen and touches such a row gets a NaN instead.
+#pragma once
+
+#include "attention.cuh"
+
+namespace h3 {
+namespace attn_bwd {
+
+using attn::BM;
+using attn::BN;
+using attn::HD;
+using attn::HALF_BYTES;
+using attn::IDESC_O;
+using attn::IDESC_S;
+using attn::TILE_BYTES;
+using attn::clean_rows;
+using attn::mma_wait;
+using attn::warp_wait;
+
+constexpr int WARPS = 16;                     // element-wise warps
+constexpr int W_PROD = WARPS;
+constexpr int W_MMA = WARPS + 1;
+constexpr int THREADS = 32 * (WARPS + 2);
+
+struct Params {
+  int n_q, n_k, n_heads, group, n_qt;         // n_qt: query tiles of 128 rows
+  float scale, scale_log2;
+  const float2* stat;                         // [B][H][n_qt * 128] (lse log2 e, D)
+  const int2* rng;                            // [B][n_qt * 128] intervals, (0, 0) past the end
+  const int4* hull;                           // [B][n_qt] (min lo, max hi, max lo, min hi)
+  __nv_bfloat16 *dq, *dk, *dv;
+  long long dq_stride, dk_stride, dv_stride;  // row strides, elements
+  unsigned long long wait_limit_ns, drain_limit_ns;
+  int err_slot;
+};
+
+// ------------------------------------------------------------------ prep ----
+
+// One block per (query tile, head, batch): 16 lanes per row, 16 rows at a time.
+// Blocks of head 0 also write the tile's intervals and hull.  Bound by the
+// reads of O and dO.
+__global__ void __launch_bounds__(256) prep_kernel(const __nv_bfloat16* __restrict__ o,
+                                                   const __nv_bfloat16* __restrict__ dout,
+                                                   const float* __restrict__ lse, const int2* __restrict__ ranges,
+                                                   int n_q, int n_k, int n_heads, int n_qt, long long o_stride,
+                                                   long long do_stride, float2* __restrict__ stat,
+                                                   int2* __restrict__ rng, int4* __restrict__ hull) {
+  const int tile = blockIdx.x, head = blockIdx.y, batch = blockIdx.z;
+  const int sub = threadIdx.x & 15;
+  const long long bh = static_cast<long long>(batch) * n_heads + head;
+#pragma unroll
+  for (int it = 0; it < BM / 16; ++it) {
+    const int row = tile * BM + it * 16 + (threadIdx.x >> 4);
+    float d = 0.f;
+    if (row < n_q) {
+      const long long r = static_cast<long long>(batch) * n_q + row;
+      const uint4 a = *reinterpret_cast<const uint4*>(o + r * o_stride + head * HD + 8 * sub);
+      const uint4 b = *reinterpret_cast<const uint4*>(dout + r * do_stride + head * HD + 8 * sub);
+      const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+      float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        s = __ffma2_rn(make_float2(__uint_as_float(wa[m] << 16), __uint_as_float(wa[m] & 0xffff0000u)),
+                       make_float2(__uint_as_float(wb[m] << 16), __uint_as_float(wb[m] & 0xffff0000u)), s);
+      d = s.x + s.y;
+    }
+#pragma unroll
+    for (int k = 8; k > 0; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
+    if (sub == 0) {
+      float l = row < n_q ? lse[bh * n_q + row] : 0.f;
+      l = l == -INFINITY ? 0.f : l * 1.4426950408889634f;   // rows without keys are masked everywhere
+      stat[bh * n_qt * BM + row] = make_float2(l, d);
+    }
+  }
+  if (head == 0) {
+    __shared__ int part[4][4];
+    if (threadIdx.x < BM) {
+      const int row = tile * BM + threadIdx.x;
+      const int2 r = row < n_q ? attn::clamp_range(ranges[static_cast<long long>(batch) * n_q + row], n_k)
+                               : make_int2(0, 0);
+      rng[(static_cast<long long>(batch) * n_qt + tile) * BM + threadIdx.x] = r;
+      const bool some = r.x < r.y;
+      const int lo = __reduce_min_sync(0xffffffffu, some ? r.x : 0x7fffffff);
+      const int hi = __reduce_max_sync(0xffffffffu, some ? r.y : 0);
+      const int all_lo = __reduce_max_sync(0xffffffffu, r.x), all_hi = __reduce_min_sync(0xffffffffu, r.y);
+      if ((threadIdx.x & 31) == 0) {
+        int* p = part[threadIdx.x >> 5];
+        p[0] = lo;
+        p[1] = hi;
+        p[2] = all_lo;
+        p[3] = all_hi;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int4 h = make_int4(0x7fffffff, 0, 0, 0x7fffffff);
+      for (int q = 0; q < 4; ++q) {
+        h.x = min(h.x, part[q][0]);
+        h.y = max(h.y, part[q][1]);
+        h.z = max(h.z, part[q][2]);
+        h.w = min(h.w, part[q][3]);
+      }
+      hull[static_cast<long long>(batch) * n_qt + tile] = h;
+    }
+  }
+}
+
+// --------------------------------------------------------------- helpers ----
+
+// Untiled bulk copy of `bytes` (a multiple of 16) global -> shared.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, int row,
+                                          int batch) {
+  tma_load_3d(dst, map, bar, col, row, batch);
+  tma_load_3d(dst + HALF_BYTES, map, bar, col + 64, row, batch);
+}
+
+// D = A B^T of two K-major 128 x 128 tiles in shared memory.
+__device__ __forceinline__ void issue_abt(uint32_t d, uint32_t a, uint32_t b) {
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    const uint32_t off = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
+    mma_ss(d, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), IDESC_S, kk > 0 ? 1u : 0u);
+  }
+}
+
+// D += A B: A in tensor memory (bf16 pairs: 64 of the 128 K values in columns
+// 0-31, the others in 64-95), B a 128 x 128 tile in shared memory, MN-major.
+__device__ __forceinline__ void issue_ab(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, smem_desc_sw128(b + kk * 2048, HALF_BYTES, 1024), IDESC_O,
+           (accumulate || kk > 0) ? 1u : 0u);
+}
+
+// This warp's 16 lanes x 64 columns of an accumulator, times `scale`, rounded to
+// bf16 rows `row_a`, `row_a + 8` (< n_rows) of an output at `out`.
+__device__ __forceinline__ void store_tile(uint32_t taddr, float scale, __nv_bfloat16* out, long long stride,
+                                           int row_a, int n_rows, int t0) {
+  uint32_t v[32];
+  __syncwarp();
+  tmem_ld16x256(taddr, v);
+  tmem_wait_ld(v);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const int col = 8 * r + 2 * t0;
+    if (row_a < n_rows)
+      *reinterpret_cast<uint32_t*>(out + row_a * stride + col) =
+          pack_bf16x2(__uint_as_float(v[4 * r]) * scale, __uint_as_float(v[4 * r + 1]) * scale);
+    if (row_a + 8 < n_rows)
+      *reinterpret_cast<uint32_t*>(out + (row_a + 8) * stride + col) =
+          pack_bf16x2(__uint_as_float(v[4 * r + 2]) * scale, __uint_as_float(v[4 * r + 3]) * scale);
+  }
+}
+
+// Rounded values of this warp's 16 x 64 piece -> tensor memory, then one arrival.
+__device__ __forceinline__ void publish(uint32_t taddr, const uint32_t (&pk)[16], uint32_t bar, int lane) {
+  __syncwarp();
+  tmem_st16x128(taddr, pk);
+  tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ uint32_t bit_of(uint32_t lo, uint32_t hi, int k) { return (k < 32 ? lo : hi) >> (k & 31) & 1u; }
+
+// ------------------------------------------------------------------ dkdv ----
+
+namespace dkdv {
+constexpr uint32_t SMEM_K = 0, SMEM_V = TILE_BYTES;
+constexpr uint32_t SMEM_Q = 2 * TILE_BYTES, SMEM_DO = 4 * TILE_BYTES;   // two slots each
+constexpr uint32_t SMEM_STAT = 6 * TILE_BYTES;                          // two slots of 128 (lse, D)
+constexpr uint32_t SMEM_RNG = SMEM_STAT + 2 * 1024;                     // two slots of 128 intervals
+constexpr uint32_t SMEM_BAR = SMEM_RNG + 2 * 1024;
+// barriers: kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], s_full, p_full, dp_full,
+//           ds_full, clean, out_full, mma_done
+constexpr int NUM_BARS = 16;
+constexpr uint32_t SMEM_MISC = SMEM_BAR + NUM_BARS * 8;                 // key sets [2], tmem base, abort, first, last
+constexpr uint32_t SMEM_BYTES = SMEM_MISC + 48 + 1024;
+constexpr uint32_t TMEM_S = 0, TMEM_DP = 128, TMEM_DV = 256, TMEM_DK = 384;
+}  // namespace dkdv
+
+// One CTA per (128 keys, K/V head, batch).
+__global__ void __launch_bounds__(THREADS, 1)
+dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const Params p) {
+  using namespace dkdv;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  const uint32_t bar0 = base + SMEM_BAR;
+  const uint32_t bar_kv = bar0;
+  auto bar_q_full = [&](int s) { return bar0 + 8u * (1 + s); };
+  auto bar_q_empty = [&](int s) { return bar0 + 8u * (3 + s); };
+  auto bar_do_full = [&](int s) { return bar0 + 8u * (5 + s); };
+  auto bar_do_empty = [&](int s) { return bar0 + 8u * (7 + s); };
+  const uint32_t bar_s = bar0 + 72u, bar_p = bar0 + 80u, bar_dp = bar0 + 88u, bar_ds = bar0 + 96u;
+  const uint32_t bar_clean = bar0 + 104u, bar_out = bar0 + 112u, bar_done = bar0 + 120u;
+  uint4* const unclean = reinterpret_cast<uint4*>(gbase + SMEM_MISC);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC + 32);
+  volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 36);
+  int* const span = reinterpret_cast<int*>(gbase + SMEM_MISC + 40);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int k0 = blockIdx.x * BN, kvh = blockIdx.y, batch = blockIdx.z;
+  const uint64_t limit = p.wait_limit_ns;
+  const int eslot = p.err_slot;
+  const int4* const hulls = p.hull + static_cast<long long>(batch) * p.n_qt;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NUM_BARS; ++i) mbar_init(bar0 + 8u * i, i == 10 || i == 12 || i == 13 ? WARPS : 1);
+    span[0] = 0x7fffffff;
+    span[1] = -1;
+    *abort_flag = 0u;
+    mbar_fence_init();
+  }
+  __syncthreads();
+  // the query tiles, first to last, with a row that sees one of these keys
+  {
+    int first = 0x7fffffff, last = -1;
+    for (int i = threadIdx.x; i < p.n_qt; i += THREADS) {
+      const int4 h = hulls[i];
+      if (h.x < k0 + BN && h.y > k0) {
+        first = min(first, i);
+        last = i;
+      }
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0 && last >= 0) {
+      atomicMin(&span[0], first);
+      atomicMax(&span[1], last);
+    }
+  }
+  __syncthreads();
+  const int qt0 = span[0], nt = span[1] - span[0] + 1;
+  if (span[1] < 0) {                             // no row sees these keys
+    for (int i = threadIdx.x; i < BN * (HD / 8); i += THREADS) {
+      const int key = k0 + i / (HD / 8), col = kvh * HD + 8 * (i % (HD / 8));
+      if (key < p.n_k) {
+        const long long r = static_cast<long long>(batch) * p.n_k + key;
+        *reinterpret_cast<uint4*>(p.dk + r * p.dk_stride + col) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(p.dv + r * p.dv_stride + col) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    return;
+  }
+  const int iters = nt * p.group;
+  if (warp == W_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == W_PROD) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar_kv, 2 * TILE_BYTES);
+      load_tile(base + SMEM_K, &tm_k, bar_kv, kvh * HD, k0, batch);
+      load_tile(base + SMEM_V, &tm_v, bar_kv, kvh * HD, k0, batch);
+      int issued_q = 0, issued_do = 0, qt = qt0, head = kvh * p.group;
+      for (int it = 0; it < iters; ++it) {
+        const int s = it & 1;
+        const uint32_t par = ((it >> 1) - 1) & 1;
+        // dO's slot frees first (after dV), Q's with dK
+        if (it > 1 && !mbar_wait_bounded(bar_do_empty(s), par, abort_flag, limit, eslot)) break;
+        mbar_arrive_expect_tx(bar_do_full(s), TILE_BYTES);
+        load_tile(base + SMEM_DO + s * TILE_BYTES, &tm_do, bar_do_full(s), head * HD, qt * BM, batch);
+        issued_do = it + 1;
+        if (it > 1 && !mbar_wait_bounded(bar_q_empty(s), par, abort_flag, limit, eslot)) break;
+        mbar_arrive_expect_tx(bar_q_full(s), TILE_BYTES + 2048);
+        load_tile(base + SMEM_Q + s * TILE_BYTES, &tm_q, bar_q_full(s), head * HD, qt * BM, batch);
+        bulk_load(base + SMEM_STAT + s * 1024,
+                  p.stat + ((static_cast<long long>(batch) * p.n_heads + head) * p.n_qt + qt) * BM, 1024, bar_q_full(s));
+        bulk_load(base + SMEM_RNG + s * 1024, p.rng + (static_cast<long long>(batch) * p.n_qt + qt) * BM, 1024,
+                  bar_q_full(s));
+        issued_q = it + 1;
+        if (++qt == qt0 + nt) qt = qt0, ++head;
+      }
+      // every load that was started lands before the CTA ends
+      volatile uint32_t never = 0u;
+      mbar_wait_bounded(bar_kv, 0, &never, p.drain_limit_ns, eslot);
+      for (int it = max(issued_q - 2, 0); it < issued_q; ++it)
+        mbar_wait_bounded(bar_q_full(it & 1), (it >> 1) & 1, &never, p.drain_limit_ns, eslot);
+      for (int it = max(issued_do - 2, 0); it < issued_do; ++it)
+        mbar_wait_bounded(bar_do_full(it & 1), (it >> 1) & 1, &never, p.drain_limit_ns, eslot);
+    }
+  } else if (warp == W_MMA) {
+    if (lane == 0) {
+      auto q_tile = [&](int s) { return base + SMEM_Q + s * TILE_BYTES; };
+      auto do_tile = [&](int s) { return base + SMEM_DO + s * TILE_BYTES; };
+      bool ok = mma_wait(bar_kv, 0, abort_flag, limit, eslot) &&
+                mma_wait(bar_q_full(0), 0, abort_flag, limit, eslot);
+      if (ok) {
+        tc_fence_after();
+        issue_abt(tmem + TMEM_S, base + SMEM_K, q_tile(0));
+        tc_commit(bar_s);
+        ok = mma_wait(bar_do_full(0), 0, abort_flag, limit, eslot);
+      }
+      if (ok) {
+        tc_fence_after();
+        issue_abt(tmem + TMEM_DP, base + SMEM_V, do_tile(0));
+        tc_commit(bar_dp);
+      }
+      for (int it = 0; ok && it < iters; ++it) {
+        const int s = it & 1, sn = s ^ 1;
+        const uint32_t par = it & 1, par_next = ((it + 1) >> 1) & 1;
+        const bool more = it + 1 < iters;
+        // dV(i) and, into the S columns it has just read P from, S(i + 1)
+        if (more ? !mbar_spin2_bounded(bar_p, par, bar_q_full(sn), par_next, abort_flag, limit, eslot)
+                 : !mma_wait(bar_p, par, abort_flag, limit, eslot))
+          break;
+        tc_fence_after();
+        issue_ab(tmem + TMEM_DV, tmem + TMEM_S, do_tile(s), it > 0);
+        tc_commit(bar_do_empty(s));
+        if (more) {
+          issue_abt(tmem + TMEM_S, base + SMEM_K, q_tile(sn));
+          tc_commit(bar_s);
+        }
+        // dK(i) and dP(i + 1)
+        if (more ? !mbar_spin2_bounded(bar_ds, par, bar_do_full(sn), par_next, abort_flag, limit, eslot)
+                 : !mma_wait(bar_ds, par, abort_flag, limit, eslot))
+          break;
+        tc_fence_after();
+        issue_ab(tmem + TMEM_DK, tmem + TMEM_DP, q_tile(s), it > 0);
+        tc_commit(bar_q_empty(s));
+        if (more) {
+          issue_abt(tmem + TMEM_DP, base + SMEM_V, do_tile(sn));
+          tc_commit(bar_dp);
+        } else {
+          tc_commit(bar_out);
+        }
+      }
+      tc_commit(bar_done);
+      volatile uint32_t never = 0u;
+      mma_wait(bar_done, 0, &never, p.drain_limit_ns, eslot);
+    }
+  } else {
+    const int t0 = lane & 3, t1 = lane >> 2;
+    const int lane16 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
+    const int half = warp >> 3;                    // queries 64 half .. 64 half + 63 of the tile
+    const uint32_t lb = static_cast<uint32_t>(lane16) << 16;
+    const uint32_t t_s = tmem + lb + TMEM_S + 64 * half, t_dp = tmem + lb + TMEM_DP + 64 * half;
+    const int key_a = k0 + lane16 + t1, key_b = key_a + 8;
+    const float sl2 = p.scale_log2;
+    bool ok = true;
+    int cleaned = 0;
+    int qt = qt0;
+    for (int it = 0; ok && it < iters; ++it) {
+      const int s = it & 1;
+      const int4 h = hulls[qt];
+      if (++qt == qt0 + nt) qt = qt0;
+      const bool partial = h.z > k0 || h.w < k0 + BN;   // some row does not see all of these keys
+      // this thread's query columns: (lse, D) and intervals of two queries at a time
+      const float4* const stat = reinterpret_cast<const float4*>(gbase + SMEM_STAT + s * 1024 + half * 512) + t0;
+      const int4* const rng = reinterpret_cast<const int4*>(gbase + SMEM_RNG + s * 1024 + half * 512) + t0;
+      uint4 bad = make_uint4(0u, 0u, 0u, 0u);
+      if (!warp_wait(bar_q_full(s), (it >> 1) & 1, abort_flag, limit, eslot) ||
+          !warp_wait(bar_s, it & 1, abort_flag, limit, eslot)) { ok = false; break; }
+      if (partial) {
+        // S(i) and dP(i) have read Q and dO; dV and dK wait for P and dS, hence for this
+        if (!warp_wait(bar_do_full(s), (it >> 1) & 1, abort_flag, limit, eslot) ||
+            !warp_wait(bar_dp, it & 1, abort_flag, limit, eslot)) { ok = false; break; }
+        const uint32_t rows = clean_rows(gbase + SMEM_Q + s * TILE_BYTES, warp, lane) |
+                              clean_rows(gbase + SMEM_DO + s * TILE_BYTES, warp, lane);
+        if (rows != 0u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (lane == 0) reinterpret_cast<volatile uint8_t*>(&unclean[cleaned & 1])[warp] = static_cast<uint8_t>(rows);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_clean);
+        if (!warp_wait(bar_clean, cleaned & 1, abort_flag, limit, eslot)) { ok = false; break; }
+        bad = unclean[cleaned & 1];
+        ++cleaned;
+      }
+      const uint32_t bad_lo = half ? bad.z : bad.x, bad_hi = half ? bad.w : bad.y;
+      tc_fence_after();
+      uint32_t sr[32];
+      tmem_ld16x256(t_s, sr);
+      tmem_wait_ld(sr);
+      float x[32];                                  // P^T: registers as loaded (4 r: key a, 4 r + 2: key b)
+      const float2 c2 = make_float2(sl2, sl2);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float4 st = stat[4 * r];
+        const float2 ml = make_float2(-st.x, -st.z);
+        const float2 ya = __ffma2_rn(make_float2(__uint_as_float(sr[4 * r]), __uint_as_float(sr[4 * r + 1])), c2, ml);
+        const float2 yb = __ffma2_rn(make_float2(__uint_as_float(sr[4 * r + 2]), __uint_as_float(sr[4 * r + 3])), c2, ml);
+        x[4 * r] = ex2_approx(ya.x);
+        x[4 * r + 1] = ex2_approx(ya.y);
+        x[4 * r + 2] = ex2_approx(yb.x);
+        x[4 * r + 3] = ex2_approx(yb.y);
+      }
+      if (partial) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int4 g = rng[4 * r];
+          const bool b0 = bit_of(bad_lo, bad_hi, 8 * r + 2 * t0), b1 = bit_of(bad_lo, bad_hi, 8 * r + 2 * t0 + 1);
+          auto masked = [](float v, int key, int lo, int hi, bool b) {
+            return key < lo || key >= hi ? 0.f : b ? __int_as_float(0x7fc00000) : v;
+          };
+          x[4 * r] = masked(x[4 * r], key_a, g.x, g.y, b0);
+          x[4 * r + 1] = masked(x[4 * r + 1], key_a, g.z, g.w, b1);
+          x[4 * r + 2] = masked(x[4 * r + 2], key_b, g.x, g.y, b0);
+          x[4 * r + 3] = masked(x[4 * r + 3], key_b, g.z, g.w, b1);
+        }
+      }
+      uint32_t pk[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) pk[r] = pack_bf16x2(x[2 * r], x[2 * r + 1]);
+      publish(t_s, pk, bar_p, lane);
+      if (!warp_wait(bar_dp, it & 1, abort_flag, limit, eslot)) { ok = false; break; }
+      tc_fence_after();
+      tmem_ld16x256(t_dp, sr);
+      tmem_wait_ld(sr);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float4 st = stat[4 * r];
+        const float2 md = make_float2(-st.y, -st.w);
+        const float2 da = __fmul2_rn(
+            make_float2(x[4 * r], x[4 * r + 1]),
+            __fadd2_rn(make_float2(__uint_as_float(sr[4 * r]), __uint_as_float(sr[4 * r + 1])), md));
+        const float2 db = __fmul2_rn(
+            make_float2(x[4 * r + 2], x[4 * r + 3]),
+            __fadd2_rn(make_float2(__uint_as_float(sr[4 * r + 2]), __uint_as_float(sr[4 * r + 3])), md));
+        x[4 * r] = da.x;
+        x[4 * r + 1] = da.y;
+        x[4 * r + 2] = db.x;
+        x[4 * r + 3] = db.y;
+      }
+      if (partial) {                                // 0 times an inf or NaN of a masked pair
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int4 g = rng[4 * r];
+          if (key_a < g.x || key_a >= g.y) x[4 * r] = 0.f;
+          if (key_a < g.z || key_a >= g.w) x[4 * r + 1] = 0.f;
+          if (key_b < g.x || key_b >= g.y) x[4 * r + 2] = 0.f;
+          if (key_b < g.z || key_b >= g.w) x[4 * r + 3] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) pk[r] = pack_bf16x2(x[2 * r], x[2 * r + 1]);
+      publish(t_dp, pk, bar_ds, lane);
+    }
+    if (ok && warp_wait(bar_out, 0, abort_flag, limit, eslot)) {
+      tc_fence_after();
+      const long long r0 = static_cast<long long>(batch) * p.n_k;
+      const int col = kvh * HD + 64 * half;
+      store_tile(tmem + lb + TMEM_DV + 64 * half, 1.f, p.dv + r0 * p.dv_stride + col, p.dv_stride, key_a, p.n_k, t0);
+      store_tile(tmem + lb + TMEM_DK + 64 * half, p.scale, p.dk + r0 * p.dk_stride + col, p.dk_stride, key_a, p.n_k, t0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// -------------------------------------------------------------------- dq ----
+
+namespace dq {
+constexpr int SLOTS = 5;                                         // K and V tiles in turn
+constexpr uint32_t SMEM_Q = 0, SMEM_DO = TILE_BYTES, SMEM_KV = 2 * TILE_BYTES;
+constexpr uint32_t SMEM_BAR = SMEM_KV + SLOTS * TILE_BYTES;
+// barriers: q_full, kv_full[5], kv_empty[5], s_full[2], dp_full, ds_full, clean, out_full, mma_done
+constexpr int NUM_BARS = 1 + 2 * SLOTS + 2 + 5;
+constexpr uint32_t SMEM_MISC = SMEM_BAR + ((NUM_BARS * 8 + 15) & ~15);   // key sets [2], tmem base, abort
+constexpr uint32_t SMEM_BYTES = SMEM_MISC + 48 + 1024;
+constexpr uint32_t TMEM_S = 0, TMEM_DP = 256, TMEM_DQ = 384;     // S in two buffers
+}  // namespace dq
+
+// One CTA per (128 query rows, head, batch), last rows first.
+__global__ void __launch_bounds__(THREADS, 1)
+dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const Params p) {
+  using namespace dq;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - raw);
+  const uint32_t bar0 = base + SMEM_BAR;
+  const uint32_t bar_q = bar0;
+  auto bar_full = [&](int s) { return bar0 + 8u * (1 + s); };
+  auto bar_empty = [&](int s) { return bar0 + 8u * (1 + SLOTS + s); };
+  auto bar_s = [&](int i) { return bar0 + 8u * (1 + 2 * SLOTS + i); };
+  const uint32_t bar_dp = bar0 + 8u * (3 + 2 * SLOTS), bar_ds = bar_dp + 8u, bar_clean = bar_dp + 16u;
+  const uint32_t bar_out = bar_dp + 24u, bar_done = bar_dp + 32u;
+  uint4* const unclean = reinterpret_cast<uint4*>(gbase + SMEM_MISC);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC + 32);
+  volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 36);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qt = gridDim.x - 1 - blockIdx.x, head = blockIdx.y, batch = blockIdx.z;
+  const int q_row0 = qt * BM, kv_col = head / p.group * HD;
+  const uint64_t limit = p.wait_limit_ns;
+  const int eslot = p.err_slot;
+  const int4 hull = p.hull[static_cast<long long>(batch) * p.n_qt + qt];
+  __nv_bfloat16* const out = p.dq + static_cast<long long>(batch) * p.n_q * p.dq_stride + head * HD;
+
+  if (hull.x >= hull.y) {                          // no row of the tile sees a key
+    for (int i = threadIdx.x; i < BM * (HD / 8); i += THREADS) {
+      const int row = q_row0 + i / (HD / 8);
+      if (row < p.n_q)
+        *reinterpret_cast<uint4*>(out + row * p.dq_stride + 8 * (i % (HD / 8))) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    return;
+  }
+  const int tile0 = hull.x / BN, nkv = (hull.y + BN - 1) / BN - tile0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NUM_BARS; ++i)
+      mbar_init(bar0 + 8u * i, i == 4 + 2 * SLOTS || i == 5 + 2 * SLOTS ? WARPS : 1);
+    *abort_flag = 0u;
+    mbar_fence_init();
+  }
+  if (warp == W_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == W_PROD) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar_q, 2 * TILE_BYTES);
+      load_tile(base + SMEM_Q, &tm_q, bar_q, head * HD, q_row0, batch);
+      load_tile(base + SMEM_DO, &tm_do, bar_q, head * HD, q_row0, batch);
+      int issued = 0;
+      for (int idx = 0; idx < 2 * nkv; ++idx) {
+        const int s = idx % SLOTS, use = idx / SLOTS;
+        if (use > 0 && !mbar_wait_bounded(bar_empty(s), (use - 1) & 1, abort_flag, limit, eslot)) break;
+        mbar_arrive_expect_tx(bar_full(s), TILE_BYTES);
+        load_tile(base + SMEM_KV + s * TILE_BYTES, (idx & 1) ? &tm_v : &tm_k, bar_full(s), kv_col,
+                  (tile0 + (idx >> 1)) * BN, batch);
+        issued = idx + 1;
+      }
+      volatile uint32_t never = 0u;
+      mbar_wait_bounded(bar_q, 0, &never, p.drain_limit_ns, eslot);
+      for (int idx = max(issued - SLOTS, 0); idx < issued; ++idx)
+        mbar_wait_bounded(bar_full(idx % SLOTS), (idx / SLOTS) & 1, &never, p.drain_limit_ns, eslot);
+    }
+  } else if (warp == W_MMA) {
+    if (lane == 0) {
+      auto kv_tile = [&](int idx) { return base + SMEM_KV + (idx % SLOTS) * TILE_BYTES; };
+      auto full_wait = [&](int idx) {
+        return mma_wait(bar_full(idx % SLOTS), (idx / SLOTS) & 1, abort_flag, limit, eslot);
+      };
+      bool ok = mma_wait(bar_q, 0, abort_flag, limit, eslot) && full_wait(0);
+      if (ok) {
+        tc_fence_after();
+        issue_abt(tmem + TMEM_S, base + SMEM_Q, kv_tile(0));
+        tc_commit(bar_s(0));
+        ok = full_wait(1);
+      }
+      if (ok) {
+        tc_fence_after();
+        issue_abt(tmem + TMEM_DP, base + SMEM_DO, kv_tile(1));
+        tc_commit(bar_dp);
+        tc_commit(bar_empty(1));
+      }
+      for (int j = 0; ok && j < nkv; ++j) {
+        const bool more = j + 1 < nkv;
+        const int kn = 2 * j + 2, vn = 2 * j + 3;
+        if (more) {
+          if (!full_wait(kn)) break;
+          tc_fence_after();
+          issue_abt(tmem + TMEM_S + 128 * ((j + 1) & 1), base + SMEM_Q, kv_tile(kn));
+          tc_commit(bar_s((j + 1) & 1));
+        }
+        if (more ? !mbar_spin2_bounded(bar_ds, j & 1, bar_full(vn % SLOTS), (vn / SLOTS) & 1, abort_flag, limit, eslot)
+                 : !mma_wait(bar_ds, j & 1, abort_flag, limit, eslot))
+          break;
+        tc_fence_after();
+        if (more) {
+          issue_abt(tmem + TMEM_DP, base + SMEM_DO, kv_tile(vn));
+          tc_commit(bar_dp);
+          tc_commit(bar_empty(vn % SLOTS));
+        }
+        issue_ab(tmem + TMEM_DQ, tmem + TMEM_S + 128 * (j & 1), kv_tile(2 * j), j > 0);
+        tc_commit(more ? bar_empty((2 * j) % SLOTS) : bar_out);
+      }
+      tc_commit(bar_done);
+      volatile uint32_t never = 0u;
+      mma_wait(bar_done, 0, &never, p.drain_limit_ns, eslot);
+    }
+  } else {
+    const int t0 = lane & 3, t1 = lane >> 2;
+    const int lane16 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
+    const int half = warp >> 3;                    // keys 64 half .. 64 half + 63 of the tile
+    const uint32_t lb = static_cast<uint32_t>(lane16) << 16;
+    const uint32_t t_dp = tmem + lb + TMEM_DP + 64 * half;
+    const int ra = lane16 + t1;                    // rows of the tile
+    const long long qp = static_cast<long long>(p.n_qt) * BM;
+    const float2* const stat = p.stat + (static_cast<long long>(batch) * p.n_heads + head) * qp + q_row0 + ra;
+    const int2* const rng = p.rng + batch * qp + q_row0 + ra;
+    const float2 st_a = stat[0], st_b = stat[8];
+    const int2 rng_a = rng[0], rng_b = rng[8];
+    const unsigned len_a = rng_a.y - rng_a.x, len_b = rng_b.y - rng_b.x;
+    const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
+    const float2 la = make_float2(-st_a.x, -st_a.x), lbv = make_float2(-st_b.x, -st_b.x);
+    const float2 da = make_float2(-st_a.y, -st_a.y), db = make_float2(-st_b.y, -st_b.y);
+    bool ok = true;
+    int cleaned = 0;
+    for (int j = 0; ok && j < nkv; ++j) {
+      const int key0 = (tile0 + j) * BN;
+      const bool partial = key0 < hull.z || key0 + BN > hull.w;
+      const uint32_t t_s = tmem + lb + TMEM_S + 128 * (j & 1) + 64 * half;
+      uint4 bad = make_uint4(0u, 0u, 0u, 0u);
+      if (!warp_wait(bar_s(j & 1), (j >> 1) & 1, abort_flag, limit, eslot)) { ok = false; break; }
+      if (partial) {
+        // S(j) has read K(j); dQ(j) waits for dS(j), hence for this
+        const int kidx = 2 * j;
+        if (!warp_wait(bar_full(kidx % SLOTS), (kidx / SLOTS) & 1, abort_flag, limit, eslot)) { ok = false; break; }
+        const uint32_t rows = clean_rows(gbase + SMEM_KV + (kidx % SLOTS) * TILE_BYTES, warp, lane);
+        if (rows != 0u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (lane == 0) reinterpret_cast<volatile uint8_t*>(&unclean[cleaned & 1])[warp] = static_cast<uint8_t>(rows);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_clean);
+        if (!warp_wait(bar_clean, cleaned & 1, abort_flag, limit, eslot)) { ok = false; break; }
+        bad = unclean[cleaned & 1];
+        ++cleaned;
+      }
+      const uint32_t bad_lo = half ? bad.z : bad.x, bad_hi = half ? bad.w : bad.y;
+      tc_fence_after();
+      uint32_t sr[32];
+      tmem_ld16x256(t_s, sr);
+      tmem_wait_ld(sr);
+      float x[32];                                  // P, then dS (4 r: row a, 4 r + 2: row b)
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float2 ya = __ffma2_rn(make_float2(__uint_as_float(sr[4 * r]), __uint_as_float(sr[4 * r + 1])), c2, la);
+        const float2 yb = __ffma2_rn(make_float2(__uint_as_float(sr[4 * r + 2]), __uint_as_float(sr[4 * r + 3])), c2, lbv);
+        x[4 * r] = ex2_approx(ya.x);
+        x[4 * r + 1] = ex2_approx(ya.y);
+        x[4 * r + 2] = ex2_approx(yb.x);
+        x[4 * r + 3] = ex2_approx(yb.y);
+      }
+      if (!warp_wait(bar_dp, j & 1, abort_flag, limit, eslot)) { ok = false; break; }
+      tc_fence_after();
+      tmem_ld16x256(t_dp, sr);
+      tmem_wait_ld(sr);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float2 va = __fmul2_rn(
+            make_float2(x[4 * r], x[4 * r + 1]),
+            __fadd2_rn(make_float2(__uint_as_float(sr[4 * r]), __uint_as_float(sr[4 * r + 1])), da));
+        const float2 vb = __fmul2_rn(
+            make_float2(x[4 * r + 2], x[4 * r + 3]),
+            __fadd2_rn(make_float2(__uint_as_float(sr[4 * r + 2]), __uint_as_float(sr[4 * r + 3])), db));
+        x[4 * r] = va.x;
+        x[4 * r + 1] = va.y;
+        x[4 * r + 2] = vb.x;
+        x[4 * r + 3] = vb.y;
+      }
+      if (partial) {
+        const int off_a = key0 + 64 * half + 2 * t0 - rng_a.x, off_b = key0 + 64 * half + 2 * t0 - rng_b.x;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int k = 8 * (e >> 2) + (e & 1);
+          const bool seen = ((e >> 1) & 1) ? static_cast<unsigned>(off_b + k) < len_b
+                                           : static_cast<unsigned>(off_a + k) < len_a;
+          if (!seen) x[e] = 0.f;
+          else if (bit_of(bad_lo, bad_hi, k + 2 * t0)) x[e] = __int_as_float(0x7fc00000);
+        }
+      }
+      uint32_t pk[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) pk[r] = pack_bf16x2(x[2 * r], x[2 * r + 1]);
+      publish(t_s, pk, bar_ds, lane);
+    }
+    if (ok && warp_wait(bar_out, 0, abort_flag, limit, eslot)) {
+      tc_fence_after();
+      store_tile(tmem + lb + TMEM_DQ + 64 * half, p.scale, out + 64 * half, p.dq_stride, q_row0 + ra, p.n_q, t0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace attn_bwd
+}  // namespace h3

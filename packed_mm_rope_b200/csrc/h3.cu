@@ -17,6 +17,7 @@
 #include "coords.cuh"
 #include "rope.cuh"
 #include "attention.cuh"
+#include "attention_bwd.cuh"
 #include "adaln.cuh"
 #include "norm.cuh"
 #include "ranges.cuh"
@@ -51,7 +52,11 @@ const DeviceState* device_state() {
     if (cudaFuncSetAttribute(h3::attn::attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(h3::attn::SMEM_BYTES)) != cudaSuccess ||
         cudaFuncSetAttribute(h3::attn::attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(h3::attn::SMEM_BYTES)) != cudaSuccess)
+                             static_cast<int>(h3::attn::SMEM_BYTES)) != cudaSuccess ||
+        cudaFuncSetAttribute(h3::attn_bwd::dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(h3::attn_bwd::dkdv::SMEM_BYTES)) != cudaSuccess ||
+        cudaFuncSetAttribute(h3::attn_bwd::dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(h3::attn_bwd::dq::SMEM_BYTES)) != cudaSuccess)
       return nullptr;
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0) st.sms = n;

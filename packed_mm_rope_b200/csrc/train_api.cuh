@@ -132,6 +132,23 @@ h3_status check_attention(const h3_attn_shape* a, std::initializer_list<int64_t>
   return st;
 }
 
+// Workspace of the backward call: (lse, D) per head and row, the rows'
+// intervals, and the hull of every query tile, each row count padded to tiles.
+struct AttentionWork {
+  int n_qt;
+  uint64_t rng, hull, bytes;             // offsets and total size; the (lse, D) pairs come first
+};
+
+AttentionWork attention_work(const h3_attn_shape* a) {
+  AttentionWork w;
+  w.n_qt = static_cast<int>((a->n_q + h3::attn::BM - 1) / h3::attn::BM);
+  const uint64_t rows = static_cast<uint64_t>(w.n_qt) * h3::attn::BM * a->batch;
+  w.rng = up256(rows * a->n_heads * 8u);
+  w.hull = w.rng + up256(rows * 8u);
+  w.bytes = w.hull + up256(static_cast<uint64_t>(w.n_qt) * a->batch * 16u) + 256u;
+  return w;
+}
+
 float attention_scale(const h3_attn_shape* a) {
   return a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / std::sqrt(128.0f);
 }
@@ -188,6 +205,83 @@ h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v,
   const dim3 grid(static_cast<unsigned>((a->n_q + 2 * h3::attn::BM - 1) / (2 * h3::attn::BM)),
                   static_cast<unsigned>(a->n_heads), static_cast<unsigned>(a->batch));
   h3::attn::attention_kernel<true><<<grid, h3::attn::THREADS, h3::attn::SMEM_BYTES, as_stream(stream)>>>(tq, tk, tv, p);
+  return launched();
+}
+
+uint64_t h3_masked_attention_backward_workspace_bytes(const h3_attn_shape* a) {
+  if (check_attention(a, {}, {}) != H3_OK) return 0;
+  return attention_work(a).bytes;
+}
+
+h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const void* d_k, const void* d_v,
+                                       const void* d_o, const float* d_lse, const int32_t* d_ranges, void* d_dq,
+                                       void* d_dk, void* d_dv, void* d_work, const h3_attn_shape* a,
+                                       const h3_attn_strides* st, void* stream) {
+  if (st == nullptr) return H3_ERR_INVALID_ARG;
+  const h3_status check = check_attention(a, {st->dout, st->q, st->o, st->dq}, {st->k, st->v, st->dk, st->dv});
+  if (check != H3_OK) return check;
+  const bool queries = a->n_q > 0, keys = a->n_k > 0;
+  if (queries && (!d_do || !d_q || !d_o || !d_lse || !d_ranges || !d_dq)) return H3_ERR_INVALID_ARG;
+  if (keys && (!d_k || !d_v || !d_dk || !d_dv)) return H3_ERR_INVALID_ARG;
+  if (!d_work || !aligned256(d_work)) return H3_ERR_INVALID_ARG;
+  for (const void* ptr : {d_do, d_q, d_k, d_v, d_o, static_cast<const void*>(d_dq), static_cast<const void*>(d_dk),
+                          static_cast<const void*>(d_dv)})
+    if (!aligned16(ptr)) return H3_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(d_ranges) & 7u) return H3_ERR_UNSUPPORTED;
+  if (!queries && !keys) return H3_OK;
+  cudaStream_t s = as_stream(stream);
+  if (!queries) {                          // no row reads the keys
+    const size_t rows = static_cast<size_t>(a->batch) * a->n_k, width = static_cast<size_t>(a->n_kv_heads) * 256u;
+    return cudaMemset2DAsync(d_dk, static_cast<size_t>(st->dk) * 2u, 0, width, rows, s) == cudaSuccess &&
+                   cudaMemset2DAsync(d_dv, static_cast<size_t>(st->dv) * 2u, 0, width, rows, s) == cudaSuccess
+               ? H3_OK
+               : H3_ERR_CUDA;
+  }
+  CUtensorMap tq, tk, tv, tdo;
+  if (!make_qkv_map(&tq, d_q, a->batch, a->n_q, a->n_heads, st->q, 128) ||
+      !make_qkv_map(&tdo, d_do, a->batch, a->n_q, a->n_heads, st->dout, 128))
+    return H3_ERR_CUDA;
+  tk = tv = tq;                            // without keys every row is empty and K, V are never read
+  if (keys && (!make_qkv_map(&tk, d_k, a->batch, a->n_k, a->n_kv_heads, st->k, 128) ||
+               !make_qkv_map(&tv, d_v, a->batch, a->n_k, a->n_kv_heads, st->v, 128)))
+    return H3_ERR_CUDA;
+  if (device_state() == nullptr) return H3_ERR_CUDA;
+  const AttentionWork w = attention_work(a);
+  uint8_t* base = static_cast<uint8_t*>(d_work);
+  h3::attn_bwd::Params p{};
+  p.n_q = static_cast<int>(a->n_q);
+  p.n_k = static_cast<int>(a->n_k);
+  p.n_heads = a->n_heads;
+  p.group = a->n_heads / a->n_kv_heads;
+  p.n_qt = w.n_qt;
+  p.scale = attention_scale(a);
+  p.scale_log2 = p.scale * 1.4426950408889634f;
+  float2* stat = reinterpret_cast<float2*>(base);
+  int2* rng = reinterpret_cast<int2*>(base + w.rng);
+  int4* hull = reinterpret_cast<int4*>(base + w.hull);
+  p.stat = stat;
+  p.rng = rng;
+  p.hull = hull;
+  p.dq = static_cast<__nv_bfloat16*>(d_dq);
+  p.dk = static_cast<__nv_bfloat16*>(d_dk);
+  p.dv = static_cast<__nv_bfloat16*>(d_dv);
+  p.dq_stride = st->dq;
+  p.dk_stride = st->dk;
+  p.dv_stride = st->dv;
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  p.drain_limit_ns = kDrainLimitNs;
+  p.err_slot = error_slot(stream);
+  const unsigned batch = static_cast<unsigned>(a->batch), heads = static_cast<unsigned>(a->n_heads);
+  h3::attn_bwd::prep_kernel<<<dim3(w.n_qt, heads, batch), 256, 0, s>>>(
+      static_cast<const __nv_bfloat16*>(d_o), static_cast<const __nv_bfloat16*>(d_do), d_lse,
+      reinterpret_cast<const int2*>(d_ranges), p.n_q, p.n_k, p.n_heads, w.n_qt, st->o, st->dout, stat, rng, hull);
+  if (keys) {
+    const unsigned n_kt = static_cast<unsigned>((a->n_k + h3::attn::BN - 1) / h3::attn::BN);
+    h3::attn_bwd::dkdv_kernel<<<dim3(n_kt, static_cast<unsigned>(a->n_kv_heads), batch), h3::attn_bwd::THREADS,
+                                h3::attn_bwd::dkdv::SMEM_BYTES, s>>>(tq, tk, tv, tdo, p);
+  }
+  h3::attn_bwd::dq_kernel<<<dim3(w.n_qt, heads, batch), h3::attn_bwd::THREADS, h3::attn_bwd::dq::SMEM_BYTES, s>>>(
+      tq, tk, tv, tdo, p);
   return launched();
 }
 

@@ -125,3 +125,34 @@ def test_adaln_backward():
         a[i] = v
         assert _err(B, *a) == want, (i, v)
     assert _err(B, *ok, -1.0) == INV
+
+
+def test_masked_attention_backward():
+    B, W = h3.h3_masked_attention_backward, h3.h3_masked_attention_backward_workspace_bytes
+    names = ("q", "k", "v", "o", "dout", "dq", "dk", "dv")
+    ok = dict(q=512, k=256, v=256, o=512, dout=512, dq=512, dk=256, dv=256)
+    S = h3.h3_attn_strides
+    ptrs = [P] * 11
+    assert W(_shape(n_heads=5)) == 0 and W(_shape(head_dim=64)) == 0 and W(_shape(batch=0)) == 0
+    assert W(_shape()) >= 128 * 4 * 8 + 128 * 8 + 16
+    B(*([0] * 10), P, _shape(n_q=0, n_k=0), S(**ok))                          # nothing to do
+    for i in range(11):
+        p = list(ptrs)
+        p[i] = 0
+        assert _err(B, *p, _shape(), S(**ok)) == INV, i
+    for i in (0, 1, 2, 3, 4, 7, 8, 9):
+        p = list(ptrs)
+        p[i] = P + 8
+        assert _err(B, *p, _shape(), S(**ok)) == UNS, i
+    p = list(ptrs)
+    p[10] = P + 128
+    assert _err(B, *p, _shape(), S(**ok)) == INV                              # workspace not 256-byte aligned
+    p = list(ptrs)
+    p[6] = P + 4
+    assert _err(B, *p, _shape(), S(**ok)) == UNS
+    for n in names:
+        assert _err(B, *ptrs, _shape(), S(**{**ok, n: ok[n] - 8})) == INV, n
+        assert _err(B, *ptrs, _shape(), S(**{**ok, n: ok[n] + 4})) == UNS, n
+    for kw in (dict(batch=0), dict(n_heads=5), dict(n_q=1 << 31), dict(n_k=-1), dict(softmax_scale=float("nan"))):
+        assert _err(B, *ptrs, _shape(**kw), S(**ok)) == INV, kw
+    assert _err(B, *ptrs, _shape(head_dim=64), S(**ok)) == UNS
