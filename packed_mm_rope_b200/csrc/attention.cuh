@@ -62,9 +62,11 @@
 // tile inside every row's interval runs as above; in the others logits outside
 // a row's interval become -inf, so their P is 0.  A 0 does not hide a V row
 // that holds inf or NaN (0 x inf = NaN on the tensor core), so in those tiles
-// the softmax warps first set the non-finite elements of V to 0 in shared
-// memory, and rows that do attend to such a key get a NaN logit there: masked
-// places cannot change a row, and what a row attends to is never hidden.  A row
+// two more warps set the non-finite elements of V to 0 in shared memory as soon
+// as it has landed, and rows that do attend to such a key get a NaN logit there:
+// masked places cannot change a row, and what a row attends to is never hidden.
+// (With the softmax warps cleaning V themselves, behind a barrier of all of
+// them, such a tile took about twice as long.)  A row
 // takes its reference m from its first 64-key half with a visible key; a row
 // without one ends with l = 0, O = 0 and a log-sum-exp of -inf.
 #pragma once
@@ -83,6 +85,9 @@ constexpr int SOFTMAX_WARPS = 16;                   // 8 per query tile, four th
 constexpr int W_PROD = SOFTMAX_WARPS;                // TMA producer
 constexpr int W_MMA = SOFTMAX_WARPS + 1;             // TMEM allocator and MMA issuer
 constexpr int THREADS = 32 * (SOFTMAX_WARPS + 2);    // 576
+constexpr int W_CLEAN = SOFTMAX_WARPS + 2;           // masked: two warps that clean V tiles
+constexpr int CLEAN_WARPS = 2;
+constexpr int MASKED_THREADS = THREADS + 32 * CLEAN_WARPS;   // 640: as many registers per thread as 576
 constexpr uint32_t TILE_BYTES = BM * HD * 2;     // 32768
 constexpr uint32_t HALF_BYTES = TILE_BYTES / 2;  // 16384
 
@@ -92,9 +97,9 @@ constexpr uint32_t SMEM_BAR = SMEM_KV + KV_STAGES * TILE_BYTES;
 // barriers: q_full[2], kv_full[S], kv_empty[S], s_full[2], p_full[2][2] (halves),
 //           pva_done[2] (first half of PV landed), o_full[2], mma_done,
 //           q_ready[2] (Q tile rotated in place, fused RoPE only)
-//           v_clean (masked: the V tile holds no inf or NaN any more)
-constexpr int NUM_BARS = 2 + 2 * KV_STAGES + 2 + 4 + 2 + 2 + 1 + 2 + 1;
-constexpr uint32_t SMEM_MISC = SMEM_BAR + NUM_BARS * 8;   // tmem base, abort flag, hull; two 16-byte key sets
+//           v_clean[2] (masked: the V tile holds no inf or NaN any more)
+constexpr int NUM_BARS = 2 + 2 * KV_STAGES + 2 + 4 + 2 + 2 + 1 + 2 + 2;
+constexpr uint32_t SMEM_MISC = SMEM_BAR + ((NUM_BARS * 8 + 15) & ~15);   // tmem base, abort, hull; two key sets
 constexpr uint32_t SMEM_BYTES = SMEM_MISC + 32 + 32 + 1024;   // + alignment slack
 static_assert(SMEM_MISC % 16 == 0, "the key sets are read 16 bytes at a time");
 
@@ -147,16 +152,36 @@ __device__ __forceinline__ int2 clamp_range(int2 r, int n_keys) {
   return r.x < r.y ? r : make_int2(0, 0);
 }
 
-// Sets the inf and NaN elements of rows 8 part .. 8 part + 7 of a swizzled
-// 128 x 128 bf16 tile (two halves of 64 columns) to 0 and returns those rows'
-// bits (one warp; the swizzle moves 16-byte pieces within their row only).
-__device__ __forceinline__ uint32_t clean_rows(uint8_t* tile, int part, int lane) {
-  uint32_t rows = 0u;
+// One warp: sets the inf and NaN elements of the 64 rows of `part` (0 or 1) of a
+// swizzled 128 x 128 bf16 tile (two halves of 64 columns) to 0 and adds those
+// rows' bits to the two words of `part` of `rows` (the swizzle moves 16-byte
+// pieces within their row only).  The writes are ordered for the tensor core.
+// Nearly every tile is finite, so the elements are first multiplied by 0 and
+// added up, one packed FMA per two of them: the sum is NaN if any is not finite.
+__device__ __forceinline__ void clean_rows(uint8_t* tile, int part, int lane, uint32_t* rows) {
+  uint4* const p = reinterpret_cast<uint4*>(tile + part * (HALF_BYTES / 2)) + lane;
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int piece = (i & 1) * 32 + lane;         // 64 pieces of 16 bytes: 8 rows of one half
-    uint4* p = reinterpret_cast<uint4*>(tile + (i >> 1) * HALF_BYTES + part * 1024 + piece * 16);
-    const uint4 u = *p;
+  for (int g = 0; g < 4; ++g) {
+    uint4 u[8];                                     // half g / 2, pieces 8 (g % 2) .. + 7 of 32
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = p[(g >> 1) * (HALF_BYTES / 16) + ((g & 1) * 8 + i) * 32];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int m = 0; m < 4; ++m) acc[m] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[m]), zero, acc[m]);
+    }
+  }
+  const __nv_bfloat162 sum = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+  if (!__any_sync(0xffffffffu, __hisnan(sum.x) || __hisnan(sum.y))) return;
+  uint32_t set[2] = {0u, 0u};
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i) {
+    const int piece = (i & 15) * 32 + lane;        // of 512 pieces of 16 bytes: 64 rows of one half
+    uint4* q = p + (i >> 4) * (HALF_BYTES / 16) + (i & 15) * 32;
+    const uint4 u = *q;
     uint32_t w[4] = {u.x, u.y, u.z, u.w};
     bool found = false;
 #pragma unroll
@@ -165,15 +190,21 @@ __device__ __forceinline__ uint32_t clean_rows(uint8_t* tile, int part, int lane
       if ((w[m] & 0x7f800000u) == 0x7f800000u) w[m] &= 0xffffu, found = true;
     }
     if (found) {
-      *p = make_uint4(w[0], w[1], w[2], w[3]);
-      rows |= 1u << (piece >> 3);
+      *q = make_uint4(w[0], w[1], w[2], w[3]);
+      const int row = piece >> 3;
+      if (row < 32) set[0] |= 1u << row;
+      else set[1] |= 1u << (row - 32);
     }
   }
-  return __reduce_or_sync(0xffffffffu, rows);
+  set[0] = __reduce_or_sync(0xffffffffu, set[0]);
+  set[1] = __reduce_or_sync(0xffffffffu, set[1]);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  if (lane < 2) rows[2 * part + lane] |= lane == 0 ? set[0] : set[1];
+  __syncwarp();
 }
 
 template <bool MASKED>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(MASKED ? MASKED_THREADS : THREADS, 1)
 attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -191,7 +222,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   auto bar_o_full = [&](int i) { return bar0 + 8u * (10 + 2 * KV_STAGES + i); };
   const uint32_t bar_mma_done = bar0 + 8u * (12 + 2 * KV_STAGES);
   auto bar_q_ready = [&](int i) { return bar0 + 8u * (13 + 2 * KV_STAGES + i); };
-  const uint32_t bar_v_clean = bar0 + 8u * (15 + 2 * KV_STAGES);
+  auto bar_v_clean = [&](int i) { return bar0 + 8u * (15 + 2 * KV_STAGES + i); };
   const bool fused_rope = !MASKED && p.rope_cs != nullptr;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC);
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 4);
@@ -221,7 +252,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     mbar_init(bar_mma_done, 1);
     mbar_init(bar_q_ready(0), 8);
     mbar_init(bar_q_ready(1), 8);
-    if (MASKED) mbar_init(bar_v_clean, SOFTMAX_WARPS);
+    if (MASKED) {
+      mbar_init(bar_v_clean(0), CLEAN_WARPS);
+      mbar_init(bar_v_clean(1), CLEAN_WARPS);
+    }
     *abort_flag = 0u;
     mbar_fence_init();
   }
@@ -265,7 +299,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       nkv = (hull[1] + BN - 1) / BN - tile0;
     }
     if (nkv == 0) {                                // no row attends to anything
-      for (int i = threadIdx.x; i < 2 * BM * (HD / 8); i += THREADS) {
+      for (int i = threadIdx.x; i < 2 * BM * (HD / 8); i += MASKED_THREADS) {
         const int row = q_row0 + i / (HD / 8);
         if (row < p.n_rows)
           *reinterpret_cast<uint4*>(p.o + batch * p.o_batch_stride + static_cast<long long>(row) * p.o_row_stride +
@@ -389,8 +423,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const bool more = j + 1 < nkv;
         // V(j) is waited for together with the first half of P0(j), K(j + 1)
         // together with its second half
-        if (!issue_pv_tile(0, vs, j, more ? bar_kv_full(ks) : 0u, (kidx / KV_STAGES) & 1, bar_kv_full(vs),
-                           (vidx / KV_STAGES) & 1))
+        if (!issue_pv_tile(0, vs, j, more ? bar_kv_full(ks) : 0u, (kidx / KV_STAGES) & 1,
+                           MASKED ? bar_v_clean(j & 1) : bar_kv_full(vs),
+                           MASKED ? (j >> 1) & 1 : (vidx / KV_STAGES) & 1))
           break;
         if (more) {
           tc_fence_after();
@@ -413,6 +448,22 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       tc_commit(bar_mma_done);
       volatile uint32_t never = 0u;
       mma_wait(bar_mma_done, 0, &never, p.drain_limit_ns, eslot);
+    }
+  } else if (MASKED && warp >= W_CLEAN) {
+    // --------------------------------------------- cleaning of V (masked) ----
+    // Every V tile passes through here (PV(j) waits for v_clean, so a tile cannot
+    // be gone before it was seen); only those with masked pairs are read.  V(j + 2)
+    // lands after PV(j) has read V(j), so two key sets are enough.
+    for (int j = 0; j < nkv; ++j) {
+      const int key0 = (tile0 + j) * BN;
+      const int vidx = 2 * j + 1, vs = vidx % KV_STAGES;
+      if (!warp_wait(bar_kv_full(vs), (vidx / KV_STAGES) & 1, abort_flag, limit, eslot)) break;
+      if (key0 < full_lo || key0 + BN > full_hi) {
+        uint32_t* rows = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC + 32 + 16 * (j & 1));
+        if (lane < 2) rows[2 * (warp - W_CLEAN) + lane] = 0u;
+        clean_rows(gbase + SMEM_KV + vs * TILE_BYTES, warp - W_CLEAN, lane, rows);
+      }
+      if (lane == 0) mbar_arrive(bar_v_clean(j & 1));
     }
   } else {
     // -------------------------------------------------------- softmax ----
@@ -437,8 +488,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (row_a < p.n_rows) rng_a = clamp_range(rg[row_a], p.n_keys);
       if (row_b < p.n_rows) rng_b = clamp_range(rg[row_b], p.n_keys);
     }
-    uint4* const unclean = reinterpret_cast<uint4*>(gbase + SMEM_MISC + 32);   // [2]: keys of V with inf or NaN
-    int cleaned = 0;                               // masked: tiles cleaned so far
+    const volatile uint32_t* const unclean = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC + 32);   // key sets of V
     float m_a = -INFINITY, m_b = -INFINITY;        // log2 units, identical in a row's 4 threads
     float l_a = 0.f, l_b = 0.f;                    // this thread's share of the row sums
     bool ok = true;
@@ -618,17 +668,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if constexpr (MASKED) {
         partial = key0 < full_lo || key0 + BN > full_hi;
         if (partial) {
-          // all softmax warps clean V(j) together; PV(j) waits for P(j), hence for them
-          const int vidx = 2 * j + 1, vs = vidx % KV_STAGES;
-          if (!warp_wait(bar_kv_full(vs), (vidx / KV_STAGES) & 1, abort_flag, limit, eslot)) { ok = false; break; }
-          const uint32_t rows = clean_rows(gbase + SMEM_KV + vs * TILE_BYTES, warp, lane);
-          if (rows != 0u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (lane == 0) reinterpret_cast<volatile uint8_t*>(&unclean[cleaned & 1])[warp] = static_cast<uint8_t>(rows);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_v_clean);
-          if (!warp_wait(bar_v_clean, cleaned & 1, abort_flag, limit, eslot)) { ok = false; break; }
-          bad = unclean[cleaned & 1];
-          ++cleaned;
+          // V(j) is clean and the keys that were not are known
+          if (!warp_wait(bar_v_clean(j & 1), (j >> 1) & 1, abort_flag, limit, eslot)) { ok = false; break; }
+          const volatile uint32_t* u = unclean + 4 * (j & 1);
+          bad = make_uint4(u[0], u[1], u[2], u[3]);
         }
       }
       if (!warp_wait(bar_s_full(wg), j & 1, abort_flag, limit, eslot)) { ok = false; break; }

@@ -31,10 +31,11 @@
 //   dkdv: .. dV(i) S(i+1) | dK(i) dP(i+1) ..   against   dS(i) | P(i+1)
 //   dq:   S(j+1) | dP(j+1) dQ(j)               against   dS(j) | P(j+1)
 //
-// Masked places (see attention.cuh): P and dS are set to 0 there by the rows'
-// intervals, never by a product, and the tiles that are B operands of a product
-// with such zeros (dO and Q in dkdv, K in dq) are freed of inf and NaN first; a
-// pair that is seen and touches such a row gets a NaN instead.
+// Masked places (see attention.cuh): P is set to 0 there by the rows' intervals
+// and dS with it, never by a product, and the tiles that are B operands of a
+// product with such zeros (dO and Q in dkdv, K in dq) are freed of inf and NaN by
+// warps 18 and 19 before any product reads them; a pair that is seen and touches
+// such a row gets a NaN instead.
 #pragma once
 
 #include "attention.cuh"
@@ -52,17 +53,19 @@ using attn::TILE_BYTES;
 using attn::clean_rows;
 using attn::mma_wait;
 using attn::warp_wait;
+using attn::CLEAN_WARPS;
 
 constexpr int WARPS = 16;                     // element-wise warps
 constexpr int W_PROD = WARPS;
 constexpr int W_MMA = WARPS + 1;
-constexpr int THREADS = 32 * (WARPS + 2);
+constexpr int W_CLEAN = WARPS + 2;
+constexpr int THREADS = 32 * (WARPS + 2 + CLEAN_WARPS);
 
 struct Params {
   int n_q, n_k, n_heads, group, n_qt;         // n_qt: query tiles of 128 rows
   float scale, scale_log2;
   const float2* stat;                         // [B][H][n_qt * 128] (lse log2 e, D)
-  const int2* rng;                            // [B][n_qt * 128] intervals, (0, 0) past the end
+  const int2* rng;                            // [B][n_qt * 128] intervals (lo, length), (0, 0) past the end
   const int4* hull;                           // [B][n_qt] (min lo, max hi, max lo, min hi)
   __nv_bfloat16 *dq, *dk, *dv;
   long long dq_stride, dk_stride, dv_stride;  // row strides, elements
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(256) prep_kernel(const __nv_bfloat16* __restri
       const int row = tile * BM + threadIdx.x;
       const int2 r = row < n_q ? attn::clamp_range(ranges[static_cast<long long>(batch) * n_q + row], n_k)
                                : make_int2(0, 0);
-      rng[(static_cast<long long>(batch) * n_qt + tile) * BM + threadIdx.x] = r;
+      rng[(static_cast<long long>(batch) * n_qt + tile) * BM + threadIdx.x] = make_int2(r.x, r.y - r.x);
       const bool some = r.x < r.y;
       const int lo = __reduce_min_sync(0xffffffffu, some ? r.x : 0x7fffffff);
       const int hi = __reduce_max_sync(0xffffffffu, some ? r.y : 0);
@@ -215,9 +218,9 @@ constexpr uint32_t SMEM_STAT = 6 * TILE_BYTES;                          // two s
 constexpr uint32_t SMEM_RNG = SMEM_STAT + 2 * 1024;                     // two slots of 128 intervals
 constexpr uint32_t SMEM_BAR = SMEM_RNG + 2 * 1024;
 // barriers: kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], s_full, p_full, dp_full,
-//           ds_full, clean, out_full, mma_done
-constexpr int NUM_BARS = 16;
-constexpr uint32_t SMEM_MISC = SMEM_BAR + NUM_BARS * 8;                 // key sets [2], tmem base, abort, first, last
+//           ds_full, out_full, mma_done, clean[2]
+constexpr int NUM_BARS = 17;
+constexpr uint32_t SMEM_MISC = SMEM_BAR + ((NUM_BARS * 8 + 15) & ~15);  // row sets [2], tmem base, abort, first, last
 constexpr uint32_t SMEM_BYTES = SMEM_MISC + 48 + 1024;
 constexpr uint32_t TMEM_S = 0, TMEM_DP = 128, TMEM_DV = 256, TMEM_DK = 384;
 }  // namespace dkdv
@@ -238,8 +241,9 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   auto bar_do_full = [&](int s) { return bar0 + 8u * (5 + s); };
   auto bar_do_empty = [&](int s) { return bar0 + 8u * (7 + s); };
   const uint32_t bar_s = bar0 + 72u, bar_p = bar0 + 80u, bar_dp = bar0 + 88u, bar_ds = bar0 + 96u;
-  const uint32_t bar_clean = bar0 + 104u, bar_out = bar0 + 112u, bar_done = bar0 + 120u;
-  uint4* const unclean = reinterpret_cast<uint4*>(gbase + SMEM_MISC);
+  const uint32_t bar_out = bar0 + 104u, bar_done = bar0 + 112u;
+  auto bar_clean = [&](int i) { return bar0 + 120u + 8u * (i & 1); };
+  uint32_t* const unclean = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC + 32);
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 36);
   int* const span = reinterpret_cast<int*>(gbase + SMEM_MISC + 40);
@@ -251,7 +255,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   const int4* const hulls = p.hull + static_cast<long long>(batch) * p.n_qt;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NUM_BARS; ++i) mbar_init(bar0 + 8u * i, i == 10 || i == 12 || i == 13 ? WARPS : 1);
+    for (int i = 0; i < NUM_BARS; ++i) mbar_init(bar0 + 8u * i, i == 10 || i == 12 ? WARPS : i >= 15 ? CLEAN_WARPS : 1);
     span[0] = 0x7fffffff;
     span[1] = -1;
     *abort_flag = 0u;
@@ -289,6 +293,8 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     return;
   }
   const int iters = nt * p.group;
+  // whether some row of query tile i does not see all of these keys
+  auto partial_tile = [&](int i) { const int4 h = hulls[i]; return h.z > k0 || h.w < k0 + BN; };
   if (warp == W_MMA) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -334,16 +340,12 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (lane == 0) {
       auto q_tile = [&](int s) { return base + SMEM_Q + s * TILE_BYTES; };
       auto do_tile = [&](int s) { return base + SMEM_DO + s * TILE_BYTES; };
-      bool ok = mma_wait(bar_kv, 0, abort_flag, limit, eslot) &&
-                mma_wait(bar_q_full(0), 0, abort_flag, limit, eslot);
+      // Q and dO are waited for together, as clean
+      bool ok = mma_wait(bar_kv, 0, abort_flag, limit, eslot) && mma_wait(bar_clean(0), 0, abort_flag, limit, eslot);
       if (ok) {
         tc_fence_after();
         issue_abt(tmem + TMEM_S, base + SMEM_K, q_tile(0));
         tc_commit(bar_s);
-        ok = mma_wait(bar_do_full(0), 0, abort_flag, limit, eslot);
-      }
-      if (ok) {
-        tc_fence_after();
         issue_abt(tmem + TMEM_DP, base + SMEM_V, do_tile(0));
         tc_commit(bar_dp);
       }
@@ -352,7 +354,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint32_t par = it & 1, par_next = ((it + 1) >> 1) & 1;
         const bool more = it + 1 < iters;
         // dV(i) and, into the S columns it has just read P from, S(i + 1)
-        if (more ? !mbar_spin2_bounded(bar_p, par, bar_q_full(sn), par_next, abort_flag, limit, eslot)
+        if (more ? !mbar_spin2_bounded(bar_p, par, bar_clean(sn), par_next, abort_flag, limit, eslot)
                  : !mma_wait(bar_p, par, abort_flag, limit, eslot))
           break;
         tc_fence_after();
@@ -363,9 +365,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           tc_commit(bar_s);
         }
         // dK(i) and dP(i + 1)
-        if (more ? !mbar_spin2_bounded(bar_ds, par, bar_do_full(sn), par_next, abort_flag, limit, eslot)
-                 : !mma_wait(bar_ds, par, abort_flag, limit, eslot))
-          break;
+        if (!mma_wait(bar_ds, par, abort_flag, limit, eslot)) break;
         tc_fence_after();
         issue_ab(tmem + TMEM_DK, tmem + TMEM_DP, q_tile(s), it > 0);
         tc_commit(bar_q_empty(s));
@@ -380,6 +380,27 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       volatile uint32_t never = 0u;
       mma_wait(bar_done, 0, &never, p.drain_limit_ns, eslot);
     }
+  } else if (warp >= W_CLEAN) {
+    // Every Q and dO tile passes through here (the products wait for `clean`, so
+    // none can be gone before it was seen); only those with masked pairs are
+    // read.  The tile two steps on lands after this one's last use, so two row
+    // sets are enough.
+    int qt = qt0;
+    for (int it = 0; it < iters; ++it) {
+      const int s = it & 1;
+      const bool partial = partial_tile(qt);
+      if (++qt == qt0 + nt) qt = qt0;
+      if (!warp_wait(bar_do_full(s), (it >> 1) & 1, abort_flag, limit, eslot) ||
+          !warp_wait(bar_q_full(s), (it >> 1) & 1, abort_flag, limit, eslot))
+        break;
+      if (partial) {
+        uint32_t* rows = unclean + 4 * s;
+        if (lane < 2) rows[2 * (warp - W_CLEAN) + lane] = 0u;
+        clean_rows(gbase + SMEM_DO + s * TILE_BYTES, warp - W_CLEAN, lane, rows);
+        clean_rows(gbase + SMEM_Q + s * TILE_BYTES, warp - W_CLEAN, lane, rows);
+      }
+      if (lane == 0) mbar_arrive(bar_clean(s));
+    }
   } else {
     const int t0 = lane & 3, t1 = lane >> 2;
     const int lane16 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
@@ -389,34 +410,23 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int key_a = k0 + lane16 + t1, key_b = key_a + 8;
     const float sl2 = p.scale_log2;
     bool ok = true;
-    int cleaned = 0;
     int qt = qt0;
     for (int it = 0; ok && it < iters; ++it) {
       const int s = it & 1;
-      const int4 h = hulls[qt];
+      const bool partial = partial_tile(qt);
       if (++qt == qt0 + nt) qt = qt0;
-      const bool partial = h.z > k0 || h.w < k0 + BN;   // some row does not see all of these keys
       // this thread's query columns: (lse, D) and intervals of two queries at a time
       const float4* const stat = reinterpret_cast<const float4*>(gbase + SMEM_STAT + s * 1024 + half * 512) + t0;
       const int4* const rng = reinterpret_cast<const int4*>(gbase + SMEM_RNG + s * 1024 + half * 512) + t0;
-      uint4 bad = make_uint4(0u, 0u, 0u, 0u);
-      if (!warp_wait(bar_q_full(s), (it >> 1) & 1, abort_flag, limit, eslot) ||
-          !warp_wait(bar_s, it & 1, abort_flag, limit, eslot)) { ok = false; break; }
+      uint32_t bad_lo = 0u, bad_hi = 0u;
+      if (!warp_wait(bar_q_full(s), (it >> 1) & 1, abort_flag, limit, eslot)) { ok = false; break; }
       if (partial) {
-        // S(i) and dP(i) have read Q and dO; dV and dK wait for P and dS, hence for this
-        if (!warp_wait(bar_do_full(s), (it >> 1) & 1, abort_flag, limit, eslot) ||
-            !warp_wait(bar_dp, it & 1, abort_flag, limit, eslot)) { ok = false; break; }
-        const uint32_t rows = clean_rows(gbase + SMEM_Q + s * TILE_BYTES, warp, lane) |
-                              clean_rows(gbase + SMEM_DO + s * TILE_BYTES, warp, lane);
-        if (rows != 0u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        if (lane == 0) reinterpret_cast<volatile uint8_t*>(&unclean[cleaned & 1])[warp] = static_cast<uint8_t>(rows);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_clean);
-        if (!warp_wait(bar_clean, cleaned & 1, abort_flag, limit, eslot)) { ok = false; break; }
-        bad = unclean[cleaned & 1];
-        ++cleaned;
+        if (!warp_wait(bar_clean(s), (it >> 1) & 1, abort_flag, limit, eslot)) { ok = false; break; }
+        const volatile uint32_t* u = unclean + 4 * s + 2 * half;
+        bad_lo = u[0];
+        bad_hi = u[1];
       }
-      const uint32_t bad_lo = half ? bad.z : bad.x, bad_hi = half ? bad.w : bad.y;
+      if (!warp_wait(bar_s, it & 1, abort_flag, limit, eslot)) { ok = false; break; }
       tc_fence_after();
       uint32_t sr[32];
       tmem_ld16x256(t_s, sr);
@@ -437,15 +447,23 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       if (partial) {
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          const int4 g = rng[4 * r];
-          const bool b0 = bit_of(bad_lo, bad_hi, 8 * r + 2 * t0), b1 = bit_of(bad_lo, bad_hi, 8 * r + 2 * t0 + 1);
-          auto masked = [](float v, int key, int lo, int hi, bool b) {
-            return key < lo || key >= hi ? 0.f : b ? __int_as_float(0x7fc00000) : v;
-          };
-          x[4 * r] = masked(x[4 * r], key_a, g.x, g.y, b0);
-          x[4 * r + 1] = masked(x[4 * r + 1], key_a, g.z, g.w, b1);
-          x[4 * r + 2] = masked(x[4 * r + 2], key_b, g.x, g.y, b0);
-          x[4 * r + 3] = masked(x[4 * r + 3], key_b, g.z, g.w, b1);
+          const int4 g = rng[4 * r];                // (lo, length) of two queries
+          auto seen = [](int key, int lo, int len) { return static_cast<unsigned>(key - lo) < static_cast<unsigned>(len); };
+          if (!seen(key_a, g.x, g.y)) x[4 * r] = 0.f;
+          if (!seen(key_a, g.z, g.w)) x[4 * r + 1] = 0.f;
+          if (!seen(key_b, g.x, g.y)) x[4 * r + 2] = 0.f;
+          if (!seen(key_b, g.z, g.w)) x[4 * r + 3] = 0.f;
+          if ((bad_lo | bad_hi) != 0u) {            // queries with inf or NaN in Q or dO
+            const float nan = __int_as_float(0x7fc00000);
+            if (bit_of(bad_lo, bad_hi, 8 * r + 2 * t0)) {
+              if (seen(key_a, g.x, g.y)) x[4 * r] = nan;
+              if (seen(key_b, g.x, g.y)) x[4 * r + 2] = nan;
+            }
+            if (bit_of(bad_lo, bad_hi, 8 * r + 2 * t0 + 1)) {
+              if (seen(key_a, g.z, g.w)) x[4 * r + 1] = nan;
+              if (seen(key_b, g.z, g.w)) x[4 * r + 3] = nan;
+            }
+          }
         }
       }
       uint32_t pk[16];
@@ -466,20 +484,11 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const float2 db = __fmul2_rn(
             make_float2(x[4 * r + 2], x[4 * r + 3]),
             __fadd2_rn(make_float2(__uint_as_float(sr[4 * r + 2]), __uint_as_float(sr[4 * r + 3])), md));
-        x[4 * r] = da.x;
-        x[4 * r + 1] = da.y;
-        x[4 * r + 2] = db.x;
-        x[4 * r + 3] = db.y;
-      }
-      if (partial) {                                // 0 times an inf or NaN of a masked pair
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int4 g = rng[4 * r];
-          if (key_a < g.x || key_a >= g.y) x[4 * r] = 0.f;
-          if (key_a < g.z || key_a >= g.w) x[4 * r + 1] = 0.f;
-          if (key_b < g.x || key_b >= g.y) x[4 * r + 2] = 0.f;
-          if (key_b < g.z || key_b >= g.w) x[4 * r + 3] = 0.f;
-        }
+        // where P is 0 a masked pair's inf or NaN must not come through
+        x[4 * r] = partial && x[4 * r] == 0.f ? 0.f : da.x;
+        x[4 * r + 1] = partial && x[4 * r + 1] == 0.f ? 0.f : da.y;
+        x[4 * r + 2] = partial && x[4 * r + 2] == 0.f ? 0.f : db.x;
+        x[4 * r + 3] = partial && x[4 * r + 3] == 0.f ? 0.f : db.y;
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r) pk[r] = pack_bf16x2(x[2 * r], x[2 * r + 1]);
@@ -508,10 +517,10 @@ namespace dq {
 constexpr int SLOTS = 5;                                         // K and V tiles in turn
 constexpr uint32_t SMEM_Q = 0, SMEM_DO = TILE_BYTES, SMEM_KV = 2 * TILE_BYTES;
 constexpr uint32_t SMEM_BAR = SMEM_KV + SLOTS * TILE_BYTES;
-// barriers: q_full, kv_full[5], kv_empty[5], s_full[2], dp_full, ds_full, clean, out_full, mma_done
-constexpr int NUM_BARS = 1 + 2 * SLOTS + 2 + 5;
-constexpr uint32_t SMEM_MISC = SMEM_BAR + ((NUM_BARS * 8 + 15) & ~15);   // key sets [2], tmem base, abort
-constexpr uint32_t SMEM_BYTES = SMEM_MISC + 48 + 1024;
+// barriers: q_full, kv_full[5], kv_empty[5], s_full[2], dp_full, ds_full, out_full, mma_done, clean[4]
+constexpr int NUM_BARS = 1 + 2 * SLOTS + 2 + 4 + 4;
+constexpr uint32_t SMEM_MISC = SMEM_BAR + ((NUM_BARS * 8 + 15) & ~15);   // key sets [4], tmem base, abort
+constexpr uint32_t SMEM_BYTES = SMEM_MISC + 80 + 1024;
 constexpr uint32_t TMEM_S = 0, TMEM_DP = 256, TMEM_DQ = 384;     // S in two buffers
 }  // namespace dq
 
@@ -529,11 +538,12 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   auto bar_full = [&](int s) { return bar0 + 8u * (1 + s); };
   auto bar_empty = [&](int s) { return bar0 + 8u * (1 + SLOTS + s); };
   auto bar_s = [&](int i) { return bar0 + 8u * (1 + 2 * SLOTS + i); };
-  const uint32_t bar_dp = bar0 + 8u * (3 + 2 * SLOTS), bar_ds = bar_dp + 8u, bar_clean = bar_dp + 16u;
-  const uint32_t bar_out = bar_dp + 24u, bar_done = bar_dp + 32u;
-  uint4* const unclean = reinterpret_cast<uint4*>(gbase + SMEM_MISC);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC + 32);
-  volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 36);
+  const uint32_t bar_dp = bar0 + 8u * (3 + 2 * SLOTS), bar_ds = bar_dp + 8u;
+  const uint32_t bar_out = bar_dp + 16u, bar_done = bar_dp + 24u;
+  auto bar_clean = [&](int i) { return bar_dp + 32u + 8u * (i & 3); };
+  uint32_t* const unclean = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC + 64);
+  volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 68);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qt = gridDim.x - 1 - blockIdx.x, head = blockIdx.y, batch = blockIdx.z;
@@ -552,9 +562,11 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     return;
   }
   const int tile0 = hull.x / BN, nkv = (hull.y + BN - 1) / BN - tile0;
+  // whether some row does not see all keys of the j-th tile
+  auto partial_tile = [&](int j) { return (tile0 + j) * BN < hull.z || (tile0 + j + 1) * BN > hull.w; };
   if (threadIdx.x == 0) {
     for (int i = 0; i < NUM_BARS; ++i)
-      mbar_init(bar0 + 8u * i, i == 4 + 2 * SLOTS || i == 5 + 2 * SLOTS ? WARPS : 1);
+      mbar_init(bar0 + 8u * i, i == 4 + 2 * SLOTS ? WARPS : i >= 7 + 2 * SLOTS ? CLEAN_WARPS : 1);
     *abort_flag = 0u;
     mbar_fence_init();
   }
@@ -592,7 +604,8 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       auto full_wait = [&](int idx) {
         return mma_wait(bar_full(idx % SLOTS), (idx / SLOTS) & 1, abort_flag, limit, eslot);
       };
-      bool ok = mma_wait(bar_q, 0, abort_flag, limit, eslot) && full_wait(0);
+      auto k_wait = [&](int j) { return mma_wait(bar_clean(j), (j >> 2) & 1, abort_flag, limit, eslot); };
+      bool ok = mma_wait(bar_q, 0, abort_flag, limit, eslot) && k_wait(0);
       if (ok) {
         tc_fence_after();
         issue_abt(tmem + TMEM_S, base + SMEM_Q, kv_tile(0));
@@ -609,7 +622,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         const bool more = j + 1 < nkv;
         const int kn = 2 * j + 2, vn = 2 * j + 3;
         if (more) {
-          if (!full_wait(kn)) break;
+          if (!k_wait(j + 1)) break;
           tc_fence_after();
           issue_abt(tmem + TMEM_S + 128 * ((j + 1) & 1), base + SMEM_Q, kv_tile(kn));
           tc_commit(bar_s((j + 1) & 1));
@@ -630,6 +643,19 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       volatile uint32_t never = 0u;
       mma_wait(bar_done, 0, &never, p.drain_limit_ns, eslot);
     }
+  } else if (warp >= W_CLEAN) {
+    // Every K tile passes through here, as in dkdv.  At most three are in the
+    // ring at once, so four key sets are enough.
+    for (int j = 0; j < nkv; ++j) {
+      const int kidx = 2 * j;
+      if (!warp_wait(bar_full(kidx % SLOTS), (kidx / SLOTS) & 1, abort_flag, limit, eslot)) break;
+      if (partial_tile(j)) {
+        uint32_t* rows = unclean + 4 * (j & 3);
+        if (lane < 2) rows[2 * (warp - W_CLEAN) + lane] = 0u;
+        clean_rows(gbase + SMEM_KV + (kidx % SLOTS) * TILE_BYTES, warp - W_CLEAN, lane, rows);
+      }
+      if (lane == 0) mbar_arrive(bar_clean(j));
+    }
   } else {
     const int t0 = lane & 3, t1 = lane >> 2;
     const int lane16 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
@@ -642,32 +668,23 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     const int2* const rng = p.rng + batch * qp + q_row0 + ra;
     const float2 st_a = stat[0], st_b = stat[8];
     const int2 rng_a = rng[0], rng_b = rng[8];
-    const unsigned len_a = rng_a.y - rng_a.x, len_b = rng_b.y - rng_b.x;
+    const unsigned len_a = rng_a.y, len_b = rng_b.y;
     const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
     const float2 la = make_float2(-st_a.x, -st_a.x), lbv = make_float2(-st_b.x, -st_b.x);
     const float2 da = make_float2(-st_a.y, -st_a.y), db = make_float2(-st_b.y, -st_b.y);
     bool ok = true;
-    int cleaned = 0;
     for (int j = 0; ok && j < nkv; ++j) {
       const int key0 = (tile0 + j) * BN;
-      const bool partial = key0 < hull.z || key0 + BN > hull.w;
+      const bool partial = partial_tile(j);
       const uint32_t t_s = tmem + lb + TMEM_S + 128 * (j & 1) + 64 * half;
-      uint4 bad = make_uint4(0u, 0u, 0u, 0u);
+      uint32_t bad_lo = 0u, bad_hi = 0u;
       if (!warp_wait(bar_s(j & 1), (j >> 1) & 1, abort_flag, limit, eslot)) { ok = false; break; }
-      if (partial) {
-        // S(j) has read K(j); dQ(j) waits for dS(j), hence for this
-        const int kidx = 2 * j;
-        if (!warp_wait(bar_full(kidx % SLOTS), (kidx / SLOTS) & 1, abort_flag, limit, eslot)) { ok = false; break; }
-        const uint32_t rows = clean_rows(gbase + SMEM_KV + (kidx % SLOTS) * TILE_BYTES, warp, lane);
-        if (rows != 0u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        if (lane == 0) reinterpret_cast<volatile uint8_t*>(&unclean[cleaned & 1])[warp] = static_cast<uint8_t>(rows);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_clean);
-        if (!warp_wait(bar_clean, cleaned & 1, abort_flag, limit, eslot)) { ok = false; break; }
-        bad = unclean[cleaned & 1];
-        ++cleaned;
+      if (partial) {                                // S(j) was read from a clean K(j)
+        if (!warp_wait(bar_clean(j), (j >> 2) & 1, abort_flag, limit, eslot)) { ok = false; break; }
+        const volatile uint32_t* u = unclean + 4 * (j & 3) + 2 * half;
+        bad_lo = u[0];
+        bad_hi = u[1];
       }
-      const uint32_t bad_lo = half ? bad.z : bad.x, bad_hi = half ? bad.w : bad.y;
       tc_fence_after();
       uint32_t sr[32];
       tmem_ld16x256(t_s, sr);
@@ -707,7 +724,15 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
           const bool seen = ((e >> 1) & 1) ? static_cast<unsigned>(off_b + k) < len_b
                                            : static_cast<unsigned>(off_a + k) < len_a;
           if (!seen) x[e] = 0.f;
-          else if (bit_of(bad_lo, bad_hi, k + 2 * t0)) x[e] = __int_as_float(0x7fc00000);
+        }
+        if ((bad_lo | bad_hi) != 0u) {              // keys with inf or NaN in K
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int k = 8 * (e >> 2) + (e & 1);
+            const bool seen = ((e >> 1) & 1) ? static_cast<unsigned>(off_b + k) < len_b
+                                             : static_cast<unsigned>(off_a + k) < len_a;
+            if (seen && bit_of(bad_lo, bad_hi, k + 2 * t0)) x[e] = __int_as_float(0x7fc00000);
+          }
         }
       }
       uint32_t pk[16];
