@@ -58,17 +58,21 @@
 //
 // MASKED: query row i attends to the keys [lo_i, hi_i) of `ranges` only (keys
 // and queries may differ in number, and groups of query heads may share a K/V
-// head).  The CTA visits the key tiles of the hull of its rows' intervals.  A
-// tile inside every row's interval runs as above; in the others logits outside
-// a row's interval become -inf, so their P is 0.  A 0 does not hide a V row
-// that holds inf or NaN (0 x inf = NaN on the tensor core), so in those tiles
-// two more warps set the non-finite elements of V to 0 in shared memory as soon
-// as it has landed, and rows that do attend to such a key get a NaN logit there:
-// masked places cannot change a row, and what a row attends to is never hidden.
-// (With the softmax warps cleaning V themselves, behind a barrier of all of
-// them, such a tile took about twice as long.)  A row
-// takes its reference m from its first 64-key half with a visible key; a row
-// without one ends with l = 0, O = 0 and a log-sum-exp of -inf.
+// head).  The CTA visits the key tiles of the hull of its rows' intervals.  In
+// tiles that some row does not see in full, each warp tells by votes whether none
+// of its 16 rows sees any of a 64-key half (P = 0 without a look at S), or each
+// row sees all of it or nothing (the code above with a reference of +inf, hence
+// numerators of 0, for the latter), or an interval ends inside: then logits
+// outside a row's interval become -inf.  A row takes
+// its reference m from its first half with a visible key; a row without one ends
+// with l = 0, O = 0 and a log-sum-exp of -inf.
+// P = 0 does not hide a V row that holds inf or NaN (0 x inf = NaN on the tensor
+// core), nor a reference of +inf a logit of inf or NaN, but neither can go unseen:
+// O is not finite then.  In that case the CTA runs a second time: logits are masked
+// one by one, the softmax warps first clear such elements of V from every tile
+// with masked pairs, and rows that do attend to such a key get a NaN logit there:
+// masked places cannot change a row, and what a row attends to is never hidden.  (Looking through V on every run, by the softmax warps or by two
+// warps of their own, made such tiles 1.5 to 2 times as long.)
 #pragma once
 
 #include "common.cuh"
@@ -85,9 +89,6 @@ constexpr int SOFTMAX_WARPS = 16;                   // 8 per query tile, four th
 constexpr int W_PROD = SOFTMAX_WARPS;                // TMA producer
 constexpr int W_MMA = SOFTMAX_WARPS + 1;             // TMEM allocator and MMA issuer
 constexpr int THREADS = 32 * (SOFTMAX_WARPS + 2);    // 576
-constexpr int W_CLEAN = SOFTMAX_WARPS + 2;           // masked: two warps that clean V tiles
-constexpr int CLEAN_WARPS = 2;
-constexpr int MASKED_THREADS = THREADS + 32 * CLEAN_WARPS;   // 640: as many registers per thread as 576
 constexpr uint32_t TILE_BYTES = BM * HD * 2;     // 32768
 constexpr uint32_t HALF_BYTES = TILE_BYTES / 2;  // 16384
 
@@ -97,10 +98,12 @@ constexpr uint32_t SMEM_BAR = SMEM_KV + KV_STAGES * TILE_BYTES;
 // barriers: q_full[2], kv_full[S], kv_empty[S], s_full[2], p_full[2][2] (halves),
 //           pva_done[2] (first half of PV landed), o_full[2], mma_done,
 //           q_ready[2] (Q tile rotated in place, fused RoPE only)
-//           v_clean[2] (masked: the V tile holds no inf or NaN any more)
-constexpr int NUM_BARS = 2 + 2 * KV_STAGES + 2 + 4 + 2 + 2 + 1 + 2 + 2;
-constexpr uint32_t SMEM_MISC = SMEM_BAR + ((NUM_BARS * 8 + 15) & ~15);   // tmem base, abort, hull; two key sets
+//           v_clean (masked, second run: the V tile holds no inf or NaN any more)
+constexpr int NUM_BARS = 2 + 2 * KV_STAGES + 2 + 4 + 2 + 2 + 1 + 2 + 1;
+constexpr uint32_t SMEM_MISC = SMEM_BAR + NUM_BARS * 8;       // tmem base, abort, hull, run again; two key sets
+constexpr uint32_t SMEM_RANGES = SMEM_MISC + 32 + 32;         // masked: intervals of the CTA's 256 rows
 constexpr uint32_t SMEM_BYTES = SMEM_MISC + 32 + 32 + 1024;   // + alignment slack
+constexpr uint32_t MASKED_SMEM_BYTES = SMEM_BYTES + 2 * BM * 8;
 static_assert(SMEM_MISC % 16 == 0, "the key sets are read 16 bytes at a time");
 
 constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, BN, false, false);   // Q, K both K-major
@@ -145,6 +148,11 @@ struct Params {
   int group;                      // query heads per K/V head
 };
 
+template <bool V>
+struct Flag {
+  static constexpr bool value = V;
+};
+
 // Keys of the row's interval that exist: an empty interval is (0, 0).
 __device__ __forceinline__ int2 clamp_range(int2 r, int n_keys) {
   r.x = max(r.x, 0);
@@ -152,35 +160,27 @@ __device__ __forceinline__ int2 clamp_range(int2 r, int n_keys) {
   return r.x < r.y ? r : make_int2(0, 0);
 }
 
-// One warp: sets the inf and NaN elements of the 64 rows of `part` (0 or 1) of a
-// swizzled 128 x 128 bf16 tile (two halves of 64 columns) to 0 and adds those
-// rows' bits to the two words of `part` of `rows` (the swizzle moves 16-byte
-// pieces within their row only).  The writes are ordered for the tensor core.
-// Nearly every tile is finite, so the elements are first multiplied by 0 and
-// added up, one packed FMA per two of them: the sum is NaN if any is not finite.
-__device__ __forceinline__ void clean_rows(uint8_t* tile, int part, int lane, uint32_t* rows) {
-  uint4* const p = reinterpret_cast<uint4*>(tile + part * (HALF_BYTES / 2)) + lane;
-  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
-  __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
+// Whether some lane of the warp holds an inf or NaN (multiplied by 0 and added
+// up, one packed FMA per two values: NaN if any is not finite).
+__device__ __forceinline__ bool any_nonfinite(const uint32_t (&v)[32]) {
+  float2 acc = make_float2(0.f, 0.f);
+  const float2 zero = acc;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    uint4 u[8];                                     // half g / 2, pieces 8 (g % 2) .. + 7 of 32
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = p[(g >> 1) * (HALF_BYTES / 16) + ((g & 1) * 8 + i) * 32];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-      for (int m = 0; m < 4; ++m) acc[m] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[m]), zero, acc[m]);
-    }
-  }
-  const __nv_bfloat162 sum = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
-  if (!__any_sync(0xffffffffu, __hisnan(sum.x) || __hisnan(sum.y))) return;
-  uint32_t set[2] = {0u, 0u};
+  for (int i = 0; i < 16; ++i)
+    acc = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), zero, acc);
+  return __any_sync(0xffffffffu, !(acc.x + acc.y == 0.f));
+}
+
+// Sets the inf and NaN elements of `rows` (8 or 64, at a multiple of 8) rows of a
+// 128 x 128 bf16 tile (two halves of 64 columns) to 0, ordered for the tensor
+// core, and returns the rows' bits (one warp; the 128-byte swizzle moves 16-byte
+// pieces within their row only).  Rare, so it is kept out of the callers' registers.
+__device__ __noinline__ uint2 zero_nonfinite(uint8_t* tile, int row0, int rows, int lane) {
+  uint32_t lo = 0u, hi = 0u;
 #pragma unroll 1
-  for (int i = 0; i < 32; ++i) {
-    const int piece = (i & 15) * 32 + lane;        // of 512 pieces of 16 bytes: 64 rows of one half
-    uint4* q = p + (i >> 4) * (HALF_BYTES / 16) + (i & 15) * 32;
+  for (int i = lane; i < rows * 16; i += 32) {      // 8 pieces of 16 bytes per row and half
+    const int row = (i % (rows * 8)) >> 3;
+    uint4* q = reinterpret_cast<uint4*>(tile + (i / (rows * 8)) * HALF_BYTES + (row0 + row) * 128 + (i & 7) * 16);
     const uint4 u = *q;
     uint32_t w[4] = {u.x, u.y, u.z, u.w};
     bool found = false;
@@ -191,20 +191,17 @@ __device__ __forceinline__ void clean_rows(uint8_t* tile, int part, int lane, ui
     }
     if (found) {
       *q = make_uint4(w[0], w[1], w[2], w[3]);
-      const int row = piece >> 3;
-      if (row < 32) set[0] |= 1u << row;
-      else set[1] |= 1u << (row - 32);
+      if (row < 32) lo |= 1u << row;
+      else hi |= 1u << (row - 32);
     }
   }
-  set[0] = __reduce_or_sync(0xffffffffu, set[0]);
-  set[1] = __reduce_or_sync(0xffffffffu, set[1]);
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  if (lane < 2) rows[2 * part + lane] |= lane == 0 ? set[0] : set[1];
   __syncwarp();
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  return make_uint2(__reduce_or_sync(0xffffffffu, lo), __reduce_or_sync(0xffffffffu, hi));
 }
 
 template <bool MASKED>
-__global__ void __launch_bounds__(MASKED ? MASKED_THREADS : THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 1)
 attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -222,7 +219,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   auto bar_o_full = [&](int i) { return bar0 + 8u * (10 + 2 * KV_STAGES + i); };
   const uint32_t bar_mma_done = bar0 + 8u * (12 + 2 * KV_STAGES);
   auto bar_q_ready = [&](int i) { return bar0 + 8u * (13 + 2 * KV_STAGES + i); };
-  auto bar_v_clean = [&](int i) { return bar0 + 8u * (15 + 2 * KV_STAGES + i); };
+  const uint32_t bar_v_clean = bar0 + 8u * (15 + 2 * KV_STAGES);
   const bool fused_rope = !MASKED && p.rope_cs != nullptr;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC);
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 4);
@@ -236,7 +233,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const uint64_t limit = p.wait_limit_ns;
   const int eslot = p.err_slot;
 
-  if (threadIdx.x == 0) {
+  auto init_bars = [&] {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_q_full(i), 1);
       mbar_init(bar_s_full(i), 1);
@@ -252,12 +249,14 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     mbar_init(bar_mma_done, 1);
     mbar_init(bar_q_ready(0), 8);
     mbar_init(bar_q_ready(1), 8);
-    if (MASKED) {
-      mbar_init(bar_v_clean(0), CLEAN_WARPS);
-      mbar_init(bar_v_clean(1), CLEAN_WARPS);
-    }
-    *abort_flag = 0u;
+    mbar_init(bar_v_clean, SOFTMAX_WARPS);
     mbar_fence_init();
+  };
+  volatile uint32_t* const again = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 24);   // masked
+  if (threadIdx.x == 0) {
+    *abort_flag = 0u;
+    *again = 0u;
+    init_bars();
   }
   int nkv = p.n_kv_tiles;
   int tile0 = 0;                     // first key tile of this CTA
@@ -278,7 +277,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         r = clamp_range(p.ranges[static_cast<long long>(batch) * p.n_rows + row], p.n_keys);
         all_lo = r.x;
         all_hi = r.y;
+        reinterpret_cast<int2*>(gbase + SMEM_RANGES)[threadIdx.x] = r;
         if (r.x >= r.y) r = make_int2(0x7fffffff, 0);
+      } else {
+        reinterpret_cast<int2*>(gbase + SMEM_RANGES)[threadIdx.x] = make_int2(0, 0x7fffffff);   // never stored
       }
       const int lo = __reduce_min_sync(0xffffffffu, r.x), hi = __reduce_max_sync(0xffffffffu, r.y);
       all_hi = __reduce_min_sync(0xffffffffu, all_hi);
@@ -299,7 +301,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       nkv = (hull[1] + BN - 1) / BN - tile0;
     }
     if (nkv == 0) {                                // no row attends to anything
-      for (int i = threadIdx.x; i < 2 * BM * (HD / 8); i += MASKED_THREADS) {
+      for (int i = threadIdx.x; i < 2 * BM * (HD / 8); i += THREADS) {
         const int row = q_row0 + i / (HD / 8);
         if (row < p.n_rows)
           *reinterpret_cast<uint4*>(p.o + batch * p.o_batch_stride + static_cast<long long>(row) * p.o_row_stride +
@@ -324,6 +326,10 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // masked: whether some row of the CTA does not see all of the j-th key tile
+  auto edge_tile = [&](int j) { return (tile0 + j) * BN < full_lo || (tile0 + j + 1) * BN > full_hi; };
+
+  for (int run = 0; run < (MASKED ? 2 : 1); ++run) {
   if (warp == W_PROD) {
     // ------------------------------------------------------------ TMA ----
     if (lane == 0) {
@@ -423,9 +429,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const bool more = j + 1 < nkv;
         // V(j) is waited for together with the first half of P0(j), K(j + 1)
         // together with its second half
-        if (!issue_pv_tile(0, vs, j, more ? bar_kv_full(ks) : 0u, (kidx / KV_STAGES) & 1,
-                           MASKED ? bar_v_clean(j & 1) : bar_kv_full(vs),
-                           MASKED ? (j >> 1) & 1 : (vidx / KV_STAGES) & 1))
+        if (!issue_pv_tile(0, vs, j, more ? bar_kv_full(ks) : 0u, (kidx / KV_STAGES) & 1, bar_kv_full(vs),
+                           (vidx / KV_STAGES) & 1))
           break;
         if (more) {
           tc_fence_after();
@@ -449,22 +454,6 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       volatile uint32_t never = 0u;
       mma_wait(bar_mma_done, 0, &never, p.drain_limit_ns, eslot);
     }
-  } else if (MASKED && warp >= W_CLEAN) {
-    // --------------------------------------------- cleaning of V (masked) ----
-    // Every V tile passes through here (PV(j) waits for v_clean, so a tile cannot
-    // be gone before it was seen); only those with masked pairs are read.  V(j + 2)
-    // lands after PV(j) has read V(j), so two key sets are enough.
-    for (int j = 0; j < nkv; ++j) {
-      const int key0 = (tile0 + j) * BN;
-      const int vidx = 2 * j + 1, vs = vidx % KV_STAGES;
-      if (!warp_wait(bar_kv_full(vs), (vidx / KV_STAGES) & 1, abort_flag, limit, eslot)) break;
-      if (key0 < full_lo || key0 + BN > full_hi) {
-        uint32_t* rows = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC + 32 + 16 * (j & 1));
-        if (lane < 2) rows[2 * (warp - W_CLEAN) + lane] = 0u;
-        clean_rows(gbase + SMEM_KV + vs * TILE_BYTES, warp - W_CLEAN, lane, rows);
-      }
-      if (lane == 0) mbar_arrive(bar_v_clean(j & 1));
-    }
   } else {
     // -------------------------------------------------------- softmax ----
     // Eight warps per query tile, four threads per row: warp w reads the 16
@@ -482,12 +471,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int tail = p.n_rows - (nkv - 1) * BN;    // valid keys in the last tile (1..128)
     const int row_a = q_row0 + wg * BM + lane16 + t1;
     const int row_b = row_a + 8;
-    int2 rng_a = make_int2(0, 0), rng_b = make_int2(0, 0);   // masked: the rows' key intervals
-    if constexpr (MASKED) {
-      const int2* rg = p.ranges + static_cast<long long>(batch) * p.n_rows;
-      if (row_a < p.n_rows) rng_a = clamp_range(rg[row_a], p.n_keys);
-      if (row_b < p.n_rows) rng_b = clamp_range(rg[row_b], p.n_keys);
-    }
+    // masked: the intervals of row_a and row_b (8 rows on)
+    const int2* const rng = reinterpret_cast<const int2*>(gbase + SMEM_RANGES) + wg * BM + lane16 + t1;
     const volatile uint32_t* const unclean = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC + 32);   // key sets of V
     float m_a = -INFINITY, m_b = -INFINITY;        // log2 units, identical in a row's 4 threads
     float l_a = 0.f, l_b = 0.f;                    // this thread's share of the row sums
@@ -517,9 +502,11 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
       }
     };
-    auto mask_logits = [&](int key0, uint32_t bad_lo, uint32_t bad_hi, float (&x)[32]) {
-      const unsigned len_a = rng_a.y - rng_a.x, len_b = rng_b.y - rng_b.x;
-      const int off_a = key0 + 2 * t0 - rng_a.x, off_b = key0 + 2 * t0 - rng_b.x;
+    enum { SEEN_NONE, SEEN_SOME, SEEN_ALL };       // what a warp's 16 rows see of 64 keys
+    auto mask_logits = [&](int key0, const volatile uint32_t* bad, float (&x)[32]) {
+      const int2 a = rng[0], b = rng[8];
+      const unsigned len_a = a.y - a.x, len_b = b.y - b.x;
+      const int off_a = key0 + 2 * t0 - a.x, off_b = key0 + 2 * t0 - b.x;
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         const int k = 8 * (e >> 2) + (e & 1);
@@ -527,7 +514,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                          : static_cast<unsigned>(off_a + k) < len_a;
         if (!seen) x[e] = -INFINITY;
       }
-      if ((bad_lo | bad_hi) != 0u) {               // a key of this half has inf or NaN in V
+      if (bad != nullptr && (bad[0] | bad[1]) != 0u) {   // a key of this half has inf or NaN in V
+        const uint32_t bad_lo = bad[0], bad_hi = bad[1];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int k = 8 * (e >> 2) + (e & 1);
@@ -538,14 +526,12 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
       }
     };
-    // whether row r sees a key of [key0, key0 + 64)
-    auto sees = [](int2 r, int key0) { return r.x < key0 + 64 && r.y > key0; };
     // numerators of the 16 keys of each row: bf16 pairs (register order of the
     // 16x128b store) and this thread's sums
-    auto exps = [&](const float (&x)[32], uint32_t (&pk)[16], float& sa, float& sb) {
+    auto exps = [&](const float (&x)[32], uint32_t (&pk)[16], float& sa, float& sb, bool none_a = false,
+                    bool none_b = false) {
       const float2 c2 = make_float2(sl2, sl2);
-      // masked: a row that has seen no key yet has no reference (its numerators are 0 or found again)
-      const float ra = MASKED && m_a == -INFINITY ? 0.f : -m_a, rb = MASKED && m_b == -INFINITY ? 0.f : -m_b;
+      const float ra = none_a ? -INFINITY : -m_a, rb = none_b ? -INFINITY : -m_b;
       const float2 ma = make_float2(ra, ra), mb = make_float2(rb, rb);
       float2 acc_a = make_float2(0.f, 0.f), acc_b = make_float2(0.f, 0.f);
 #pragma unroll
@@ -592,13 +578,13 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       fa = 1.f;
       fb = 1.f;
       if (na) {
-        const float mn = fmaxf(m_a, xa * sl2);
+        const float mn = fmaxf(first_a ? -INFINITY : m_a, xa * sl2);
         fa = first_a ? 0.f : ex2_approx(m_a - mn);
         m_a = mn;
         l_a *= fa;
       }
       if (nb) {
-        const float mn = fmaxf(m_b, xb * sl2);
+        const float mn = fmaxf(first_b ? -INFINITY : m_b, xb * sl2);
         fb = first_b ? 0.f : ex2_approx(m_b - mn);
         m_b = mn;
         l_b *= fb;
@@ -661,48 +647,54 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (lane == 0) mbar_arrive(bar_q_ready(wg));
     }
 
-    for (int j = 0; ok && j < nkv; ++j) {
+    // One key tile.  EDGE (masked): the rows see what seen0, seen1 say of its halves
+    // or have no reference yet.  Otherwise each row has one and sees all of a half,
+    // or (bits of `none`: row a, row b of half 0, of half 1) nothing.
+    bool set_a = !MASKED, set_b = !MASKED;         // masked: the rows have a reference (else m is 0, and l)
+    auto step = [&](auto edge, int j, int seen0, int seen1, int none, const volatile uint32_t* bad) -> bool {
+      constexpr bool EDGE = decltype(edge)::value;
       const int key0 = (tile0 + j) * BN;
-      bool partial = false;                         // masked: some row does not see all of the tile
-      uint4 bad = make_uint4(0u, 0u, 0u, 0u);
-      if constexpr (MASKED) {
-        partial = key0 < full_lo || key0 + BN > full_hi;
-        if (partial) {
-          // V(j) is clean and the keys that were not are known
-          if (!warp_wait(bar_v_clean(j & 1), (j >> 1) & 1, abort_flag, limit, eslot)) { ok = false; break; }
-          const volatile uint32_t* u = unclean + 4 * (j & 1);
-          bad = make_uint4(u[0], u[1], u[2], u[3]);
-        }
-      }
-      if (!warp_wait(bar_s_full(wg), j & 1, abort_flag, limit, eslot)) { ok = false; break; }
-      tc_fence_after();
       const bool last = j == nkv - 1;
-      {
+      // whether a row takes its reference from the 64 keys at `key`
+      auto first_of = [&](bool set, int i, int key) {
+        if (set) return false;
+        const int2 r = rng[i];
+        return r.x < key + 64 && r.y > key;
+      };
+      if (MASKED && seen0 == SEEN_NONE) {
+        const uint32_t pk[16] = {};
+        store_p(0, pk);
+      } else {
         // ---- keys 0..63 ----
         uint32_t r[32];
         tmem_ld16x256(t_s, r);
         tmem_wait_ld(r);
         float x[32];
         to_logits(r, 0, last, x);
-        if (MASKED && partial) mask_logits(key0, bad.x, bad.y, x);
+        if (EDGE && seen0 != SEEN_ALL) mask_logits(key0, bad, x);
         uint32_t pk[16];
         float sa, sb;
-        exps(x, pk, sa, sb);                        // speculative against the references
-        const bool first_a = MASKED ? m_a == -INFINITY && sees(rng_a, key0) : j == 0;
-        const bool first_b = MASKED ? m_b == -INFINITY && sees(rng_b, key0) : j == 0;
+        const bool na = MASKED && !EDGE && (none & 1), nb = MASKED && !EDGE && (none & 2);
+        exps(x, pk, sa, sb, na, nb);                // speculative against the references
+        const bool first_a = EDGE ? first_of(set_a, 0, key0) : !MASKED && j == 0;
+        const bool first_b = EDGE ? first_of(set_b, 8, key0) : !MASKED && j == 0;
         const bool need = first_a || first_b || !(sa <= PART_LIMIT) || !(sb <= PART_LIMIT);
         if (__any_sync(0xffffffffu, need)) {
           float fa, fb;
           new_reference(x, first_a, first_b, sa, sb, fa, fb);
+          if (EDGE) set_a |= first_a, set_b |= first_b;
           __syncwarp();
           if (j > 0) rescale_o(fa, fb);   // O holds PV(j-1); PV(j) has not started
-          exps(x, pk, sa, sb);
+          exps(x, pk, sa, sb, na, nb);
         }
         l_a += sa;
         l_b += sb;
         store_p(0, pk);
       }
-      {
+      if (MASKED && seen1 == SEEN_NONE) {
+        const uint32_t pk[16] = {};
+        store_p(1, pk);
+      } else {
         // ---- keys 64..127 ----
         uint32_t r[32];
         __syncwarp();
@@ -710,28 +702,73 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tmem_wait_ld(r);
         float x[32];
         to_logits(r, 64, last, x);
-        if (MASKED && partial) mask_logits(key0 + 64, bad.z, bad.w, x);
+        if (EDGE && seen1 != SEEN_ALL) mask_logits(key0 + 64, bad != nullptr ? bad + 2 : bad, x);
         uint32_t pk[16];
         float sa, sb;
-        exps(x, pk, sa, sb);
-        const bool first_a = MASKED && m_a == -INFINITY && sees(rng_a, key0 + 64);
-        const bool first_b = MASKED && m_b == -INFINITY && sees(rng_b, key0 + 64);
+        const bool na = MASKED && !EDGE && (none & 4), nb = MASKED && !EDGE && (none & 8);
+        exps(x, pk, sa, sb, na, nb);
+        const bool first_a = EDGE && first_of(set_a, 0, key0 + 64);
+        const bool first_b = EDGE && first_of(set_b, 8, key0 + 64);
         const bool need = first_a || first_b || !(sa <= PART_LIMIT) || !(sb <= PART_LIMIT);
         if (__any_sync(0xffffffffu, need)) {
           // the first half of PV(j) may be in flight: let it land, then rescale
           // O (which now includes it) together with the running sums
-          if (!warp_wait(bar_pva_done(wg), j & 1, abort_flag, limit, eslot)) { ok = false; break; }
+          if (!warp_wait(bar_pva_done(wg), j & 1, abort_flag, limit, eslot)) return false;
           tc_fence_after();
           float fa, fb;
           new_reference(x, first_a, first_b, sa, sb, fa, fb);
+          if (EDGE) set_a |= first_a, set_b |= first_b;
           __syncwarp();
           rescale_o(fa, fb);
-          exps(x, pk, sa, sb);
+          exps(x, pk, sa, sb, na, nb);
         }
         l_a += sa;
         l_b += sb;
         store_p(1, pk);
       }
+      return true;
+    };
+    int edges = 0;                                 // masked, second run: tiles cleared so far
+    if (MASKED) m_a = m_b = 0.f;
+    for (int j = 0; ok && j < nkv; ++j) {
+      int seen0 = SEEN_ALL, seen1 = SEEN_ALL;       // masked: of the two halves of the tile, by the warp's rows
+      int none = 0;
+      bool plain = set_a && set_b;                  // no logit has to be masked, no reference found
+      const volatile uint32_t* bad = nullptr;
+      if (MASKED && edge_tile(j)) {
+        const int key0 = (tile0 + j) * BN;
+        if (run == 1) {
+          // all softmax warps clear V(j) together; PV(j) waits for P(j), hence for them
+          const int vidx = 2 * j + 1, vs = vidx % KV_STAGES;
+          if (!warp_wait(bar_kv_full(vs), (vidx / KV_STAGES) & 1, abort_flag, limit, eslot)) { ok = false; break; }
+          const uint2 rows = zero_nonfinite(gbase + SMEM_KV + vs * TILE_BYTES, 8 * warp, 8, lane);
+          if (lane == 0)
+            reinterpret_cast<volatile uint8_t*>(gbase + SMEM_MISC + 32 + 16 * (edges & 1))[warp] =
+                static_cast<uint8_t>(rows.x);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_v_clean);
+          if (!warp_wait(bar_v_clean, edges & 1, abort_flag, limit, eslot)) { ok = false; break; }
+          bad = unclean + 4 * (edges & 1);          // read before the next arrival: two sets are enough
+          ++edges;
+        }
+        const int2 a = rng[0], b = rng[8];
+        auto nothing = [](int2 r, int key) { return r.x >= key + 64 || r.y <= key; };
+        auto all = [](int2 r, int key) { return r.x <= key && r.y >= key + 64; };
+        none = (nothing(a, key0) ? 1 : 0) | (nothing(b, key0) ? 2 : 0) | (nothing(a, key0 + 64) ? 4 : 0) |
+               (nothing(b, key0 + 64) ? 8 : 0);
+        plain = run == 0 && ((none & 1) || (set_a && all(a, key0))) && ((none & 2) || (set_b && all(b, key0))) &&
+                ((none & 4) || (set_a && all(a, key0 + 64))) && ((none & 8) || (set_b && all(b, key0 + 64)));
+        if (__all_sync(0xffffffffu, (none & 3) == 3)) seen0 = SEEN_NONE;
+        if (__all_sync(0xffffffffu, (none & 12) == 12)) seen1 = SEEN_NONE;
+        if (seen0 != SEEN_NONE) seen0 = SEEN_SOME;
+        if (seen1 != SEEN_NONE) seen1 = SEEN_SOME;
+      }
+      if (!warp_wait(bar_s_full(wg), j & 1, abort_flag, limit, eslot)) { ok = false; break; }
+      tc_fence_after();
+      if (!MASKED || __all_sync(0xffffffffu, plain))
+        ok = step(Flag<false>{}, j, seen0, seen1, none, bad);
+      else
+        ok = step(Flag<true>{}, j, seen0, seen1, none, bad);
     }
 
     // epilogue: O / l -> bf16 -> global; optional log-sum-exp
@@ -743,7 +780,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
       l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
       // masked: a row without keys has l = 0 and O = 0
-      const float inv_a = MASKED && l_a == 0.f ? 0.f : 1.f / l_a, inv_b = MASKED && l_b == 0.f ? 0.f : 1.f / l_b;
+      const bool empty_a = MASKED && rng[0].x >= rng[0].y, empty_b = MASKED && rng[8].x >= rng[8].y;
+      const float inv_a = empty_a ? 0.f : 1.f / l_a, inv_b = empty_b ? 0.f : 1.f / l_b;
       __nv_bfloat16* orow_a = p.o + batch * p.o_batch_stride + static_cast<long long>(row_a) * p.o_row_stride + head * HD;
       __nv_bfloat16* orow_b = orow_a + 8 * p.o_row_stride;
 #pragma unroll 1
@@ -752,6 +790,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         __syncwarp();
         tmem_ld16x256(t_o + 64 * h, o);
         tmem_wait_ld(o);
+        if (MASKED && run == 0 && any_nonfinite(o) && (edge_tile(0) || edge_tile(nkv - 1))) *again = 1u;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const int col = 64 * h + 8 * q + 2 * t0;
@@ -765,6 +804,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       if (p.lse != nullptr && t0 == 0) {
         float* lrow = p.lse + (static_cast<long long>(batch) * p.n_heads + head) * p.n_rows;
+        // masked: without keys m = l = 0 and log 0 = -inf
         if (row_a < p.n_rows) lrow[row_a] = (m_a + __log2f(l_a)) * 0.69314718055994530942f;
         if (row_b < p.n_rows) lrow[row_b] = (m_b + __log2f(l_b)) * 0.69314718055994530942f;
       }
@@ -773,6 +813,24 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (MASKED) {
+    if (run == 1 || *again == 0u || *abort_flag != 0u) break;
+    // second run: loads, products and waits of the first have ended; the commits
+    // that nothing waited for arrive, then the barriers start over
+    if (threadIdx.x == 0) {
+      volatile uint32_t never = 0u;
+      for (int s = 0; s < KV_STAGES; ++s) {
+        const int uses = (2 * nkv - s + KV_STAGES - 1) / KV_STAGES;
+        if (uses > 0) mbar_wait_bounded(bar_kv_empty(s), (uses - 1) & 1, &never, p.drain_limit_ns, eslot);
+      }
+      for (int i = 0; i < 2; ++i) mbar_wait_bounded(bar_pva_done(i), (nkv - 1) & 1, &never, p.drain_limit_ns, eslot);
+      for (int i = 0; i < NUM_BARS; ++i) mbar_inval(bar0 + 8u * i);
+      init_bars();
+    }
+    __syncthreads();
+    tc_fence_after();
+  }
+  }
   if (warp == W_MMA) {
     __syncwarp();
     tc_fence_after();

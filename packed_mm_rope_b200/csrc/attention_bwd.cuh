@@ -32,10 +32,14 @@
 //   dq:   S(j+1) | dP(j+1) dQ(j)               against   dS(j) | P(j+1)
 //
 // Masked places (see attention.cuh): P is set to 0 there by the rows' intervals
-// and dS with it, never by a product, and the tiles that are B operands of a
-// product with such zeros (dO and Q in dkdv, K in dq) are freed of inf and NaN by
-// warps 18 and 19 before any product reads them; a pair that is seen and touches
-// such a row gets a NaN instead.
+// and dS with it, never by a product.  The tiles that are B operands of a product
+// with such zeros (dO and Q in dkdv, K in dq) may hold inf or NaN in masked rows.
+// dq: such a row of K makes its column of S non-finite, so in tiles with masked
+// pairs each warp looks at the S it holds anyway (one packed FMA per two values)
+// and, if need be, clears K's rows of its half before it hands dS on.  dkdv: looking
+// at dP before P is handed on would cost such tiles half their time again, so the
+// CTA runs a second time with that look if its dK or dV come out non-finite.  A
+// pair that is seen and not finite gets a NaN P or dS.
 #pragma once
 
 #include "attention.cuh"
@@ -50,16 +54,15 @@ using attn::HALF_BYTES;
 using attn::IDESC_O;
 using attn::IDESC_S;
 using attn::TILE_BYTES;
-using attn::clean_rows;
+using attn::any_nonfinite;
+using attn::zero_nonfinite;
 using attn::mma_wait;
 using attn::warp_wait;
-using attn::CLEAN_WARPS;
 
 constexpr int WARPS = 16;                     // element-wise warps
 constexpr int W_PROD = WARPS;
 constexpr int W_MMA = WARPS + 1;
-constexpr int W_CLEAN = WARPS + 2;
-constexpr int THREADS = 32 * (WARPS + 2 + CLEAN_WARPS);
+constexpr int THREADS = 32 * (WARPS + 2);
 
 struct Params {
   int n_q, n_k, n_heads, group, n_qt;         // n_qt: query tiles of 128 rows
@@ -106,8 +109,8 @@ __global__ void __launch_bounds__(256) prep_kernel(const __nv_bfloat16* __restri
 #pragma unroll
     for (int k = 8; k > 0; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
     if (sub == 0) {
-      float l = row < n_q ? lse[bh * n_q + row] : 0.f;
-      l = l == -INFINITY ? 0.f : l * 1.4426950408889634f;   // rows without keys are masked everywhere
+      // rows without keys (lse = -inf) are masked everywhere
+      const float l = row < n_q ? lse[bh * n_q + row] * 1.4426950408889634f : 0.f;
       stat[bh * n_qt * BM + row] = make_float2(l, d);
     }
   }
@@ -178,8 +181,9 @@ __device__ __forceinline__ void issue_ab(uint32_t d, uint32_t a, uint32_t b, boo
 }
 
 // This warp's 16 lanes x 64 columns of an accumulator, times `scale`, rounded to
-// bf16 rows `row_a`, `row_a + 8` (< n_rows) of an output at `out`.
-__device__ __forceinline__ void store_tile(uint32_t taddr, float scale, __nv_bfloat16* out, long long stride,
+// bf16 rows `row_a`, `row_a + 8` (< n_rows) of an output at `out`.  Returns whether
+// all of it is finite.
+__device__ __forceinline__ bool store_tile(uint32_t taddr, float scale, __nv_bfloat16* out, long long stride,
                                            int row_a, int n_rows, int t0) {
   uint32_t v[32];
   __syncwarp();
@@ -195,6 +199,7 @@ __device__ __forceinline__ void store_tile(uint32_t taddr, float scale, __nv_bfl
       *reinterpret_cast<uint32_t*>(out + (row_a + 8) * stride + col) =
           pack_bf16x2(__uint_as_float(v[4 * r + 2]) * scale, __uint_as_float(v[4 * r + 3]) * scale);
   }
+  return !any_nonfinite(v);
 }
 
 // Rounded values of this warp's 16 x 64 piece -> tensor memory, then one arrival.
@@ -207,7 +212,7 @@ __device__ __forceinline__ void publish(uint32_t taddr, const uint32_t (&pk)[16]
   if (lane == 0) mbar_arrive(bar);
 }
 
-__device__ __forceinline__ uint32_t bit_of(uint32_t lo, uint32_t hi, int k) { return (k < 32 ? lo : hi) >> (k & 31) & 1u; }
+__device__ __forceinline__ bool nonfinite(uint32_t v) { return (v & 0x7f800000u) == 0x7f800000u; }
 
 // ------------------------------------------------------------------ dkdv ----
 
@@ -218,10 +223,10 @@ constexpr uint32_t SMEM_STAT = 6 * TILE_BYTES;                          // two s
 constexpr uint32_t SMEM_RNG = SMEM_STAT + 2 * 1024;                     // two slots of 128 intervals
 constexpr uint32_t SMEM_BAR = SMEM_RNG + 2 * 1024;
 // barriers: kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], s_full, p_full, dp_full,
-//           ds_full, out_full, mma_done, clean[2]
-constexpr int NUM_BARS = 17;
-constexpr uint32_t SMEM_MISC = SMEM_BAR + ((NUM_BARS * 8 + 15) & ~15);  // row sets [2], tmem base, abort, first, last
-constexpr uint32_t SMEM_BYTES = SMEM_MISC + 48 + 1024;
+//           ds_full, out_full, mma_done
+constexpr int NUM_BARS = 15;
+constexpr uint32_t SMEM_MISC = SMEM_BAR + NUM_BARS * 8;                 // tmem base, abort, first, last, run again
+constexpr uint32_t SMEM_BYTES = SMEM_MISC + 24 + 1024;
 constexpr uint32_t TMEM_S = 0, TMEM_DP = 128, TMEM_DV = 256, TMEM_DK = 384;
 }  // namespace dkdv
 
@@ -242,24 +247,27 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   auto bar_do_empty = [&](int s) { return bar0 + 8u * (7 + s); };
   const uint32_t bar_s = bar0 + 72u, bar_p = bar0 + 80u, bar_dp = bar0 + 88u, bar_ds = bar0 + 96u;
   const uint32_t bar_out = bar0 + 104u, bar_done = bar0 + 112u;
-  auto bar_clean = [&](int i) { return bar0 + 120u + 8u * (i & 1); };
-  uint32_t* const unclean = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC + 32);
-  volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 36);
-  int* const span = reinterpret_cast<int*>(gbase + SMEM_MISC + 40);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC);
+  volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 4);
+  int* const span = reinterpret_cast<int*>(gbase + SMEM_MISC + 8);
+  volatile uint32_t* const again = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 16);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int k0 = blockIdx.x * BN, kvh = blockIdx.y, batch = blockIdx.z;
   const uint64_t limit = p.wait_limit_ns;
   const int eslot = p.err_slot;
   const int4* const hulls = p.hull + static_cast<long long>(batch) * p.n_qt;
+  auto init_bars = [&] {
+    for (int i = 0; i < NUM_BARS; ++i) mbar_init(bar0 + 8u * i, i == 10 || i == 12 ? WARPS : 1);
+    mbar_fence_init();
+  };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NUM_BARS; ++i) mbar_init(bar0 + 8u * i, i == 10 || i == 12 ? WARPS : i >= 15 ? CLEAN_WARPS : 1);
+    init_bars();
     span[0] = 0x7fffffff;
     span[1] = -1;
     *abort_flag = 0u;
-    mbar_fence_init();
+    *again = 0u;
   }
   __syncthreads();
   // the query tiles, first to last, with a row that sees one of these keys
@@ -294,7 +302,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   }
   const int iters = nt * p.group;
   // whether some row of query tile i does not see all of these keys
-  auto partial_tile = [&](int i) { const int4 h = hulls[i]; return h.z > k0 || h.w < k0 + BN; };
+  auto edge_tile = [&](int i) { const int4 h = hulls[i]; return h.z > k0 || h.w < k0 + BN; };
   if (warp == W_MMA) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -304,6 +312,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  for (int run = 0; run < 2; ++run) {
   if (warp == W_PROD) {
     if (lane == 0) {
       mbar_arrive_expect_tx(bar_kv, 2 * TILE_BYTES);
@@ -340,12 +349,16 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (lane == 0) {
       auto q_tile = [&](int s) { return base + SMEM_Q + s * TILE_BYTES; };
       auto do_tile = [&](int s) { return base + SMEM_DO + s * TILE_BYTES; };
-      // Q and dO are waited for together, as clean
-      bool ok = mma_wait(bar_kv, 0, abort_flag, limit, eslot) && mma_wait(bar_clean(0), 0, abort_flag, limit, eslot);
+      bool ok = mma_wait(bar_kv, 0, abort_flag, limit, eslot) &&
+                mma_wait(bar_q_full(0), 0, abort_flag, limit, eslot);
       if (ok) {
         tc_fence_after();
         issue_abt(tmem + TMEM_S, base + SMEM_K, q_tile(0));
         tc_commit(bar_s);
+        ok = mma_wait(bar_do_full(0), 0, abort_flag, limit, eslot);
+      }
+      if (ok) {
+        tc_fence_after();
         issue_abt(tmem + TMEM_DP, base + SMEM_V, do_tile(0));
         tc_commit(bar_dp);
       }
@@ -354,7 +367,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint32_t par = it & 1, par_next = ((it + 1) >> 1) & 1;
         const bool more = it + 1 < iters;
         // dV(i) and, into the S columns it has just read P from, S(i + 1)
-        if (more ? !mbar_spin2_bounded(bar_p, par, bar_clean(sn), par_next, abort_flag, limit, eslot)
+        if (more ? !mbar_spin2_bounded(bar_p, par, bar_q_full(sn), par_next, abort_flag, limit, eslot)
                  : !mma_wait(bar_p, par, abort_flag, limit, eslot))
           break;
         tc_fence_after();
@@ -365,7 +378,9 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           tc_commit(bar_s);
         }
         // dK(i) and dP(i + 1)
-        if (!mma_wait(bar_ds, par, abort_flag, limit, eslot)) break;
+        if (more ? !mbar_spin2_bounded(bar_ds, par, bar_do_full(sn), par_next, abort_flag, limit, eslot)
+                 : !mma_wait(bar_ds, par, abort_flag, limit, eslot))
+          break;
         tc_fence_after();
         issue_ab(tmem + TMEM_DK, tmem + TMEM_DP, q_tile(s), it > 0);
         tc_commit(bar_q_empty(s));
@@ -380,27 +395,6 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       volatile uint32_t never = 0u;
       mma_wait(bar_done, 0, &never, p.drain_limit_ns, eslot);
     }
-  } else if (warp >= W_CLEAN) {
-    // Every Q and dO tile passes through here (the products wait for `clean`, so
-    // none can be gone before it was seen); only those with masked pairs are
-    // read.  The tile two steps on lands after this one's last use, so two row
-    // sets are enough.
-    int qt = qt0;
-    for (int it = 0; it < iters; ++it) {
-      const int s = it & 1;
-      const bool partial = partial_tile(qt);
-      if (++qt == qt0 + nt) qt = qt0;
-      if (!warp_wait(bar_do_full(s), (it >> 1) & 1, abort_flag, limit, eslot) ||
-          !warp_wait(bar_q_full(s), (it >> 1) & 1, abort_flag, limit, eslot))
-        break;
-      if (partial) {
-        uint32_t* rows = unclean + 4 * s;
-        if (lane < 2) rows[2 * (warp - W_CLEAN) + lane] = 0u;
-        clean_rows(gbase + SMEM_DO + s * TILE_BYTES, warp - W_CLEAN, lane, rows);
-        clean_rows(gbase + SMEM_Q + s * TILE_BYTES, warp - W_CLEAN, lane, rows);
-      }
-      if (lane == 0) mbar_arrive(bar_clean(s));
-    }
   } else {
     const int t0 = lane & 3, t1 = lane >> 2;
     const int lane16 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
@@ -413,22 +407,47 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     int qt = qt0;
     for (int it = 0; ok && it < iters; ++it) {
       const int s = it & 1;
-      const bool partial = partial_tile(qt);
-      if (++qt == qt0 + nt) qt = qt0;
       // this thread's query columns: (lse, D) and intervals of two queries at a time
       const float4* const stat = reinterpret_cast<const float4*>(gbase + SMEM_STAT + s * 1024 + half * 512) + t0;
       const int4* const rng = reinterpret_cast<const int4*>(gbase + SMEM_RNG + s * 1024 + half * 512) + t0;
-      uint32_t bad_lo = 0u, bad_hi = 0u;
-      if (!warp_wait(bar_q_full(s), (it >> 1) & 1, abort_flag, limit, eslot)) { ok = false; break; }
-      if (partial) {
-        if (!warp_wait(bar_clean(s), (it >> 1) & 1, abort_flag, limit, eslot)) { ok = false; break; }
-        const volatile uint32_t* u = unclean + 4 * s + 2 * half;
-        bad_lo = u[0];
-        bad_hi = u[1];
-      }
-      if (!warp_wait(bar_s, it & 1, abort_flag, limit, eslot)) { ok = false; break; }
+      const bool edge = edge_tile(qt);              // some row does not see all of these keys
+      if (++qt == qt0 + nt) qt = qt0;
+      bool partial = false, none = false;           // of this warp's 16 keys x 64 queries
+      bool odd = false;                             // some S or dP in sight is not finite
+      if (!warp_wait(bar_q_full(s), (it >> 1) & 1, abort_flag, limit, eslot) ||
+          !warp_wait(bar_s, it & 1, abort_flag, limit, eslot)) { ok = false; break; }
       tc_fence_after();
       uint32_t sr[32];
+      if (edge) {
+        const int kw = k0 + lane16;
+        const int4 g = (rng - t0)[lane];            // (lo, length) of two of the 64 queries
+        const bool all = max(g.x, g.z) <= kw && min(g.x + g.y, g.z + g.w) >= kw + 16;
+        const bool any = (g.x < kw + 16 && g.x + g.y > kw) || (g.z < kw + 16 && g.z + g.w > kw);
+        partial = !__all_sync(0xffffffffu, all);
+        none = !__any_sync(0xffffffffu, any);
+        if (run == 1) {
+          if (!warp_wait(bar_dp, it & 1, abort_flag, limit, eslot)) { ok = false; break; }
+          tc_fence_after();
+          tmem_ld16x256(t_dp, sr);
+          tmem_wait_ld(sr);
+          odd = any_nonfinite(sr);
+          tmem_ld16x256(t_s, sr);
+          tmem_wait_ld(sr);
+          odd |= any_nonfinite(sr);
+          if (odd) {                                // S(i) and dP(i) have read Q and dO, dV(i) and dK(i) have not
+            zero_nonfinite(gbase + SMEM_Q + s * TILE_BYTES, 64 * half, 64, lane);
+            zero_nonfinite(gbase + SMEM_DO + s * TILE_BYTES, 64 * half, 64, lane);
+          }
+        }
+        if (none) {                                 // P = dS = 0
+          const uint32_t zero[16] = {};
+          publish(t_s, zero, bar_p, lane);
+          if (!warp_wait(bar_dp, it & 1, abort_flag, limit, eslot)) { ok = false; break; }
+          tc_fence_after();
+          publish(t_dp, zero, bar_ds, lane);
+          continue;
+        }
+      }
       tmem_ld16x256(t_s, sr);
       tmem_wait_ld(sr);
       float x[32];                                  // P^T: registers as loaded (4 r: key a, 4 r + 2: key b)
@@ -453,16 +472,20 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           if (!seen(key_a, g.z, g.w)) x[4 * r + 1] = 0.f;
           if (!seen(key_b, g.x, g.y)) x[4 * r + 2] = 0.f;
           if (!seen(key_b, g.z, g.w)) x[4 * r + 3] = 0.f;
-          if ((bad_lo | bad_hi) != 0u) {            // queries with inf or NaN in Q or dO
-            const float nan = __int_as_float(0x7fc00000);
-            if (bit_of(bad_lo, bad_hi, 8 * r + 2 * t0)) {
-              if (seen(key_a, g.x, g.y)) x[4 * r] = nan;
-              if (seen(key_b, g.x, g.y)) x[4 * r + 2] = nan;
-            }
-            if (bit_of(bad_lo, bad_hi, 8 * r + 2 * t0 + 1)) {
-              if (seen(key_a, g.z, g.w)) x[4 * r + 1] = nan;
-              if (seen(key_b, g.z, g.w)) x[4 * r + 3] = nan;
-            }
+        }
+      }
+      if (odd) {                                    // seen pairs that are not finite: dV and dK must not hide them
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+          __syncwarp();
+          tmem_ld16x256(which == 0 ? t_dp : t_s, sr);
+          tmem_wait_ld(sr);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int4 g = rng[4 * (e >> 2)];
+            const int key = (e & 2) ? key_b : key_a, lo = (e & 1) ? g.z : g.x, len = (e & 1) ? g.w : g.y;
+            if (nonfinite(sr[e]) && static_cast<unsigned>(key - lo) < static_cast<unsigned>(len))
+              x[e] = __int_as_float(0x7fc00000);
           }
         }
       }
@@ -498,12 +521,32 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       tc_fence_after();
       const long long r0 = static_cast<long long>(batch) * p.n_k;
       const int col = kvh * HD + 64 * half;
-      store_tile(tmem + lb + TMEM_DV + 64 * half, 1.f, p.dv + r0 * p.dv_stride + col, p.dv_stride, key_a, p.n_k, t0);
-      store_tile(tmem + lb + TMEM_DK + 64 * half, p.scale, p.dk + r0 * p.dk_stride + col, p.dk_stride, key_a, p.n_k, t0);
+      bool finite = store_tile(tmem + lb + TMEM_DV + 64 * half, 1.f, p.dv + r0 * p.dv_stride + col, p.dv_stride,
+                               key_a, p.n_k, t0);
+      finite &= store_tile(tmem + lb + TMEM_DK + 64 * half, p.scale, p.dk + r0 * p.dk_stride + col, p.dk_stride,
+                           key_a, p.n_k, t0);
+      if (!finite && lane == 0) *again = 1u;
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (run == 1 || *again == 0u || *abort_flag != 0u) break;
+  // second run: loads, products and waits of the first have ended; the commits
+  // that nothing waited for arrive, then the barriers start over
+  if (threadIdx.x == 0) {
+    volatile uint32_t never = 0u;
+    for (int s = 0; s < 2; ++s) {
+      const int uses = (iters - s + 1) / 2;
+      if (uses == 0) continue;
+      mbar_wait_bounded(bar_q_empty(s), (uses - 1) & 1, &never, p.drain_limit_ns, eslot);
+      mbar_wait_bounded(bar_do_empty(s), (uses - 1) & 1, &never, p.drain_limit_ns, eslot);
+    }
+    for (int i = 0; i < NUM_BARS; ++i) mbar_inval(bar0 + 8u * i);
+    init_bars();
+  }
+  __syncthreads();
+  tc_fence_after();
+  }
   if (warp == W_MMA) {
     __syncwarp();
     tc_fence_after();
@@ -517,10 +560,10 @@ namespace dq {
 constexpr int SLOTS = 5;                                         // K and V tiles in turn
 constexpr uint32_t SMEM_Q = 0, SMEM_DO = TILE_BYTES, SMEM_KV = 2 * TILE_BYTES;
 constexpr uint32_t SMEM_BAR = SMEM_KV + SLOTS * TILE_BYTES;
-// barriers: q_full, kv_full[5], kv_empty[5], s_full[2], dp_full, ds_full, out_full, mma_done, clean[4]
-constexpr int NUM_BARS = 1 + 2 * SLOTS + 2 + 4 + 4;
-constexpr uint32_t SMEM_MISC = SMEM_BAR + ((NUM_BARS * 8 + 15) & ~15);   // key sets [4], tmem base, abort
-constexpr uint32_t SMEM_BYTES = SMEM_MISC + 80 + 1024;
+// barriers: q_full, kv_full[5], kv_empty[5], s_full[2], dp_full, ds_full, out_full, mma_done
+constexpr int NUM_BARS = 1 + 2 * SLOTS + 2 + 4;
+constexpr uint32_t SMEM_MISC = SMEM_BAR + NUM_BARS * 8;          // tmem base, abort
+constexpr uint32_t SMEM_BYTES = SMEM_MISC + 8 + 1024;
 constexpr uint32_t TMEM_S = 0, TMEM_DP = 256, TMEM_DQ = 384;     // S in two buffers
 }  // namespace dq
 
@@ -540,10 +583,8 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   auto bar_s = [&](int i) { return bar0 + 8u * (1 + 2 * SLOTS + i); };
   const uint32_t bar_dp = bar0 + 8u * (3 + 2 * SLOTS), bar_ds = bar_dp + 8u;
   const uint32_t bar_out = bar_dp + 16u, bar_done = bar_dp + 24u;
-  auto bar_clean = [&](int i) { return bar_dp + 32u + 8u * (i & 3); };
-  uint32_t* const unclean = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC + 64);
-  volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 68);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + SMEM_MISC);
+  volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qt = gridDim.x - 1 - blockIdx.x, head = blockIdx.y, batch = blockIdx.z;
@@ -563,10 +604,10 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   }
   const int tile0 = hull.x / BN, nkv = (hull.y + BN - 1) / BN - tile0;
   // whether some row does not see all keys of the j-th tile
-  auto partial_tile = [&](int j) { return (tile0 + j) * BN < hull.z || (tile0 + j + 1) * BN > hull.w; };
+  auto edge_tile = [&](int j) { return (tile0 + j) * BN < hull.z || (tile0 + j + 1) * BN > hull.w; };
   if (threadIdx.x == 0) {
     for (int i = 0; i < NUM_BARS; ++i)
-      mbar_init(bar0 + 8u * i, i == 4 + 2 * SLOTS ? WARPS : i >= 7 + 2 * SLOTS ? CLEAN_WARPS : 1);
+      mbar_init(bar0 + 8u * i, i == 4 + 2 * SLOTS ? WARPS : 1);
     *abort_flag = 0u;
     mbar_fence_init();
   }
@@ -604,8 +645,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       auto full_wait = [&](int idx) {
         return mma_wait(bar_full(idx % SLOTS), (idx / SLOTS) & 1, abort_flag, limit, eslot);
       };
-      auto k_wait = [&](int j) { return mma_wait(bar_clean(j), (j >> 2) & 1, abort_flag, limit, eslot); };
-      bool ok = mma_wait(bar_q, 0, abort_flag, limit, eslot) && k_wait(0);
+      bool ok = mma_wait(bar_q, 0, abort_flag, limit, eslot) && full_wait(0);
       if (ok) {
         tc_fence_after();
         issue_abt(tmem + TMEM_S, base + SMEM_Q, kv_tile(0));
@@ -622,7 +662,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         const bool more = j + 1 < nkv;
         const int kn = 2 * j + 2, vn = 2 * j + 3;
         if (more) {
-          if (!k_wait(j + 1)) break;
+          if (!full_wait(kn)) break;
           tc_fence_after();
           issue_abt(tmem + TMEM_S + 128 * ((j + 1) & 1), base + SMEM_Q, kv_tile(kn));
           tc_commit(bar_s((j + 1) & 1));
@@ -643,19 +683,6 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
       volatile uint32_t never = 0u;
       mma_wait(bar_done, 0, &never, p.drain_limit_ns, eslot);
     }
-  } else if (warp >= W_CLEAN) {
-    // Every K tile passes through here, as in dkdv.  At most three are in the
-    // ring at once, so four key sets are enough.
-    for (int j = 0; j < nkv; ++j) {
-      const int kidx = 2 * j;
-      if (!warp_wait(bar_full(kidx % SLOTS), (kidx / SLOTS) & 1, abort_flag, limit, eslot)) break;
-      if (partial_tile(j)) {
-        uint32_t* rows = unclean + 4 * (j & 3);
-        if (lane < 2) rows[2 * (warp - W_CLEAN) + lane] = 0u;
-        clean_rows(gbase + SMEM_KV + (kidx % SLOTS) * TILE_BYTES, warp - W_CLEAN, lane, rows);
-      }
-      if (lane == 0) mbar_arrive(bar_clean(j));
-    }
   } else {
     const int t0 = lane & 3, t1 = lane >> 2;
     const int lane16 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
@@ -675,20 +702,28 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     bool ok = true;
     for (int j = 0; ok && j < nkv; ++j) {
       const int key0 = (tile0 + j) * BN;
-      const bool partial = partial_tile(j);
       const uint32_t t_s = tmem + lb + TMEM_S + 128 * (j & 1) + 64 * half;
-      uint32_t bad_lo = 0u, bad_hi = 0u;
+      bool partial = false, odd = false;            // of this warp's 16 rows x 64 keys
       if (!warp_wait(bar_s(j & 1), (j >> 1) & 1, abort_flag, limit, eslot)) { ok = false; break; }
-      if (partial) {                                // S(j) was read from a clean K(j)
-        if (!warp_wait(bar_clean(j), (j >> 2) & 1, abort_flag, limit, eslot)) { ok = false; break; }
-        const volatile uint32_t* u = unclean + 4 * (j & 3) + 2 * half;
-        bad_lo = u[0];
-        bad_hi = u[1];
-      }
       tc_fence_after();
       uint32_t sr[32];
       tmem_ld16x256(t_s, sr);
       tmem_wait_ld(sr);
+      if (edge_tile(j)) {
+        const int kw = key0 + 64 * half;
+        const bool all = max(rng_a.x, rng_b.x) <= kw && min(rng_a.x + rng_a.y, rng_b.x + rng_b.y) >= kw + 64;
+        const bool any = (rng_a.x < kw + 64 && rng_a.x + rng_a.y > kw) || (rng_b.x < kw + 64 && rng_b.x + rng_b.y > kw);
+        partial = !__all_sync(0xffffffffu, all);
+        odd = any_nonfinite(sr);                    // S(j) has read K(j), dQ(j) has not
+        if (odd) zero_nonfinite(gbase + SMEM_KV + ((2 * j) % SLOTS) * TILE_BYTES, 64 * half, 64, lane);
+        if (!__any_sync(0xffffffffu, any)) {        // dS = 0
+          const uint32_t zero[16] = {};
+          if (!warp_wait(bar_dp, j & 1, abort_flag, limit, eslot)) { ok = false; break; }
+          tc_fence_after();
+          publish(t_s, zero, bar_ds, lane);
+          continue;
+        }
+      }
       float x[32];                                  // P, then dS (4 r: row a, 4 r + 2: row b)
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
@@ -698,6 +733,11 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
         x[4 * r + 1] = ex2_approx(ya.y);
         x[4 * r + 2] = ex2_approx(yb.x);
         x[4 * r + 3] = ex2_approx(yb.y);
+      }
+      if (odd) {                                    // a seen pair with a non-finite S: its dS, whatever P is
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (nonfinite(sr[e])) x[e] = __int_as_float(0x7fc00000);
       }
       if (!warp_wait(bar_dp, j & 1, abort_flag, limit, eslot)) { ok = false; break; }
       tc_fence_after();
@@ -724,15 +764,6 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
           const bool seen = ((e >> 1) & 1) ? static_cast<unsigned>(off_b + k) < len_b
                                            : static_cast<unsigned>(off_a + k) < len_a;
           if (!seen) x[e] = 0.f;
-        }
-        if ((bad_lo | bad_hi) != 0u) {              // keys with inf or NaN in K
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int k = 8 * (e >> 2) + (e & 1);
-            const bool seen = ((e >> 1) & 1) ? static_cast<unsigned>(off_b + k) < len_b
-                                             : static_cast<unsigned>(off_a + k) < len_a;
-            if (seen && bit_of(bad_lo, bad_hi, k + 2 * t0)) x[e] = __int_as_float(0x7fc00000);
-          }
         }
       }
       uint32_t pk[16];

@@ -52,7 +52,7 @@ const DeviceState* device_state() {
     if (cudaFuncSetAttribute(h3::attn::attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(h3::attn::SMEM_BYTES)) != cudaSuccess ||
         cudaFuncSetAttribute(h3::attn::attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(h3::attn::SMEM_BYTES)) != cudaSuccess ||
+                             static_cast<int>(h3::attn::MASKED_SMEM_BYTES)) != cudaSuccess ||
         cudaFuncSetAttribute(h3::attn_bwd::dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(h3::attn_bwd::dkdv::SMEM_BYTES)) != cudaSuccess ||
         cudaFuncSetAttribute(h3::attn_bwd::dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -204,7 +204,7 @@ h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v,
   p.err_slot = error_slot(stream);
   const dim3 grid(static_cast<unsigned>((a->n_q + 2 * h3::attn::BM - 1) / (2 * h3::attn::BM)),
                   static_cast<unsigned>(a->n_heads), static_cast<unsigned>(a->batch));
-  h3::attn::attention_kernel<true><<<grid, h3::attn::MASKED_THREADS, h3::attn::SMEM_BYTES, as_stream(stream)>>>(tq, tk, tv, p);
+  h3::attn::attention_kernel<true><<<grid, h3::attn::THREADS, h3::attn::MASKED_SMEM_BYTES, as_stream(stream)>>>(tq, tk, tv, p);
   return launched();
 }
 
