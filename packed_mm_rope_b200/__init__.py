@@ -36,8 +36,12 @@ load = _lib.load
 
 def _stream(stream=None) -> int:
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # ~3 us less than building a Stream object
+    if raw is not None:
+        return raw(torch.cuda.current_device())
+    return int(torch.cuda.current_stream().cuda_stream)
 
 
 def _on_device(t, what: str) -> None:
@@ -262,16 +266,59 @@ def adaln_modulate(x, timestep_index, token_tag, table, out=None, eps: float = 1
 
 
 # ------------------------------------------------ masks, grouped heads, training --
+#
+# These calls are short against a Python interpreter (some kernels take 2 us), so
+# the checks below read each attribute of a tensor once.
 
 MASK_MODES = {"document": _lib.H3_MASK_DOCUMENT, "prefix_causal": _lib.H3_MASK_PREFIX_CAUSAL,
               "prefix_block": _lib.H3_MASK_PREFIX_BLOCK}
 
 
-def _allocate_on(stream):
-    """Context in which tensors are allocated for use on ``stream`` (None: the current one)."""
-    import contextlib
+def _empty(stream, *args, **kw):
+    """torch.empty for use on ``stream`` (None: the current one)."""
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return torch.empty(*args, **kw)
+    with torch.cuda.stream(stream):
+        return torch.empty(*args, **kw)
+
+
+def _empty_like(x, stream):
+    """A contiguous tensor shaped as ``x`` for use on ``stream`` (None: the current one)."""
+    import torch
+    if stream is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _heads(x, dev: int, what: str):
+    """(batch, n_rows, n_heads, row_stride) of a [.., N, H, 128] bf16 view on device ``dev``."""
+    import torch
+    shape, stride = x.shape, x.stride()
+    if x.dtype is not torch.bfloat16 or x.get_device() != dev:
+        raise TypeError(f"{what} must be a bf16 tensor on the current CUDA device")
+    if len(shape) == 3:
+        n, h, d = shape
+        rs, hs, ds = stride
+        b = 1
+    elif len(shape) == 4:
+        b, n, h, d = shape
+        bs, rs, hs, ds = stride
+        if b > 1 and bs != n * rs:
+            raise ValueError(f"{what}: the batch stride must be n_rows * row_stride")
+    else:
+        raise ValueError(f"{what} must be [N, H, 128] or [B, N, H, 128]")
+    if d != 128 or ds != 1 or hs != 128:
+        raise ValueError(f"{what} must be [N, H, 128] or [B, N, H, 128] with heads contiguous")
+    return b, n, h, (rs if n > 1 or b > 1 else max(rs, 128 * h))
+
+
+def _plain(t, dev: int, dtype, numel: int, what: str) -> int:
+    """data_ptr of a contiguous tensor of ``numel`` elements of ``dtype`` on device ``dev``."""
+    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {numel} elements on the current CUDA device")
+    return t.data_ptr()
 
 
 def mmrope_rotate(q, k, coords, q_out=None, k_out=None, inverse: bool = False, theta=10000.0,
@@ -283,33 +330,31 @@ def mmrope_rotate(q, k, coords, q_out=None, k_out=None, inverse: bool = False, t
     Q and K to those of the unrotated ones.  Pass q_out=q, k_out=k for in place.
     """
     import torch
+    dev = torch.cuda.current_device()
     rows = None
-    ptr, heads, stride, out_stride, outs = [0, 0], [0, 0], [0, 0], [0, 0], [None, None]
+    ptr, out_ptr, heads, stride, out_stride, outs = [0, 0], [0, 0], [0, 0], [0, 0], [0, 0], [None, None]
     for i, (x, out) in enumerate(((q, q_out), (k, k_out))):
         if x is None:
             if out is not None:
                 raise ValueError("an output without its input")
             continue
-        b, n, heads[i], stride[i] = _row_layout(x)
+        b, n, h, stride[i] = _heads(x, dev, "q and k")
         if rows is not None and rows != (b, n):
             raise ValueError("q and k differ in their rows")
         rows = (b, n)
         if out is None:
-            with _allocate_on(stream):
-                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        ob, on, oh, out_stride[i] = _row_layout(out)
-        if (ob, on, oh) != (b, n, heads[i]):
-            raise ValueError("outputs must have the inputs' shape")
-        ptr[i], outs[i] = x.data_ptr(), out
+            out = _empty_like(x, stream)
+            out_stride[i] = 128 * h
+        else:
+            ob, on, oh, out_stride[i] = _heads(out, dev, "outputs")
+            if (ob, on, oh) != (b, n, h):
+                raise ValueError("outputs must have the inputs' shape")
+        ptr[i], out_ptr[i], heads[i], outs[i] = x.data_ptr(), out.data_ptr(), h, out
     if rows is None:
         raise ValueError("neither q nor k given")
     n = rows[0] * rows[1]
-    if coords.dtype != torch.float32 or coords.numel() != 3 * n or not coords.is_contiguous():
-        raise ValueError("coords must be contiguous fp32 [rows, 3]")
-    _on_device(coords, "coords")
-    h3_mmrope_rotate(ptr[0], ptr[1], outs[0].data_ptr() if outs[0] is not None else 0,
-                     outs[1].data_ptr() if outs[1] is not None else 0, coords.data_ptr(), n, heads[0], heads[1],
-                     stride[0], stride[1], out_stride[0], out_stride[1],
+    h3_mmrope_rotate(ptr[0], ptr[1], out_ptr[0], out_ptr[1], _plain(coords, dev, torch.float32, 3 * n, "coords"), n,
+                     heads[0], heads[1], stride[0], stride[1], out_stride[0], out_stride[1],
                      rope_cfg(theta, 128, sections, pair_layout, freq_rule), inverse, _stream(stream))
     return outs[0], outs[1]
 
@@ -323,41 +368,36 @@ def build_key_ranges(doc_starts, n_rows: int, mode: str = "document", prefix=Non
     attend to the prefix, the others to the whole document).  Rows in no document get (0, 0).
     """
     import torch
-    if mode not in MASK_MODES:
+    code = MASK_MODES.get(mode)
+    if code is None:
         raise ValueError(f"mode must be one of {sorted(MASK_MODES)}")
-    if doc_starts.dtype != torch.int32 or doc_starts.dim() != 1 or doc_starts.numel() < 1 \
-            or not doc_starts.is_contiguous():
-        raise ValueError("doc_starts must be a contiguous int32 [documents + 1] tensor")
-    _on_device(doc_starts, "doc_starts")
+    dev = torch.cuda.current_device()
     n_docs = doc_starts.numel() - 1
-    if prefix is not None:
-        _exact(prefix, torch.int32, (n_docs,), "prefix")
-        _on_device(prefix, "prefix")
+    if n_docs < 0 or doc_starts.dim() != 1:
+        raise ValueError("doc_starts must be a contiguous int32 [documents + 1] tensor")
+    starts = _plain(doc_starts, dev, torch.int32, n_docs + 1, "doc_starts")
+    lengths = _plain(prefix, dev, torch.int32, n_docs, "prefix") if prefix is not None else 0
     if out is None:
-        with _allocate_on(stream):
-            out = torch.empty((n_rows, 2), dtype=torch.int32, device=doc_starts.device)
-    _exact(out, torch.int32, (n_rows, 2), "out")
-    _on_device(out, "out")
-    h3_build_key_ranges(doc_starts.data_ptr(), prefix.data_ptr() if prefix is not None else 0, n_docs, n_rows,
-                        MASK_MODES[mode], out.data_ptr(), _stream(stream))
+        out = _empty(stream, (n_rows, 2), dtype=torch.int32, device=doc_starts.device)
+    h3_build_key_ranges(starts, lengths, n_docs, n_rows, code, _plain(out, dev, torch.int32, 2 * n_rows, "out"),
+                        _stream(stream))
     return out
 
 
-def _masked_shape(q, k, v, key_ranges, softmax_scale):
-    """(shape struct, strides of q, k, v) of a masked attention problem, its tensors checked."""
+def _masked_shape(q, k, v, key_ranges, softmax_scale, dev: int):
+    """(shape struct, strides of q, k, v, pointer of key_ranges) of a masked attention problem, checked."""
     import torch
-    b, n, h, qs = _row_layout(q)
-    kb, nk, hk, ks = _row_layout(k)
-    vb, nv, hv, vs = _row_layout(v)
-    if (vb, nv, hv) != (kb, nk, hk) or kb != b:
+    b, n, h, qs = _heads(q, dev, "q")
+    kb, nk, hk, ks = _heads(k, dev, "k")
+    vb, nv, hv, vs = _heads(v, dev, "v")
+    if vb != kb or nv != nk or hv != hk or kb != b:
         raise ValueError("k and v must have one shape and q's batch")
     if h < 1 or hk < 1 or h % hk:
         raise ValueError("the query heads must be a multiple of the K/V heads")
-    if key_ranges.dtype != torch.int32 or key_ranges.numel() != 2 * b * n or not key_ranges.is_contiguous() \
-            or key_ranges.shape[-1] != 2:
+    if key_ranges.dim() < 2 or key_ranges.shape[-1] != 2:
         raise ValueError("key_ranges must be contiguous int32 [rows, 2]")
-    _on_device(key_ranges, "key_ranges")
-    return h3_attn_shape(n, nk, b, h, hk, 128, softmax_scale), qs, ks, vs
+    r = _plain(key_ranges, dev, torch.int32, 2 * b * n, "key_ranges")
+    return h3_attn_shape(n, nk, b, h, hk, 128, softmax_scale), qs, ks, vs, r
 
 
 def masked_attention(q, k, v, key_ranges, out=None, lse=None, softmax_scale: float = 0.0, stream=None):
@@ -369,21 +409,18 @@ def masked_attention(q, k, v, key_ranges, out=None, lse=None, softmax_scale: flo
     if given (``masked_attention_backward`` needs it).
     """
     import torch
-    shape, qs, ks, vs = _masked_shape(q, k, v, key_ranges, softmax_scale)
+    dev = torch.cuda.current_device()
+    shape, qs, ks, vs, r = _masked_shape(q, k, v, key_ranges, softmax_scale, dev)
+    b, n, h = shape.batch, shape.n_q, shape.n_heads
     if out is None:
-        with _allocate_on(stream):
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    b, n, h, os_ = _row_layout(out)
-    if (b, n, h) != (shape.batch, shape.n_q, shape.n_heads):
-        raise ValueError("output must have q's shape")
-    lp = 0
-    if lse is not None:
-        if lse.dtype != torch.float32 or lse.numel() != b * h * n or not lse.is_contiguous():
-            raise ValueError("lse must be contiguous fp32 [B, H, Nq]")
-        _on_device(lse, "lse")
-        lp = lse.data_ptr()
-    h3_masked_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, key_ranges.data_ptr(), shape,
-                        qs, ks, vs, os_, _stream(stream))
+        out, os_ = _empty_like(q, stream), 128 * h
+    else:
+        ob, on, oh, os_ = _heads(out, dev, "out")
+        if (ob, on, oh) != (b, n, h):
+            raise ValueError("output must have q's shape")
+    lp = _plain(lse, dev, torch.float32, b * h * n, "lse") if lse is not None else 0
+    h3_masked_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, r, shape, qs, ks, vs, os_,
+                        _stream(stream))
     return out
 
 
@@ -395,49 +432,53 @@ def masked_attention_backward(dout, q, k, v, out, lse, key_ranges, dq=None, dk=N
     ``h3_masked_attention_backward_workspace_bytes`` bytes, one per call that may overlap in time.
     """
     import torch
-    shape, qs, ks, vs = _masked_shape(q, k, v, key_ranges, softmax_scale)
-    with _allocate_on(stream):
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-        dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
-    strides = {"q": qs, "k": ks, "v": vs}
-    for name, t, n, h in (("o", out, shape.n_q, shape.n_heads), ("dout", dout, shape.n_q, shape.n_heads),
-                          ("dq", dq, shape.n_q, shape.n_heads), ("dk", dk, shape.n_k, shape.n_kv_heads),
-                          ("dv", dv, shape.n_k, shape.n_kv_heads)):
-        b, rows, heads, strides[name] = _row_layout(t)
-        if (b, rows, heads) != (shape.batch, n, h):
-            raise ValueError(f"{name} must be shaped as the tensor it belongs to")
-    if lse.dtype != torch.float32 or lse.numel() != shape.batch * shape.n_heads * shape.n_q or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous fp32 [B, H, Nq]")
-    _on_device(lse, "lse")
+    dev = torch.cuda.current_device()
+    shape, qs, ks, vs, r = _masked_shape(q, k, v, key_ranges, softmax_scale, dev)
+    b, n, h, nk, hk = shape.batch, shape.n_q, shape.n_heads, shape.n_k, shape.n_kv_heads
+
+    def grad(t, x, rows, heads, what):
+        if t is None:
+            return _empty_like(x, stream), 128 * heads
+        tb, tn, th, ts = _heads(t, dev, what)
+        if (tb, tn, th) != (b, rows, heads):
+            raise ValueError(f"{what} must be shaped as the tensor it belongs to")
+        return t, ts
+
+    _, dos = grad(dout, q, n, h, "dout")
+    _, os_ = grad(out, q, n, h, "out")
+    dq, dqs = grad(dq, q, n, h, "dq")
+    dk, dks = grad(dk, k, nk, hk, "dk")
+    dv, dvs = grad(dv, v, nk, hk, "dv")
+    lp = _plain(lse, dev, torch.float32, b * h * n, "lse")
     workspace = _workspace(workspace, h3_masked_attention_backward_workspace_bytes(shape), q.device, stream)
-    h3_masked_attention_backward(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                 lse.data_ptr(), key_ranges.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                 workspace.data_ptr(), shape, h3_attn_strides(**strides), _stream(stream))
+    h3_masked_attention_backward(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, r,
+                                 dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), shape,
+                                 h3_attn_strides(qs, ks, vs, os_, dos, dqs, dks, dvs), _stream(stream))
     return dq, dk, dv
 
 
-def _dtype_code(t, what: str) -> int:
+def _dtype_code(dtype, what: str) -> int:
     import torch
-    codes = {torch.bfloat16: _lib.H3_DTYPE_BF16, torch.float16: _lib.H3_DTYPE_F16, torch.float32: _lib.H3_DTYPE_F32}
-    if t.dtype not in codes:
+    code = (_lib.H3_DTYPE_BF16 if dtype is torch.bfloat16 else _lib.H3_DTYPE_F32 if dtype is torch.float32
+            else _lib.H3_DTYPE_F16 if dtype is torch.float16 else None)
+    if code is None:
         raise ValueError(f"{what} must be bf16, fp16 or fp32")
-    return codes[t.dtype]
+    return code
 
 
-def _norm_rows(t, n: int, c: int, dtype, what: str) -> int:
+def _norm_rows(t, n: int, c: int, dtype, dev: int, what: str) -> int:
     """Row stride of an [n, c] tensor with unit inner stride."""
-    if t.dtype != dtype or tuple(t.shape) != (n, c) or (c > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < c):
-        raise ValueError(f"{what} must be a {dtype} [{n}, {c}] tensor with unit inner stride")
-    _on_device(t, what)
-    return t.stride(0) if n > 1 else max(c, t.stride(0))
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not dtype or len(shape) != 2 or shape[0] != n or shape[1] != c or (c > 1 and stride[1] != 1) \
+            or (n > 1 and stride[0] < c) or t.get_device() != dev:
+        raise ValueError(f"{what} must be a {dtype} [{n}, {c}] tensor with unit inner stride on the current CUDA device")
+    return stride[0] if n > 1 else max(c, stride[0])
 
 
 def _workspace(workspace, need: int, device, stream):
     import torch
     if workspace is None:
-        with _allocate_on(stream):
-            return torch.empty(need, dtype=torch.uint8, device=device)
+        return _empty(stream, need, dtype=torch.uint8, device=device)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes")
     _on_device(workspace, "workspace")
@@ -453,26 +494,28 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None
     import torch
     if x.dim() != 2:
         raise ValueError("x must be [N, C]")
+    dev = torch.cuda.current_device()
     n, c = x.shape
-    dt = _dtype_code(x, "x")
-    xs = _norm_rows(x, n, c, x.dtype, "x")
-    pdt = dt
-    for t, what in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            pdt = _dtype_code(t, what)
-            _exact(t, (weight if weight is not None else bias).dtype, (c,), what)
-            _on_device(t, what)
-    with _allocate_on(stream):
-        out = torch.empty((n, c), dtype=x.dtype, device=x.device) if out is None else out
-        mean = torch.empty(n, dtype=torch.float32, device=x.device) if mean is None else mean
-        rstd = torch.empty(n, dtype=torch.float32, device=x.device) if rstd is None else rstd
-    ys = _norm_rows(out, n, c, x.dtype, "out")
-    for t, what in ((mean, "mean"), (rstd, "rstd")):
-        _exact(t, torch.float32, (n,), what)
-        _on_device(t, what)
-    h3_layernorm(x.data_ptr(), out.data_ptr(), weight.data_ptr() if weight is not None else 0,
-                 bias.data_ptr() if bias is not None else 0, mean.data_ptr(), rstd.data_ptr(), n, c, xs, ys, dt, pdt,
-                 eps, _stream(stream))
+    dtype = x.dtype
+    dt = pdt = _dtype_code(dtype, "x")
+    xs = _norm_rows(x, n, c, dtype, dev, "x")
+    wp = bp = 0
+    if weight is not None:
+        pdt = _dtype_code(weight.dtype, "weight")
+        wp = _plain(weight, dev, weight.dtype, c, "weight")
+    if bias is not None:
+        pdt = _dtype_code(bias.dtype, "bias")
+        bp = _plain(bias, dev, bias.dtype if weight is None else weight.dtype, c, "bias")
+    if out is None:
+        out, ys = _empty_like(x, stream), c
+    else:
+        ys = _norm_rows(out, n, c, dtype, dev, "out")
+    if mean is None:
+        mean = _empty(stream, n, dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = _empty(stream, n, dtype=torch.float32, device=x.device)
+    h3_layernorm(x.data_ptr(), out.data_ptr(), wp, bp, _plain(mean, dev, torch.float32, n, "mean"),
+                 _plain(rstd, dev, torch.float32, n, "rstd"), n, c, xs, ys, dt, pdt, eps, _stream(stream))
     return out, mean, rstd
 
 
@@ -481,37 +524,37 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, param_dtype=None, dx=Non
     """(dx, dweight, dbias) of ``layer_norm``; dweight and dbias are None without ``param_grads``.
 
     The parameter gradients have the weight's type (``param_dtype``, or fp32, without a weight).
+    Pass dx=dy (or x) for in place.
     """
     import torch
     if x.dim() != 2:
         raise ValueError("x must be [N, C]")
+    dev = torch.cuda.current_device()
     n, c = x.shape
-    dt = _dtype_code(x, "x")
-    xs, dys = _norm_rows(x, n, c, x.dtype, "x"), _norm_rows(dy, n, c, x.dtype, "dy")
-    for t, what in ((mean, "mean"), (rstd, "rstd")):
-        _exact(t, torch.float32, (n,), what)
-        _on_device(t, what)
+    dtype = x.dtype
+    dt = _dtype_code(dtype, "x")
+    xs, dys = _norm_rows(x, n, c, dtype, dev, "x"), _norm_rows(dy, n, c, dtype, dev, "dy")
+    mp, rp = _plain(mean, dev, torch.float32, n, "mean"), _plain(rstd, dev, torch.float32, n, "rstd")
+    wp = 0
     if weight is not None:
-        _exact(weight, weight.dtype, (c,), "weight")
-        _on_device(weight, "weight")
         param_dtype = weight.dtype
+        wp = _plain(weight, dev, param_dtype, c, "weight")
+    elif param_dtype is None:
+        param_dtype = torch.float32
+    pdt = _dtype_code(param_dtype, "weight")
+    if dx is None:
+        dx, dxs = _empty_like(x, stream), c
     else:
-        param_dtype = param_dtype or torch.float32
+        dxs = _norm_rows(dx, n, c, dtype, dev, "dx")
     dw = db = None
-    with _allocate_on(stream):
-        dx = torch.empty((n, c), dtype=x.dtype, device=x.device) if dx is None else dx
-        if param_grads:
-            dw = torch.empty(c, dtype=param_dtype, device=x.device)
-            db = torch.empty(c, dtype=param_dtype, device=x.device)
-            pdt = _dtype_code(dw, "weight")
-            workspace = _workspace(workspace, h3_layernorm_backward_workspace_bytes(n, c), x.device, stream)
-        else:
-            pdt = _dtype_code(weight, "weight") if weight is not None else dt
-    dxs = _norm_rows(dx, n, c, x.dtype, "dx")
-    h3_layernorm_backward(dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                          weight.data_ptr() if weight is not None else 0, dx.data_ptr(),
-                          dw.data_ptr() if param_grads else 0, db.data_ptr() if param_grads else 0,
-                          workspace.data_ptr() if param_grads else 0, n, c, dys, xs, dxs, dt, pdt, _stream(stream))
+    dwp = dbp = work = 0
+    if param_grads:
+        dw = _empty(stream, c, dtype=param_dtype, device=x.device)
+        db = _empty(stream, c, dtype=param_dtype, device=x.device)
+        workspace = _workspace(workspace, h3_layernorm_backward_workspace_bytes(n, c), x.device, stream)
+        dwp, dbp, work = dw.data_ptr(), db.data_ptr(), workspace.data_ptr()
+    h3_layernorm_backward(dy.data_ptr(), x.data_ptr(), mp, rp, wp, dx.data_ptr(), dwp, dbp, work, n, c, dys, xs, dxs,
+                          dt, pdt, _stream(stream))
     return dx, dw, db
 
 
@@ -523,30 +566,28 @@ def adaln_modulate_backward(dy, x, timestep_index, token_tag, table, eps: float 
     computed again from x.  Pass dx=dy (or x) for in place.
     """
     import torch
-    if x.dim() != 2:
-        raise ValueError("x must be [N, C]")
+    if x.dim() != 2 or table.dim() != 3:
+        raise ValueError("x must be [N, C] and table [E, 2, C]")
+    dev = torch.cuda.current_device()
     n, c = x.shape
-    xs, dys = _norm_rows(x, n, c, torch.bfloat16, "x"), _norm_rows(dy, n, c, torch.bfloat16, "dy")
-    for t in (timestep_index, token_tag):
-        if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
-            raise ValueError("indices must be contiguous CUDA int32 [N]")
-        _on_device(t, "indices")
-    if table.dim() != 3:
+    e, two, tc = table.shape
+    if two != 2 or tc != c:
         raise ValueError("table must be [E, 2, C]")
-    e = table.shape[0]
-    _exact(table, torch.float32, (e, 2, c), "table")
-    _on_device(table, "table")
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    xs, dys = _norm_rows(x, n, c, bf16, dev, "x"), _norm_rows(dy, n, c, bf16, dev, "dy")
+    ts, tags = _plain(timestep_index, dev, i32, n, "timestep_index"), _plain(token_tag, dev, i32, n, "token_tag")
+    tp = _plain(table, dev, f32, 2 * e * c, "table")
     need = h3_adaln_backward_workspace_bytes(n, c, e)
     if need == 0:
         raise ValueError("hidden must be a multiple of 8 up to 8192, with 1 to 8192 table entries")
-    with _allocate_on(stream):
-        dx = torch.empty((n, c), dtype=x.dtype, device=x.device) if dx is None else dx
-        dtable = torch.empty((e, 2, c), dtype=torch.float32, device=x.device) if dtable is None else dtable
-    _exact(dtable, torch.float32, (e, 2, c), "dtable")
-    _on_device(dtable, "dtable")
+    if dx is None:
+        dx, dxs = _empty_like(x, stream), c
+    else:
+        dxs = _norm_rows(dx, n, c, bf16, dev, "dx")
+    if dtable is None:
+        dtable = _empty(stream, (e, 2, c), dtype=f32, device=x.device)
     workspace = _workspace(workspace, need, x.device, stream)
-    dxs = _norm_rows(dx, n, c, torch.bfloat16, "dx")
-    h3_adaln_modulate_backward(dy.data_ptr(), x.data_ptr(), timestep_index.data_ptr(), token_tag.data_ptr(),
-                               table.data_ptr(), dx.data_ptr(), dtable.data_ptr(), workspace.data_ptr(), e, n, c,
-                               dys, xs, dxs, eps, _stream(stream))
+    h3_adaln_modulate_backward(dy.data_ptr(), x.data_ptr(), ts, tags, tp, dx.data_ptr(),
+                               _plain(dtable, dev, f32, 2 * e * c, "dtable"), workspace.data_ptr(), e, n, c, dys, xs,
+                               dxs, eps, _stream(stream))
     return dx, dtable

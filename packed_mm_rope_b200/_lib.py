@@ -212,22 +212,22 @@ def h3_adaln_modulate(d_x: int, d_y: int, d_ts: int, d_tags: int, d_table: int, 
 def h3_mmrope_rotate(d_q: int, d_k: int, d_q_out: int, d_k_out: int, d_coords: int, n_rows: int, n_heads: int,
                      n_kv_heads: int, q_stride: int, k_stride: int, q_out_stride: int, k_out_stride: int,
                      cfg: h3_rope_cfg, inverse: bool = False, stream: int = 0) -> None:
-    _check(load().h3_mmrope_rotate(d_q or None, d_k or None, d_q_out or None, d_k_out or None, d_coords or None,
+    _check(load().h3_mmrope_rotate(d_q, d_k, d_q_out, d_k_out, d_coords,
                                    n_rows, n_heads, n_kv_heads, q_stride, k_stride, q_out_stride, k_out_stride,
-                                   ctypes.byref(cfg), int(inverse), stream or None), "h3_mmrope_rotate")
+                                   ctypes.byref(cfg), int(inverse), stream), "h3_mmrope_rotate")
 
 
 def h3_build_key_ranges(d_doc_starts: int, d_prefix: int, n_docs: int, n_rows: int, mode: int, d_ranges: int,
                         stream: int = 0) -> None:
-    _check(load().h3_build_key_ranges(d_doc_starts or None, d_prefix or None, n_docs, n_rows, mode, d_ranges or None,
-                                      stream or None), "h3_build_key_ranges")
+    _check(load().h3_build_key_ranges(d_doc_starts, d_prefix, n_docs, n_rows, mode, d_ranges,
+                                      stream), "h3_build_key_ranges")
 
 
 def h3_masked_attention(d_q: int, d_k: int, d_v: int, d_o: int, d_lse: int, d_ranges: int, shape: h3_attn_shape,
                         q_stride: int, k_stride: int, v_stride: int, o_stride: int, stream: int = 0) -> None:
-    _check(load().h3_masked_attention(d_q or None, d_k or None, d_v or None, d_o or None, d_lse or None,
-                                      d_ranges or None, ctypes.byref(shape), q_stride, k_stride, v_stride, o_stride,
-                                      stream or None), "h3_masked_attention")
+    _check(load().h3_masked_attention(d_q, d_k, d_v, d_o, d_lse,
+                                      d_ranges, ctypes.byref(shape), q_stride, k_stride, v_stride, o_stride,
+                                      stream), "h3_masked_attention")
 
 
 def h3_masked_attention_backward_workspace_bytes(shape: h3_attn_shape) -> int:
@@ -237,18 +237,18 @@ def h3_masked_attention_backward_workspace_bytes(shape: h3_attn_shape) -> int:
 def h3_masked_attention_backward(d_do: int, d_q: int, d_k: int, d_v: int, d_o: int, d_lse: int, d_ranges: int,
                                  d_dq: int, d_dk: int, d_dv: int, d_work: int, shape: h3_attn_shape,
                                  strides: h3_attn_strides, stream: int = 0) -> None:
-    _check(load().h3_masked_attention_backward(d_do or None, d_q or None, d_k or None, d_v or None, d_o or None,
-                                               d_lse or None, d_ranges or None, d_dq or None, d_dk or None,
-                                               d_dv or None, d_work or None, ctypes.byref(shape),
-                                               ctypes.byref(strides), stream or None), "h3_masked_attention_backward")
+    _check(load().h3_masked_attention_backward(d_do, d_q, d_k, d_v, d_o,
+                                               d_lse, d_ranges, d_dq, d_dk,
+                                               d_dv, d_work, ctypes.byref(shape),
+                                               ctypes.byref(strides), stream), "h3_masked_attention_backward")
 
 
 def h3_layernorm(d_x: int, d_y: int, d_weight: int, d_bias: int, d_mean: int, d_rstd: int, n_rows: int, hidden: int,
                  x_row_stride: int, y_row_stride: int, dtype: int = 0, param_dtype: int = 2, eps: float = 1e-5,
                  stream: int = 0) -> None:
-    _check(load().h3_layernorm(d_x or None, d_y or None, d_weight or None, d_bias or None, d_mean or None,
-                               d_rstd or None, n_rows, hidden, x_row_stride, y_row_stride, dtype, param_dtype, eps,
-                               stream or None), "h3_layernorm")
+    _check(load().h3_layernorm(d_x, d_y, d_weight, d_bias, d_mean,
+                               d_rstd, n_rows, hidden, x_row_stride, y_row_stride, dtype, param_dtype, eps,
+                               stream), "h3_layernorm")
 
 
 def h3_layernorm_backward_workspace_bytes(n_rows: int, hidden: int) -> int:
@@ -258,10 +258,10 @@ def h3_layernorm_backward_workspace_bytes(n_rows: int, hidden: int) -> int:
 def h3_layernorm_backward(d_dy: int, d_x: int, d_mean: int, d_rstd: int, d_weight: int, d_dx: int, d_dweight: int,
                           d_dbias: int, d_work: int, n_rows: int, hidden: int, dy_row_stride: int, x_row_stride: int,
                           dx_row_stride: int, dtype: int = 0, param_dtype: int = 2, stream: int = 0) -> None:
-    _check(load().h3_layernorm_backward(d_dy or None, d_x or None, d_mean or None, d_rstd or None, d_weight or None,
-                                        d_dx or None, d_dweight or None, d_dbias or None, d_work or None, n_rows,
+    _check(load().h3_layernorm_backward(d_dy, d_x, d_mean, d_rstd, d_weight,
+                                        d_dx, d_dweight, d_dbias, d_work, n_rows,
                                         hidden, dy_row_stride, x_row_stride, dx_row_stride, dtype, param_dtype,
-                                        stream or None), "h3_layernorm_backward")
+                                        stream), "h3_layernorm_backward")
 
 
 def h3_adaln_backward_workspace_bytes(n_rows: int, hidden: int, n_entries: int) -> int:
@@ -271,10 +271,10 @@ def h3_adaln_backward_workspace_bytes(n_rows: int, hidden: int, n_entries: int) 
 def h3_adaln_modulate_backward(d_dy: int, d_x: int, d_ts: int, d_tags: int, d_table: int, d_dx: int, d_dtable: int,
                                d_work: int, n_entries: int, n_rows: int, hidden: int, dy_row_stride: int,
                                x_row_stride: int, dx_row_stride: int, eps: float = 1e-6, stream: int = 0) -> None:
-    _check(load().h3_adaln_modulate_backward(d_dy or None, d_x or None, d_ts or None, d_tags or None, d_table or None,
-                                             d_dx or None, d_dtable or None, d_work or None, n_entries, n_rows,
+    _check(load().h3_adaln_modulate_backward(d_dy, d_x, d_ts, d_tags, d_table,
+                                             d_dx, d_dtable, d_work, n_entries, n_rows,
                                              hidden, dy_row_stride, x_row_stride, dx_row_stride, eps,
-                                             stream or None), "h3_adaln_modulate_backward")
+                                             stream), "h3_adaln_modulate_backward")
 
 
 def h3_check_device_error(stream: int = 0) -> int:

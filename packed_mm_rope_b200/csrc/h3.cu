@@ -138,7 +138,7 @@ bool valid_rope_cfg(const h3_rope_cfg* cfg) {
   return true;
 }
 
-h3::RopeTable make_rope_table(const h3_rope_cfg* cfg) {
+h3::RopeTable compute_rope_table(const h3_rope_cfg* cfg) {
   h3::RopeTable t;
   const int sec[3] = {cfg->sec_t, cfg->sec_h, cfg->sec_w};
   int p = 0;
@@ -150,6 +150,18 @@ h3::RopeTable make_rope_table(const h3_rope_cfg* cfg) {
       t.axis[p] = a;
     }
   return t;
+}
+
+// The table of `cfg`; a thread keeps the last one (64 powers take about 2 us).
+h3::RopeTable make_rope_table(const h3_rope_cfg* cfg) {
+  static thread_local h3_rope_cfg last = {};
+  static thread_local h3::RopeTable tab;
+  if (last.theta != cfg->theta || last.head_dim != cfg->head_dim || last.sec_t != cfg->sec_t ||
+      last.sec_h != cfg->sec_h || last.sec_w != cfg->sec_w || last.freq_rule != cfg->freq_rule) {
+    tab = compute_rope_table(cfg);
+    last = *cfg;
+  }
+  return tab;
 }
 
 // Checks a segment table against n_rows and packs it for the coordinate
