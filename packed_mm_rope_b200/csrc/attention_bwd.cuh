@@ -149,13 +149,6 @@ __global__ void __launch_bounds__(256) prep_kernel(const __nv_bfloat16* __restri
 
 // --------------------------------------------------------------- helpers ----
 
-// Untiled bulk copy of `bytes` (a multiple of 16) global -> shared.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, int row,
                                           int batch) {
   tma_load_3d(dst, map, bar, col, row, batch);

@@ -42,6 +42,7 @@ struct DeviceState {
 
 std::mutex g_state_mu;
 DeviceState g_states[64];
+std::atomic<uint32_t> g_attr_epoch{1};   // raised by h3_shutdown: kernel attributes are set again
 
 const DeviceState* device_state() {
   int dev = 0;
@@ -703,6 +704,7 @@ void h3_shutdown(void) {
   {
     std::lock_guard<std::mutex> lock(g_state_mu);
     for (auto& st : g_states) st = DeviceState();
+    g_attr_epoch.fetch_add(1);
   }
   {
     std::lock_guard<std::mutex> lock(g_slot_mu);

@@ -386,39 +386,447 @@ __global__ void __launch_bounds__(G > THREADS ? G : THREADS) layernorm_backward_
   if (partials != nullptr) store_partial<G, CH>(partials + group * 2 * hidden, t, chunks, hidden, dw, db);
 }
 
-// Sums over the partial rows first, first + 1, ... < last of `partials`
-// [..][2][hidden] for column sets of 32: eight thread rows take every eighth
-// partial each, in order, and are added in order.  `half` 0: dw, 1: db.
-constexpr int REDUCE_ROWS = 8;
-__device__ __forceinline__ float reduce_partials(const float* __restrict__ partials, long long first, long long last,
-                                                 int half, int hidden, int col, float (*buf)[32]) {
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  float s = 0.f;
+// ------------------------------------------------------- rings of rows ----
+
+// Long aligned rows: a block of G threads with CH chunks of a row each takes R rows
+// at a time.  One more warp copies rows into a ring of shared memory (bulk copies),
+// so reads from HBM go on while the block reduces and writes, and every pass reads
+// the rows from there, so that a thread's registers hold its parameters and column
+// sums for all rows.  A block is bound by the latency of its reductions and by
+// instruction issue; R rows share one reduction.
+constexpr int MAX_SLOTS = 4;
+constexpr unsigned long long RING_DRAIN_NS = 2000000000ull;
+
+struct RingAt {             // slot and phase of a step
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int slots) {
+    if (++slot == slots) slot = 0, phase ^= 1u;
+  }
+};
+
+struct Ring {
+  uint32_t full, empty;     // mbarriers, one per slot each
+  uint32_t data;            // shared address of slot 0
+  uint32_t row_bytes;       // of one row of one tensor
+  uint32_t slot_bytes;      // R rows of each tensor: [tensor][R][row]
+  int slots;
+  volatile uint32_t* abort;
+  unsigned long long limit;
+  int err_slot;
+
+  __device__ __forceinline__ void init(int consumer_warps) const {
+    for (int s = 0; s < slots; ++s) {
+      mbar_init(full + 8u * s, 1);
+      mbar_init(empty + 8u * s, consumer_warps);
+    }
+    mbar_fence_init();
+  }
+  // Consumers: whether the step has landed (bounded wait); its slot is free again.
+  __device__ __forceinline__ bool wait(RingAt at) const {
+    return mbar_wait_bounded(full + 8u * at.slot, at.phase, abort, limit, err_slot);
+  }
+  __device__ __forceinline__ void release(RingAt at) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8u * at.slot);
+  }
+  // Producer thread: steps 0 .. count - 1 of rows(i) rows each; src(tensor, i, r)
+  // names row r of step i.  Ends when every copy has landed.
+  template <int R, int TENSORS, typename Rows, typename Src>
+  __device__ __forceinline__ void produce(int count, Rows rows, Src src) const {
+    RingAt at;
+    int issued = 0;
+    for (; issued < count; ++issued, at.next(slots)) {
+      if (issued >= slots && !mbar_wait_bounded(empty + 8u * at.slot, at.phase ^ 1u, abort, limit, err_slot)) break;
+      const uint32_t bar = full + 8u * at.slot, to = data + at.slot * slot_bytes;
+      const int n = rows(issued);
+      mbar_arrive_expect_tx(bar, n * TENSORS * row_bytes);
+      for (int r = 0; r < n; ++r)
+#pragma unroll
+        for (int t = 0; t < TENSORS; ++t) bulk_load(to + (t * R + r) * row_bytes, src(t, issued, r), row_bytes, bar);
+    }
+    volatile uint32_t never = 0u;
+    for (int i = issued > slots ? issued - slots : 0; i < issued; ++i)
+      mbar_wait_bounded(full + 8u * (i % slots), (i / slots) & 1, &never, RING_DRAIN_NS, err_slot);
+  }
+};
+
+constexpr int pow2_of(int n) { return n <= 1 ? 1 : 2 * pow2_of((n + 1) / 2); }
+
+// Sums of N values over the G consumer threads; returns whether `fail` holds in any
+// of them (all take the same way out).  Each warp halves the number of values a lane
+// carries in the first shuffles, so N values take about N + 4 of them, not 5 N; the
+// warps' partials meet in `buf` [2][values][warps] (two sets in turn) behind one
+// barrier and every warp adds them up with lanes side by side.
+template <int G, int N>
+struct BlockSum {
+  static constexpr int M = pow2_of(N);             // values, padded
+  static constexpr int W = G / 32;
+  static constexpr int WP = pow2_of(W);            // warps, padded
+  static constexpr int PER = 32 / WP;              // values that the lanes add up at once
+  static constexpr int SIZE = 2 * M * WP;
+
+  static __device__ __forceinline__ bool sum(float (&v)[N], float* buf, int& parity, bool fail) {
+    const int lane = threadIdx.x & 31;
+    float a[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) a[i] = i < N ? v[i] : 0.f;
+    int offset = 16;
+#pragma unroll
+    for (int width = M; width > 1; width /= 2, offset /= 2) {
+      const bool upper = (lane & offset) != 0;
+#pragma unroll
+      for (int i = 0; i < width / 2; ++i) {
+        const float send = upper ? a[i] : a[i + width / 2];
+        a[i] = (upper ? a[i + width / 2] : a[i]) + __shfl_xor_sync(0xffffffffu, send, offset);
+      }
+    }
+#pragma unroll
+    for (; offset > 0; offset /= 2) a[0] += __shfl_xor_sync(0xffffffffu, a[0], offset);
+    float* const set = buf + parity * (M * WP);
+    if ((lane & (32 / M - 1)) == 0) set[(lane / (32 / M)) * WP + (threadIdx.x >> 5)] = a[0];
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(fail ? 1u : 0u), "n"(G)
+        : "memory");
+#pragma unroll
+    for (int g = 0; g < (N + PER - 1) / PER; ++g) {
+      float s = (lane & (WP - 1)) < W ? set[g * 32 + lane] : 0.f;
+#pragma unroll
+      for (int o = WP / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (g * PER + i < N) v[g * PER + i] = PER == 1 ? s : __shfl_sync(0xffffffffu, s, i * WP);
+    }
+    parity ^= 1;
+    return any != 0u;
+  }
+};
+
+// Chunk c of a row in shared memory.
+template <typename T>
+__device__ __forceinline__ Chunk<T> ring_chunk(const uint8_t* row, int c) {
+  Chunk<T> u;
+#pragma unroll
+  for (int k = 0; k < Chunk<T>::W / 4; ++k) {
+    const uint4 v = *reinterpret_cast<const uint4*>(row + c * static_cast<int>(sizeof(Chunk<T>)) + 16 * k);
+    u.w[4 * k] = v.x;
+    u.w[4 * k + 1] = v.y;
+    u.w[4 * k + 2] = v.z;
+    u.w[4 * k + 3] = v.w;
+  }
+  return u;
+}
+
+// Means of R rows in shared memory.  Returns the verdict on `fail`.
+template <typename T, int G, int CH, int R>
+__device__ __forceinline__ bool ring_means(const uint8_t* rows, uint32_t row_bytes, int chunks, float inv_n, float* buf,
+                                           int& parity, bool fail, float (&mean)[R]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = threadIdx.x + G * i;
+      if (c >= chunks) continue;
+      const Chunk<T> u = ring_chunk<T>(rows + r * row_bytes, c);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) s = __fadd2_rn(s, pair_of(u, m));
+    }
+    mean[r] = s.x + s.y;
+  }
+  const bool failed = BlockSum<G, R>::sum(mean, buf, parity, fail);
+#pragma unroll
+  for (int r = 0; r < R; ++r) mean[r] *= inv_n;
+  return failed;
+}
+
+// Their rstd, from squared deviations.
+template <typename T, int G, int CH, int R>
+__device__ __forceinline__ void ring_rstds(const uint8_t* rows, uint32_t row_bytes, int chunks, float inv_n, float eps,
+                                           float* buf, int& parity, const float (&mean)[R], float (&rstd)[R]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float2 nm = make_float2(-mean[r], -mean[r]);
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = threadIdx.x + G * i;
+      if (c >= chunks) continue;
+      const Chunk<T> u = ring_chunk<T>(rows + r * row_bytes, c);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float2 d = __fadd2_rn(pair_of(u, m), nm);
+        s = __ffma2_rn(d, d, s);
+      }
+    }
+    rstd[r] = s.x + s.y;
+  }
+  BlockSum<G, R>::sum(rstd, buf, parity, false);
+#pragma unroll
+  for (int r = 0; r < R; ++r) rstd[r] = rsqrtf(fmaf(rstd[r], inv_n, eps));
+}
+
+// The blocks take sets of R rows in turn: set i of this block starts at row(i).
+template <int R>
+struct RowSets {
+  long long n_rows;
+  __device__ __forceinline__ int count() const {
+    return static_cast<int>(((n_rows + R - 1) / R - blockIdx.x + gridDim.x - 1) / gridDim.x);
+  }
+  __device__ __forceinline__ long long row(int i) const {
+    return (blockIdx.x + static_cast<long long>(i) * gridDim.x) * R;
+  }
+  __device__ __forceinline__ int rows(int i) const {
+    const long long left = n_rows - row(i);
+    return left < R ? static_cast<int>(left) : R;
+  }
+};
+
+template <typename T, typename P, int G, int CH, int R, int MINB>
+__global__ void __launch_bounds__(G + 32, MINB) layernorm_ring_kernel(
+    const T* x, T* y, const P* __restrict__ weight, const P* __restrict__ bias, float* __restrict__ mean_out,
+    float* __restrict__ rstd_out, long long n_rows, int hidden, long long x_stride, long long y_stride, float eps,
+    int slots, unsigned long long limit, int err_slot) {
+  extern __shared__ __align__(128) uint8_t rows[];
+  __shared__ uint64_t bars[2 * MAX_SLOTS];
+  __shared__ uint32_t abort_word;
+  __shared__ float buf[BlockSum<G, R>::SIZE];
+  const int t = threadIdx.x, chunks = hidden / 8;
+  const uint32_t row_bytes = static_cast<uint32_t>(hidden * sizeof(T));
+  const Ring ring{smem_u32(bars), smem_u32(bars + MAX_SLOTS), smem_u32(rows), row_bytes, R * row_bytes, slots,
+                  &abort_word, limit, err_slot};
+  const RowSets<R> sets{n_rows};
+  if (t == 0) {
+    abort_word = 0u;
+    ring.init(G / 32);
+  }
+  __syncthreads();
+  if (t >= G) {
+    if (t == G)
+      ring.produce<R, 1>(sets.count(), [&](int i) { return sets.rows(i); },
+                         [&](int, int i, int r) { return x + (sets.row(i) + r) * x_stride; });
+    return;
+  }
+  const float inv_n = 1.f / static_cast<float>(hidden);
+  float2 w[CH][4], b[CH][4];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    if (t + G * i < chunks) {
+      load_param<P, true>(weight, 8 * (t + G * i), hidden, 1.f, w[i]);
+      load_param<P, true>(bias, 8 * (t + G * i), hidden, 0.f, b[i]);
+    }
+  }
+  int parity = 0;
+  RingAt at;
+  for (int i = 0, count = sets.count(); i < count; ++i, at.next(slots)) {
+    const bool landed = ring.wait(at);
+    const uint8_t* in = rows + at.slot * ring.slot_bytes;
+    float mean[R], rstd[R];
+    if (ring_means<T, G, CH, R>(in, row_bytes, chunks, inv_n, buf, parity, !landed, mean)) break;
+    ring_rstds<T, G, CH, R>(in, row_bytes, chunks, inv_n, eps, buf, parity, mean, rstd);
+    const long long r0 = sets.row(i);
+    const int n = sets.rows(i);
+    T* out = y + r0 * y_stride;
+#pragma unroll
+    for (int r = 0; r < R; ++r, out += y_stride) {
+      if (r >= n) continue;
+      if (t == 0) {
+        if (mean_out != nullptr) mean_out[r0 + r] = mean[r];
+        if (rstd_out != nullptr) rstd_out[r0 + r] = rstd[r];
+      }
+      const float2 rs = make_float2(rstd[r], rstd[r]), nm = make_float2(-mean[r], -mean[r]);
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int c = t + G * k;
+        if (c >= chunks) continue;
+        const Chunk<T> u = ring_chunk<T>(in + r * row_bytes, c);
+        Chunk<T> o;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          set_pair(o, m, __ffma2_rn(__fmul2_rn(__fadd2_rn(pair_of(u, m), nm), rs), w[k][m], b[k][m]));
+        store_chunk<T, true>(out, 8 * c, hidden, o);
+      }
+    }
+    ring.release(at);
+  }
+}
+
+// R rows of a backward pass, x and dy in shared memory (`at`, `at_d`): their
+// statistics are known and their weight is in registers.  Rows of the bit set
+// `active` get their dx (dst(r)) and add to the column sums.  Returns the verdict on
+// `fail`.  With xhat = x rstd - mean rstd the row's result is
+//   dx = (dy w) rstd + x B + C,  B = -mean(g xhat) rstd^2,  C = -rstd (mean(g) + mean B / rstd).
+template <typename T, int G, int CH, int R, typename Dst>
+__device__ __forceinline__ bool ring_backward_rows(const uint8_t* at, const uint8_t* at_d, uint32_t row_bytes,
+                                                   const float (&mean)[R], const float (&rstd)[R], unsigned active,
+                                                   const float2 (&w)[CH][4], float inv_n, float* buf, int& parity,
+                                                   bool fail, Dst dst, int chunks, int hidden, float2 (&dw)[CH][4],
+                                                   float2 (&db)[CH][4]) {
+  const int t = threadIdx.x;
+  float s[2 * R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float2 a1 = make_float2(0.f, 0.f), a2 = make_float2(0.f, 0.f);
+    if (active >> r & 1u) {
+      const float mr = -mean[r] * rstd[r];
+      const float2 rs = make_float2(rstd[r], rstd[r]), nm = make_float2(mr, mr);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = t + G * i;
+        if (c >= chunks) continue;
+        const Chunk<T> ux = ring_chunk<T>(at + r * row_bytes, c), ud = ring_chunk<T>(at_d + r * row_bytes, c);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float2 d = pair_of(ud, m);
+          const float2 xh = __ffma2_rn(pair_of(ux, m), rs, nm);
+          const float2 g = __fmul2_rn(d, w[i][m]);
+          a1 = __fadd2_rn(a1, g);
+          a2 = __ffma2_rn(g, xh, a2);
+          dw[i][m] = __ffma2_rn(d, xh, dw[i][m]);
+          db[i][m] = __fadd2_rn(db[i][m], d);
+        }
+      }
+    }
+    s[2 * r] = a1.x + a1.y;
+    s[2 * r + 1] = a2.x + a2.y;
+  }
+  if (BlockSum<G, 2 * R>::sum(s, buf, parity, fail)) return true;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (!(active >> r & 1u)) continue;
+    const float c2 = -s[2 * r + 1] * inv_n * rstd[r], cb = c2 * rstd[r];
+    const float cc = fmaf(-mean[r], cb, -s[2 * r] * inv_n * rstd[r]);
+    const float2 rs = make_float2(rstd[r], rstd[r]), b2 = make_float2(cb, cb), c = make_float2(cc, cc);
+    T* dxr = dst(r);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int ch = t + G * i;
+      if (ch >= chunks) continue;
+      const Chunk<T> ux = ring_chunk<T>(at + r * row_bytes, ch), ud = ring_chunk<T>(at_d + r * row_bytes, ch);
+      Chunk<T> o;
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        set_pair(o, m, __ffma2_rn(__fmul2_rn(pair_of(ud, m), w[i][m]), rs, __ffma2_rn(pair_of(ux, m), b2, c)));
+      store_chunk<T, true>(dxr, 8 * ch, hidden, o);
+    }
+  }
+  return false;
+}
+
+// Layer norm's gradients by rings of (x, dy) rows; partial row blockIdx.
+template <typename T, typename P, int G, int CH, int R, int MINB>
+__global__ void __launch_bounds__(G + 32, MINB) layernorm_backward_ring_kernel(
+    const T* dy, const T* x, const float* __restrict__ mean, const float* __restrict__ rstd,
+    const P* __restrict__ weight, T* dx, float* __restrict__ partials, long long n_rows, int hidden,
+    long long dy_stride, long long x_stride, long long dx_stride, int slots, unsigned long long limit, int err_slot) {
+  extern __shared__ __align__(128) uint8_t rows[];
+  __shared__ uint64_t bars[2 * MAX_SLOTS];
+  __shared__ uint32_t abort_word;
+  __shared__ float buf[BlockSum<G, 2 * R>::SIZE];
+  const int t = threadIdx.x, chunks = hidden / 8;
+  const uint32_t row_bytes = static_cast<uint32_t>(hidden * sizeof(T));
+  const Ring ring{smem_u32(bars), smem_u32(bars + MAX_SLOTS), smem_u32(rows), row_bytes, 2 * R * row_bytes, slots,
+                  &abort_word, limit, err_slot};
+  const RowSets<R> sets{n_rows};
+  if (t == 0) {
+    abort_word = 0u;
+    ring.init(G / 32);
+  }
+  __syncthreads();
+  if (t >= G) {
+    if (t == G)
+      ring.produce<R, 2>(sets.count(), [&](int i) { return sets.rows(i); }, [&](int tensor, int i, int r) {
+        const long long row = sets.row(i) + r;
+        return tensor == 0 ? x + row * x_stride : dy + row * dy_stride;
+      });
+    return;
+  }
+  const float inv_n = 1.f / static_cast<float>(hidden);
+  float2 w[CH][4], dw[CH][4], db[CH][4];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) dw[i][m] = db[i][m] = make_float2(0.f, 0.f);
+    if (t + G * i < chunks) load_param<P, true>(weight, 8 * (t + G * i), hidden, 1.f, w[i]);
+  }
+  int parity = 0;
+  RingAt at;
+  for (int i = 0, count = sets.count(); i < count; ++i, at.next(slots)) {
+    const int n = sets.rows(i);
+    const long long r0 = sets.row(i);
+    float m[R], s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = r < n ? mean[r0 + r] : 0.f;
+      s[r] = r < n ? rstd[r0 + r] : 0.f;
+    }
+    const bool landed = ring.wait(at);
+    const uint8_t* in = rows + at.slot * ring.slot_bytes;
+    if (ring_backward_rows<T, G, CH, R>(in, in + R * row_bytes, row_bytes, m, s, (1u << n) - 1u, w, inv_n, buf, parity,
+                                        !landed, [&](int r) { return dx + (r0 + r) * dx_stride; }, chunks, hidden, dw,
+                                        db))
+      break;
+    ring.release(at);
+  }
+  if (partials != nullptr)
+    store_partial<G, CH>(partials + static_cast<long long>(blockIdx.x) * 2 * hidden, t, chunks, hidden, dw, db);
+}
+
+// ------------------------------------------------- sums of partial rows ----
+
+// Sums over the partial rows first .. last - 1 of `partials` [..][dw, db][hidden].
+// A block takes 64 x W columns: 64 threads side by side, ROWS such rows of threads
+// take every ROWS-th partial, in order, and their sums are added in order.  Few
+// partials per sum want few rows and W = 4, many want many rows and, where one sum is
+// all there is, W = 1 for more blocks.
+template <int ROWS, int W, typename Store>
+__device__ __forceinline__ void reduce_partials(const float* __restrict__ partials, long long first, long long last,
+                                                int half, int hidden, Store store) {
+  __shared__ float buf[ROWS][64][W];
+  const int lane = threadIdx.x & 63, row = threadIdx.x >> 6;
+  const int col = (blockIdx.x * 64 + lane) * W;
+  float s[W] = {};
   if (col < hidden) {
     const float* p = partials + half * static_cast<long long>(hidden) + col;
 #pragma unroll 4
-    for (long long i = first + row; i < last; i += REDUCE_ROWS) s += __ldcs(p + i * 2 * hidden);
+    for (long long i = first + row; i < last; i += ROWS) {
+      if constexpr (W == 4) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(p + i * 2 * hidden));
+        s[0] += v.x;
+        s[1] += v.y;
+        s[2] += v.z;
+        s[3] += v.w;
+      } else {
+        s[0] += __ldcs(p + i * 2 * hidden);
+      }
+    }
   }
-  buf[row][lane] = s;
-  __syncthreads();
-  float total = 0.f;
-  if (row == 0) {
 #pragma unroll
-    for (int q = 0; q < REDUCE_ROWS; ++q) total += buf[q][lane];
+  for (int k = 0; k < W; ++k) buf[row][lane][k] = s[k];
+  __syncthreads();
+  if (row != 0 || col >= hidden) return;
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    float total = s[k];
+#pragma unroll
+    for (int q = 1; q < ROWS; ++q) total += buf[q][lane][k];
+    store(col + k, total);
   }
-  return total;
 }
 
 template <typename P>
-__global__ void __launch_bounds__(32 * REDUCE_ROWS) norm_reduce_kernel(const float* __restrict__ partials,
-                                                                       int n_partials, int hidden, P* dweight,
-                                                                       P* dbias) {
-  __shared__ float buf[REDUCE_ROWS][32];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31);
+__global__ void __launch_bounds__(64 * 16) norm_reduce_kernel(const float* __restrict__ partials, int n_partials,
+                                                                int hidden, P* dweight, P* dbias) {
   P* out = blockIdx.y == 0 ? dweight : dbias;
   if (out == nullptr) return;
-  const float s = reduce_partials(partials, 0, n_partials, blockIdx.y, hidden, col, buf);
-  if (threadIdx.x < 32 && col < hidden) out[col] = from_float<P>(s);
+  reduce_partials<16, 1>(partials, 0, n_partials, blockIdx.y, hidden,
+                           [&](int col, float v) { out[col] = from_float<P>(v); });
 }
 
 // ------------------------------------------- AdaLN backward: row sorting ----
@@ -585,18 +993,191 @@ __global__ void __launch_bounds__(G > THREADS ? G : THREADS) adaln_backward_kern
     store_partial<G, CH>(partials + (group + entry) * 2 * hidden, t, chunks, hidden, dw, db);
 }
 
+// R rows of the AdaLN backward pass whose means are known, as ring_backward_rows:
+// one reduction joins the squared deviations with sum(g) and sum(g (x - mean)).
+template <int G, int CH, int R, typename Dst>
+__device__ __forceinline__ void ring_adaln_rows(const uint8_t* at, const uint8_t* at_d, uint32_t row_bytes,
+                                                const float (&mean)[R], unsigned active, const float2 (&w)[CH][4],
+                                                float inv_n, float eps, float* buf, int& parity, Dst dst, int chunks,
+                                                int hidden, float2 (&dw)[CH][4], float2 (&db)[CH][4]) {
+  using T = __nv_bfloat16;
+  const int t = threadIdx.x;
+  float s[3 * R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float2 a0 = make_float2(0.f, 0.f), a1 = a0, a2 = a0;
+    if (active >> r & 1u) {
+      const float2 nm = make_float2(-mean[r], -mean[r]);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = t + G * i;
+        if (c >= chunks) continue;
+        const Chunk<T> ux = ring_chunk<T>(at + r * row_bytes, c), ud = ring_chunk<T>(at_d + r * row_bytes, c);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float2 xc = __fadd2_rn(pair_of(ux, m), nm);
+          const float2 g = __fmul2_rn(pair_of(ud, m), w[i][m]);
+          a0 = __ffma2_rn(xc, xc, a0);
+          a1 = __fadd2_rn(a1, g);
+          a2 = __ffma2_rn(g, xc, a2);
+        }
+      }
+    }
+    s[3 * r] = a0.x + a0.y;
+    s[3 * r + 1] = a1.x + a1.y;
+    s[3 * r + 2] = a2.x + a2.y;
+  }
+  BlockSum<G, 3 * R>::sum(s, buf, parity, false);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (!(active >> r & 1u)) continue;
+    const float rstd = rsqrtf(fmaf(s[3 * r], inv_n, eps));
+    const float mr = -mean[r] * rstd;
+    const float cb = -s[3 * r + 2] * inv_n * rstd * rstd * rstd;
+    const float cc = fmaf(-mean[r], cb, -s[3 * r + 1] * inv_n * rstd);
+    const float2 rs = make_float2(rstd, rstd), nm = make_float2(mr, mr), b2 = make_float2(cb, cb);
+    const float2 c0 = make_float2(cc, cc);
+    T* dxr = dst(r);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + G * i;
+      if (c >= chunks) continue;
+      const Chunk<T> ux = ring_chunk<T>(at + r * row_bytes, c), ud = ring_chunk<T>(at_d + r * row_bytes, c);
+      Chunk<T> o;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float2 x = pair_of(ux, m), d = pair_of(ud, m);
+        dw[i][m] = __ffma2_rn(d, __ffma2_rn(x, rs, nm), dw[i][m]);
+        db[i][m] = __fadd2_rn(db[i][m], d);
+        set_pair(o, m, __ffma2_rn(__fmul2_rn(d, w[i][m]), rs, __ffma2_rn(x, b2, c0)));
+      }
+      store_chunk<T, true>(dxr, 8 * c, hidden, o);
+    }
+  }
+}
+
+// The same by rings of (x, dy) rows, one block per group; the entry's weights
+// stay in registers while it lasts.
+template <int G, int CH, int R, int MINB>
+__global__ void __launch_bounds__(G + 32, MINB) adaln_backward_ring_kernel(
+    const __nv_bfloat16* dy, const __nv_bfloat16* x, const float* __restrict__ table, const int2* __restrict__ order,
+    __nv_bfloat16* dx, float* __restrict__ partials, int n_entries, long long n_rows, long long per, int hidden,
+    long long dy_stride, long long x_stride, long long dx_stride, float eps, int slots, unsigned long long limit,
+    int err_slot) {
+  using T = __nv_bfloat16;
+  extern __shared__ __align__(128) uint8_t rows[];
+  __shared__ uint64_t bars[2 * MAX_SLOTS];
+  __shared__ uint32_t abort_word;
+  __shared__ float buf1[BlockSum<G, R>::SIZE];
+  __shared__ float buf2[BlockSum<G, 3 * R>::SIZE];
+  const int t = threadIdx.x, chunks = hidden / 8;
+  const uint32_t row_bytes = static_cast<uint32_t>(hidden * sizeof(T));
+  const Ring ring{smem_u32(bars), smem_u32(bars + MAX_SLOTS), smem_u32(rows), row_bytes, 2 * R * row_bytes, slots,
+                  &abort_word, limit, err_slot};
+  const long long group = blockIdx.x, first = group * per;
+  const long long last = first + per < n_rows ? first + per : n_rows;
+  const int n_pos = last > first ? static_cast<int>(last - first) : 0;
+  const int count = (n_pos + R - 1) / R;
+  auto n_of = [&](int i) { return n_pos - i * R < R ? n_pos - i * R : R; };
+  order += first;
+  if (t == 0) {
+    abort_word = 0u;
+    ring.init(G / 32);
+  }
+  __syncthreads();
+  if (t >= G) {
+    if (t == G)
+      ring.produce<R, 2>(count, n_of, [&](int tensor, int i, int r) {
+        const long long row = order[i * R + r].x;
+        return tensor == 0 ? x + row * x_stride : dy + row * dy_stride;
+      });
+    return;
+  }
+  const float inv_n = 1.f / static_cast<float>(hidden);
+  float2 w[CH][4], dw[CH][4], db[CH][4];
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) dw[i][m] = db[i][m] = make_float2(0.f, 0.f);
+  };
+  clear();
+  int parity1 = 0, parity2 = 0, entry = -1;
+  int2 next[R];                                    // (row, entry) of the next step's positions
+  auto look = [&](int i) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) next[r] = i * R + r < n_pos ? order[i * R + r] : make_int2(0, -1);
+  };
+  look(0);
+  RingAt at;
+  for (int i = 0; i < count; ++i, at.next(slots)) {
+    int2 here[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) here[r] = next[r];
+    look(i + 1);
+    const bool landed = ring.wait(at);
+    const uint8_t* in = rows + at.slot * ring.slot_bytes;
+    float mean[R];
+    if (ring_means<T, G, CH, R>(in, row_bytes, chunks, inv_n, buf1, parity1, !landed, mean)) break;
+    // entries ascend: the rows of one entry at a time (nearly always all R)
+    unsigned left = (1u << n_of(i)) - 1u;
+    while (left != 0u) {
+      int e = 0;
+      unsigned active = 0u;
+#pragma unroll
+      for (int r = R - 1; r >= 0; --r)
+        if (left >> r & 1u) e = here[r].y;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if ((left >> r & 1u) && here[r].y == e) active |= 1u << r;
+      left &= ~active;
+      if (e != entry) {
+        if (entry >= 0 && entry < n_entries)
+          store_partial<G, CH>(partials + (group + entry) * 2 * hidden, t, chunks, hidden, dw, db);
+        entry = e;
+        clear();
+        if (entry < n_entries) {
+#pragma unroll
+          for (int k = 0; k < CH; ++k) {
+            if (t + G * k >= chunks) continue;
+            load_param<float, true>(table + (2LL * entry + 1) * hidden, 8 * (t + G * k), hidden, 0.f, w[k]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) w[k][m] = __fadd2_rn(w[k][m], make_float2(1.f, 1.f));
+          }
+        }
+      }
+      auto dst = [&](int r) { return dx + here[r].x * dx_stride; };
+      if (entry == n_entries) {            // no such table entry: NaN, as the forward call gives
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (!(active >> r & 1u)) continue;
+#pragma unroll
+          for (int k = 0; k < CH; ++k) {
+            const Chunk<T> nan = {{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u}};
+            if (t + G * k < chunks) store_chunk<T, true>(dst(r), 8 * (t + G * k), hidden, nan);
+          }
+        }
+      } else {
+        ring_adaln_rows<G, CH, R>(in, in + R * row_bytes, row_bytes, mean, active, w, inv_n, eps, buf2, parity2, dst,
+                                  chunks, hidden, dw, db);
+      }
+    }
+    ring.release(at);
+  }
+  if (entry >= 0 && entry < n_entries)
+    store_partial<G, CH>(partials + (group + entry) * 2 * hidden, t, chunks, hidden, dw, db);
+}
+
 // d_table[e][0] = sum of dy (shift), [e][1] = sum of dy xhat (scale)
-__global__ void __launch_bounds__(32 * REDUCE_ROWS) adaln_reduce_kernel(const float* __restrict__ partials,
-                                                                        const int* __restrict__ starts, long long per,
-                                                                        int hidden, float* __restrict__ dtable) {
-  __shared__ float buf[REDUCE_ROWS][32];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31);
+template <int ROWS>
+__global__ void __launch_bounds__(64 * ROWS) adaln_reduce_kernel(const float* __restrict__ partials,
+                                                                 const int* __restrict__ starts, long long per,
+                                                                 int hidden, float* __restrict__ dtable) {
   const int e = blockIdx.y >> 1, half = blockIdx.y & 1;
   const long long a = starts[e], b = starts[e + 1];
   const long long c0 = a / per, c1 = b > a ? (b - 1) / per + 1 : c0;   // groups with rows of entry e
-  const float s = reduce_partials(partials, c0 + e, c1 + e, half, hidden, col, buf);
-  if (threadIdx.x < 32 && col < hidden)
-    dtable[(2LL * e + (half == 0 ? 1 : 0)) * hidden + col] = s;
+  float* out = dtable + (2LL * e + (half == 0 ? 1 : 0)) * hidden;
+  reduce_partials<ROWS, 4>(partials, c0 + e, c1 + e, half, hidden, [&](int col, float v) { out[col] = v; });
 }
 
 }  // namespace norm

@@ -24,6 +24,10 @@ template <typename T>
 struct TypeTag {
   using type = T;
 };
+template <int V>
+struct IntTag {
+  static constexpr int value = V;
+};
 
 // Calls f with the types of (x dtype, parameter dtype); the parameters share
 // x's type or are fp32.
@@ -45,10 +49,12 @@ struct RowShape {
   static constexpr int G = G_, CH = CH_;
   static constexpr int BLOCK = G > h3::norm::THREADS ? G : h3::norm::THREADS;
   static constexpr int GROUPS = BLOCK / G;
+  // aligned rows of other lengths go to the ring kernels
+  static constexpr bool ALIGNED = G * CH <= 128 || G * CH == 2048;
 };
 
 // Forward: a warp per row up to 1,024 elements, else 128 or 256 threads with
-// up to 8 chunks each.
+// up to 8 chunks each (rows that the ring kernels do not take).
 template <typename F>
 h3_status with_forward_shape(int hidden, F f) {
   const int chunks = (hidden + 7) / 8;
@@ -72,14 +78,87 @@ h3_status with_backward_shape(int hidden, F f) {
   return f(RowShape<512, 4>{});
 }
 
-constexpr int kBackwardBlocks = 296;   // two blocks per SM of a B200: every partial row is read once more
+// Ring kernels (aligned rows of more than 1,024 elements): G consumer threads with
+// CH chunks each, CTAS blocks per SM.  With the producer warp a block has 256, 288
+// or 512 threads: 224 consumers leave a thread 128 registers at two blocks per SM,
+// which the backward kernels need (256 consumers spill: 208 against 156 us for layer
+// norm's gradients at 28,196 x 5,376 bf16).
+template <int G_, int CH_, int CTAS_>
+struct RingShape {
+  static constexpr int G = G_, CH = CH_, CTAS = CTAS_;
+};
 
-// Blocks of the backward row kernels (a partial row per group of each).
+template <typename F>
+h3_status with_forward_ring(int hidden, F f) {
+  const int chunks = hidden / 8;
+  if (chunks <= 256) return f(RingShape<256, 1, 2>{});
+  if (chunks <= 512) return f(RingShape<256, 2, 2>{});
+  if (chunks <= 768) return f(RingShape<256, 3, 2>{});
+  if (chunks <= 960) return f(RingShape<480, 2, 1>{});
+  return f(RingShape<480, 3, 1>{});
+}
+
+template <typename F>
+h3_status with_backward_ring(int hidden, F f) {
+  const int chunks = hidden / 8;
+  if (chunks <= 224) return f(RingShape<224, 1, 2>{});
+  if (chunks <= 448) return f(RingShape<224, 2, 2>{});
+  if (chunks <= 672) return f(RingShape<224, 3, 2>{});
+  if (chunks <= 960) return f(RingShape<480, 2, 1>{});
+  return f(RingShape<480, 3, 1>{});
+}
+
+bool ring_takes(int hidden) { return hidden > 1024 && hidden <= 8 * 3 * 480; }
+
+constexpr int kRingSms = 148;                    // SMs of a B200: sizes grids, and with them partial rows
+constexpr uint64_t kRingSmem = 224u << 10;       // shared memory of an SM that its blocks share
+
+// Rows per step (R) and slots of a ring: the most rows of `choices` with which every
+// block gets several steps and two slots fit; `tensors` rows are read per row.
+struct RingPlan {
+  int rows, slots;
+  long long blocks;
+  size_t smem;
+};
+
+RingPlan ring_plan(int64_t n_rows, size_t row_bytes, int tensors, int ctas, std::initializer_list<int> choices) {
+  const uint64_t budget = kRingSmem / ctas - 3072u;
+  RingPlan p{1, 1, 0, 0};
+  for (int r : choices)
+    if (n_rows >= 2LL * r * ctas * kRingSms && 2u * r * tensors * row_bytes <= budget) p.rows = std::max(p.rows, r);
+  const uint64_t slot = static_cast<uint64_t>(p.rows) * tensors * row_bytes;
+  p.slots = static_cast<int>(std::min<uint64_t>(h3::norm::MAX_SLOTS, std::max<uint64_t>(1u, budget / slot)));
+  p.smem = static_cast<size_t>(p.slots * slot);
+  p.blocks = std::min<long long>(static_cast<long long>(ctas) * kRingSms, (n_rows + p.rows - 1) / p.rows);
+  return p;
+}
+
+template <auto Kernel, typename... Args>
+h3_status launch_ring(const RingPlan& plan, int threads, cudaStream_t s, Args... args) {
+  // the opt-in to more than 48 KB of shared memory, once per kernel and device until h3_shutdown
+  static std::atomic<uint32_t> done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return H3_ERR_CUDA;
+  const uint32_t epoch = g_attr_epoch.load();
+  if (done[dev].load() != epoch) {
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingSmem)) !=
+        cudaSuccess)
+      return H3_ERR_CUDA;
+    done[dev].store(epoch);
+  }
+  Kernel<<<static_cast<unsigned>(plan.blocks), threads, plan.smem, s>>>(args...);
+  return launched();
+}
+
+// Blocks of the plain backward row kernels (a partial row per group of each).
+constexpr int kBackwardBlocks = 2 * kRingSms;
+
 template <typename S>
 long long backward_blocks(int64_t n_rows) {
   return std::min<long long>(kBackwardBlocks, (n_rows + S::GROUPS - 1) / S::GROUPS);
 }
 
+// Partial rows that the backward pass over n_rows rows leaves at most, by either kind of kernel.
 long long backward_groups(int64_t n_rows, int hidden) {
   long long groups = 0;
   with_backward_shape(hidden, [&](auto shape) {
@@ -87,7 +166,7 @@ long long backward_groups(int64_t n_rows, int hidden) {
     groups = backward_blocks<S>(n_rows) * S::GROUPS;
     return H3_OK;
   });
-  return groups;
+  return ring_takes(hidden) ? std::max<long long>(groups, std::min<long long>(2LL * kRingSms, n_rows)) : groups;
 }
 
 // ---- AdaLN backward: workspace ----
@@ -101,6 +180,11 @@ struct AdalnWork {
 AdalnWork adaln_work(int64_t n_rows, int hidden, int32_t n_entries) {
   AdalnWork w;
   w.groups = std::max<long long>(1, backward_groups(n_rows, hidden));
+  if (ring_takes(hidden))              // the rows are always aligned: one group per block of the ring kernel
+    with_backward_ring(hidden, [&](auto shape) {
+      w.groups = std::max<long long>(1, std::min<long long>(decltype(shape)::CTAS * kRingSms, n_rows));
+      return H3_OK;
+    });
   w.per = std::max<long long>(1, (n_rows + w.groups - 1) / w.groups);
   w.blocks = static_cast<int>((n_rows + h3::norm::SORT_ROWS - 1) / h3::norm::SORT_ROWS);
   w.order = 0;
@@ -342,18 +426,33 @@ h3_status h3_layernorm(const void* d_x, void* d_y, const void* d_weight, const v
   return with_types(dtype, param_dtype, [&](auto tt, auto pt) {
     using T = typename decltype(tt)::type;
     using P = typename decltype(pt)::type;
+    if (vec && ring_takes(hidden))
+      return with_forward_ring(hidden, [&](auto shape) {
+        using S = decltype(shape);
+        const RingPlan plan = ring_plan(n_rows, sizeof(T) * hidden, 1, S::CTAS, {1, 2, 4});
+        auto go = [&](auto rows) {
+          return launch_ring<h3::norm::layernorm_ring_kernel<T, P, S::G, S::CH, decltype(rows)::value, S::CTAS>>(
+              plan, S::G + 32, as_stream(stream), static_cast<const T*>(d_x), static_cast<T*>(d_y),
+              static_cast<const P*>(d_weight), static_cast<const P*>(d_bias), d_mean, d_rstd,
+              static_cast<long long>(n_rows), hidden, static_cast<long long>(x_row_stride),
+              static_cast<long long>(y_row_stride), eps, plan.slots,
+              static_cast<unsigned long long>(g_wait_limit_ns.load()), error_slot(stream));
+        };
+        return plan.rows == 4 ? go(IntTag<4>{}) : plan.rows == 2 ? go(IntTag<2>{}) : go(IntTag<1>{});
+      });
     return with_forward_shape(hidden, [&](auto shape) {
       using S = decltype(shape);
       const long long grid = std::min<long long>((n_rows + S::GROUPS - 1) / S::GROUPS, 16LL * sms);
       auto go = [&](auto kernel) {
-        kernel<<<static_cast<int>(grid), S::BLOCK, 0, as_stream(stream)>>>(
+        kernel<<<static_cast<unsigned>(grid), S::BLOCK, 0, as_stream(stream)>>>(
             static_cast<const T*>(d_x), static_cast<T*>(d_y), static_cast<const P*>(d_weight),
             static_cast<const P*>(d_bias), d_mean, d_rstd, static_cast<long long>(n_rows), hidden, x_row_stride,
             y_row_stride, eps);
         return launched();
       };
-      return vec ? go(h3::norm::layernorm_kernel<T, P, true, S::G, S::CH>)
-                 : go(h3::norm::layernorm_kernel<T, P, false, S::G, S::CH>);
+      if constexpr (S::ALIGNED)
+        if (vec) return go(h3::norm::layernorm_kernel<T, P, true, S::G, S::CH>);
+      return go(h3::norm::layernorm_kernel<T, P, false, S::G, S::CH>);
     });
   });
 }
@@ -379,27 +478,45 @@ h3_status h3_layernorm_backward(const void* d_dy, const void* d_x, const float* 
   return with_types(dtype, param_dtype, [&](auto tt, auto pt) {
     using T = typename decltype(tt)::type;
     using P = typename decltype(pt)::type;
-    return with_backward_shape(hidden, [&](auto shape) {
-      using S = decltype(shape);
-      const long long grid = backward_blocks<S>(n_rows);
-      if (grid > 0) {
+    long long groups = 0;                          // partial rows
+    h3_status st = H3_OK;
+    if (n_rows > 0 && vec && ring_takes(hidden)) {
+      st = with_backward_ring(hidden, [&](auto shape) {
+        using S = decltype(shape);
+        const RingPlan plan = ring_plan(n_rows, sizeof(T) * hidden, 2, S::CTAS, {1, 2});
+        groups = plan.blocks;
+        auto go = [&](auto rows) {
+          return launch_ring<
+              h3::norm::layernorm_backward_ring_kernel<T, P, S::G, S::CH, decltype(rows)::value, S::CTAS>>(
+              plan, S::G + 32, as_stream(stream), static_cast<const T*>(d_dy), static_cast<const T*>(d_x), d_mean,
+              d_rstd, static_cast<const P*>(d_weight), static_cast<T*>(d_dx), partials, static_cast<long long>(n_rows),
+              hidden, static_cast<long long>(dy_row_stride), static_cast<long long>(x_row_stride),
+              static_cast<long long>(dx_row_stride), plan.slots,
+              static_cast<unsigned long long>(g_wait_limit_ns.load()), error_slot(stream));
+        };
+        return plan.rows == 2 ? go(IntTag<2>{}) : go(IntTag<1>{});
+      });
+    } else if (n_rows > 0) {
+      st = with_backward_shape(hidden, [&](auto shape) {
+        using S = decltype(shape);
+        const long long grid = backward_blocks<S>(n_rows);
+        groups = grid * S::GROUPS;
         auto go = [&](auto kernel) {
-          kernel<<<static_cast<int>(grid), S::BLOCK, 0, as_stream(stream)>>>(
+          kernel<<<static_cast<unsigned>(grid), S::BLOCK, 0, as_stream(stream)>>>(
               static_cast<const T*>(d_dy), static_cast<const T*>(d_x), d_mean, d_rstd, static_cast<const P*>(d_weight),
               static_cast<T*>(d_dx), partials, static_cast<long long>(n_rows), hidden, dy_row_stride, x_row_stride,
               dx_row_stride);
           return launched();
         };
-        const h3_status st = vec ? go(h3::norm::layernorm_backward_kernel<T, P, true, S::G, S::CH>)
-                                 : go(h3::norm::layernorm_backward_kernel<T, P, false, S::G, S::CH>);
-        if (st != H3_OK) return st;
-      }
-      if (!params) return H3_OK;
-      const dim3 rgrid((hidden + 31) / 32, 2);
-      h3::norm::norm_reduce_kernel<P><<<rgrid, 32 * h3::norm::REDUCE_ROWS, 0, as_stream(stream)>>>(
-          partials, static_cast<int>(grid * S::GROUPS), hidden, static_cast<P*>(d_dweight), static_cast<P*>(d_dbias));
-      return launched();
-    });
+        if constexpr (S::ALIGNED)
+          if (vec) return go(h3::norm::layernorm_backward_kernel<T, P, true, S::G, S::CH>);
+        return go(h3::norm::layernorm_backward_kernel<T, P, false, S::G, S::CH>);
+      });
+    }
+    if (st != H3_OK || !params) return st;
+    h3::norm::norm_reduce_kernel<P><<<dim3((hidden + 63) / 64, 2), 64 * 16, 0, as_stream(stream)>>>(
+        partials, static_cast<int>(groups), hidden, static_cast<P*>(d_dweight), static_cast<P*>(d_dbias));
+    return launched();
   });
 }
 
@@ -442,21 +559,41 @@ h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const in
                                                                            n_rows, hist, w.blocks, order, starts);
   h3_status st = launched();
   if (st != H3_OK) return st;
-  st = with_backward_shape(hidden, [&](auto shape) {
-    using S = decltype(shape);
-    if constexpr (S::G <= 256) {   // up to ADALN_MAX_HIDDEN
-      h3::norm::adaln_backward_kernel<S::G, S::CH><<<static_cast<int>(w.groups / S::GROUPS), S::BLOCK, 0, s>>>(
-          static_cast<const __nv_bfloat16*>(d_dy), static_cast<const __nv_bfloat16*>(d_x), d_table, order,
-          static_cast<__nv_bfloat16*>(d_dx), partials, n_entries, n_rows, w.per, hidden, dy_row_stride, x_row_stride,
-          dx_row_stride, eps);
-      return launched();
-    } else {
-      return H3_ERR_UNSUPPORTED;
-    }
-  });
+  if (ring_takes(hidden))
+    st = with_backward_ring(hidden, [&](auto shape) {
+      using S = decltype(shape);
+      RingPlan plan = ring_plan(n_rows, 2u * hidden, 2, S::CTAS, {1, 2});
+      plan.blocks = w.groups;
+      auto go = [&](auto rows) {
+        return launch_ring<h3::norm::adaln_backward_ring_kernel<S::G, S::CH, decltype(rows)::value, S::CTAS>>(
+            plan, S::G + 32, s, static_cast<const __nv_bfloat16*>(d_dy), static_cast<const __nv_bfloat16*>(d_x),
+            d_table, static_cast<const int2*>(order), static_cast<__nv_bfloat16*>(d_dx), partials, n_entries,
+            static_cast<long long>(n_rows), w.per, hidden, static_cast<long long>(dy_row_stride),
+            static_cast<long long>(x_row_stride), static_cast<long long>(dx_row_stride), eps, plan.slots,
+            static_cast<unsigned long long>(g_wait_limit_ns.load()), error_slot(stream));
+      };
+      return plan.rows == 2 ? go(IntTag<2>{}) : go(IntTag<1>{});
+    });
+  else
+    st = with_backward_shape(hidden, [&](auto shape) {
+      using S = decltype(shape);
+      if constexpr (S::G == 32) {            // up to 1,024 elements
+        h3::norm::adaln_backward_kernel<S::G, S::CH><<<static_cast<unsigned>(w.groups / S::GROUPS), S::BLOCK, 0, s>>>(
+            static_cast<const __nv_bfloat16*>(d_dy), static_cast<const __nv_bfloat16*>(d_x), d_table, order,
+            static_cast<__nv_bfloat16*>(d_dx), partials, n_entries, n_rows, w.per, hidden, dy_row_stride, x_row_stride,
+            dx_row_stride, eps);
+        return launched();
+      } else {
+        return H3_ERR_UNSUPPORTED;
+      }
+    });
   if (st != H3_OK) return st;
-  const dim3 rgrid((hidden + 31) / 32, 2 * n_entries);
-  h3::norm::adaln_reduce_kernel<<<rgrid, 32 * h3::norm::REDUCE_ROWS, 0, s>>>(partials, starts, w.per, hidden, d_dtable);
+  // many partial rows per entry are added by 16 rows of threads, few by 2
+  const dim3 rgrid((hidden + 255) / 256, 2 * n_entries);
+  if (w.groups >= 32LL * n_entries)
+    h3::norm::adaln_reduce_kernel<16><<<rgrid, 64 * 16, 0, s>>>(partials, starts, w.per, hidden, d_dtable);
+  else
+    h3::norm::adaln_reduce_kernel<2><<<rgrid, 64 * 2, 0, s>>>(partials, starts, w.per, hidden, d_dtable);
   return launched();
 }
 

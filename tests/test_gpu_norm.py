@@ -19,7 +19,8 @@ def h3():
 
 
 SIZES = [(1, 1), (3, 2), (5, 7), (82, 129), (33, 256), (7, 257), (9, 1024), (5, 1032), (4, 4096), (6, 4104),
-         (3, 5376), (2, 8192), (2, 8200), (3, 16384), (3, 16377), (2500, 64), (700, 5376)]
+         (3, 5376), (2, 8192), (2, 8200), (3, 11520), (2, 11528), (3, 16384), (3, 16377), (2500, 64), (700, 5376),
+         (1301, 1800), (2403, 2056), (1, 6152), (601, 7680)]
 TYPES = [(torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16), (torch.float16, torch.float32),
          (torch.float16, torch.float16), (torch.float32, torch.float32)]
 
@@ -77,7 +78,11 @@ def test_layer_norm_no_rows(h3):
 
 @pytest.mark.parametrize("c", [129, 512, 5376])
 def test_layer_norm_strides_offsets_and_in_place(h3, c):
-    """Rows inside a wider buffer, at an odd offset too: the same bits as contiguous rows, the rest untouched."""
+    """Rows inside a wider buffer, at an odd offset too: in bounds, the rest untouched, in place alike.
+
+    Rows that are not 16-byte aligned may be summed in another order than aligned ones, so results are held to
+    the bounds of the formula, not to another call's bits.
+    """
     n = 21
     for off in (0, 1, 8):
         for dt in (torch.bfloat16, torch.float32):
@@ -86,20 +91,30 @@ def test_layer_norm_strides_offsets_and_in_place(h3, c):
             x = wide[:, off:off + c]
             w = randn(6, c, dtype=torch.float32)
             dy = randn(7, n, c, dtype=dt)
-            y0, mean, rstd = h3.layer_norm(x.contiguous(), w, eps=EPS)
-            g0 = h3.layer_norm_backward(dy, x.contiguous(), mean, rstd, w)
             out = torch.full_like(wide, 7.0)
-            y1, mean1, rstd1 = h3.layer_norm(x, w, eps=EPS, out=out[:, off:off + c])
-            assert torch.equal(mean, mean1) and torch.equal(y0, y1) and torch.equal(wide, keep)
+            y, mean, rstd = h3.layer_norm(x, w, eps=EPS, out=out[:, off:off + c])
+            xhat, _, _, ex = norm_terms(x, EPS)
+            want, bound = norm_y_bound(xhat, ex, w.double(), torch.zeros_like(w).double(), dt)
+            within(y, want, bound, "y")
+            y = y.clone()
+            assert torch.equal(wide, keep)
             assert bool((out[:, :off] == 7).all()) and bool((out[:, off + c:] == 7).all())
-            g1 = h3.layer_norm_backward(dy, x, mean, rstd, w, dx=out[:, off:off + c])
-            for a, b in zip(g0, g1):
-                assert torch.equal(a, b)
+            g = h3.layer_norm_backward(dy, x, mean, rstd, w, dx=out[:, off:off + c])
+            rdx, bdx, rdw, bdw, rdb, bdb = norm_backward(dy, x, w.double(), EPS, dt, _chain(n, c))
+            within(g[0], rdx, bdx, "dx")
+            within(g[1], rdw.sum(0), bdw.sum(0) + half(torch.float32) * rdw.sum(0).abs(), "dweight")
+            within(g[2], rdb.sum(0), bdb.sum(0) + half(torch.float32) * rdb.sum(0).abs(), "dbias")
+            dx = g[0].clone()
             assert bool((out[:, :off] == 7).all()) and bool((out[:, off + c:] == 7).all())
+            # in place: the same bits
             h3.layer_norm(x, w, eps=EPS, out=x)
-            assert torch.equal(x, y0) and torch.equal(wide[:, :off], keep[:, :off])
-            dy2 = dy.clone()
-            assert torch.equal(h3.layer_norm_backward(dy2, keep[:, off:off + c], mean, rstd, w, dx=dy2)[0], g0[0])
+            assert torch.equal(x, y) and torch.equal(wide[:, :off], keep[:, :off])
+            wide_dy = keep.clone()
+            wide_dy[:, off:off + c] = dy
+            view = wide_dy[:, off:off + c]
+            first = h3.layer_norm_backward(view, keep[:, off:off + c], mean, rstd, w)[0]
+            assert torch.equal(h3.layer_norm_backward(view, keep[:, off:off + c], mean, rstd, w, dx=view)[0], first)
+            within(view, dx.double(), 2 * bdx, "dx in place")
 
 
 def test_layer_norm_large_mean_and_infinite_rows(h3):
@@ -274,3 +289,31 @@ def test_norm_binding_refuses(h3):
         h3.layer_norm(x.float(), w.bfloat16())          # parameters neither of x's type nor fp32
     with pytest.raises(h3.H3Error):
         h3.layer_norm(torch.zeros(2, 16385, device="cuda"))
+
+
+def test_norm_waits_are_bounded(h3):
+    """With a wait limit of 1 ns a call either ends with its results or reports the expiry; the next ones are right.
+
+    (A wait looks several times before it looks at the clock, so rows that come quickly are not missed.)
+    """
+    x, dy = randn(1, 400, 2056), randn(2, 400, 2056)
+    w = randn(3, 2056, dtype=torch.float32)
+    ts, tags = _rows(400, 4, True)
+    table = randn(4, 12, 2, 2056, dtype=torch.float32)
+    _, mean, rstd = h3.layer_norm(x, w)
+    calls = (lambda: h3.layer_norm(x, w), lambda: h3.layer_norm_backward(dy, x, mean, rstd, w),
+             lambda: h3.adaln_modulate_backward(dy, x, ts, tags, table))
+    for call in calls:
+        want = call()
+        assert h3.h3_check_device_error() == h3.H3_OK
+        h3.h3_set_wait_limit_ns(1)
+        try:
+            got = call()
+            status = h3.h3_check_device_error()
+        finally:
+            h3.h3_set_wait_limit_ns(0)
+        assert status in (h3.H3_OK, h3.H3_ERR_TIMEOUT)
+        if status == h3.H3_OK:
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
+        assert h3.h3_check_device_error() == h3.H3_OK
+        assert all(torch.equal(a, b) for a, b in zip(want, call()))
