@@ -6,14 +6,18 @@
 //   dQ_i = scale sum_j dS_ij k_j   dK_j  = scale sum_i dS_ij q_i
 // and the query heads that share a K/V head add up in its dK and dV.
 //
-// Three kernels.  `prep` forms D (one pass over O and dO) and lays the rows'
-// (lse, D), intervals and their hulls per 128-row tile out in the workspace,
-// padded to whole tiles.  `dkdv` owns 128 keys of a K/V head and walks the query
-// tiles that see them, over all heads of the group; `dq` owns 128 query rows of
-// a head and walks their key tiles.  Both recompute S and dP, 7 products of
-// 128 x 128 x 128 per pair of tiles where a single kernel would need 5: the price
-// of sums that stay in tensor memory, need no atomics and come out the same on
-// every run.
+// `prep` forms D (one pass over O and dO) and lays the rows' (lse, D), intervals
+// and their hulls per 128-row tile out in the workspace, padded to whole tiles.  The
+// main kernel then runs two kinds of blocks: `dkdv` owns 128 keys of a K/V head and
+// walks the query tiles that see them, over all heads of the group; `dq` owns 128
+// query rows of a head and walks their key tiles.  Both recompute S and dP, 7
+// products of 128 x 128 x 128 per pair of tiles where one walk would need 5: the
+// price of sums that stay in tensor memory, need no atomics and come out the same on
+// every run.  The kinds share a launch so that the shorter dq blocks fill the SMs
+// that the dkdv blocks leave (1,127 rows x 8 heads: 72 blocks of each kind side by
+// side).  Where there are few key tiles, a tile's walk is cut into `parts`, whose
+// fp32 sums go to the workspace and are added in order by a third kernel
+// (9,001 + 5,097 rows, 14 heads over 2 K/V heads: 222 walks of up to 777 steps).
 //
 // dkdv works on S^T = K Q^T and dP^T = V dO^T (keys on the 128 TMEM lanes), so
 // that P^T and dS^T are, rounded to bf16 in place, the A operands of
@@ -72,6 +76,9 @@ struct Params {
   const int4* hull;                           // [B][n_qt] (min lo, max hi, max lo, min hi)
   __nv_bfloat16 *dq, *dk, *dv;
   long long dq_stride, dk_stride, dv_stride;  // row strides, elements
+  int n_kv_heads, n_kt, batch;                // n_kt: key tiles of 128 rows
+  int parts;                                  // pieces of a key tile's walk
+  float* partial;                             // parts > 1: [parts][B][n_kv_heads][n_kt][dV, dK][128][128]
   unsigned long long wait_limit_ns, drain_limit_ns;
   int err_slot;
 };
@@ -173,15 +180,17 @@ __device__ __forceinline__ void issue_ab(uint32_t d, uint32_t a, uint32_t b, boo
            (accumulate || kk > 0) ? 1u : 0u);
 }
 
-// This warp's 16 lanes x 64 columns of an accumulator, times `scale`, rounded to
-// bf16 rows `row_a`, `row_a + 8` (< n_rows) of an output at `out`.  Returns whether
-// all of it is finite.
-__device__ __forceinline__ bool store_tile(uint32_t taddr, float scale, __nv_bfloat16* out, long long stride,
-                                           int row_a, int n_rows, int t0) {
-  uint32_t v[32];
+// This warp's 16 lanes x 64 columns of an accumulator -> v.
+__device__ __forceinline__ void load_acc(uint32_t taddr, uint32_t (&v)[32]) {
   __syncwarp();
   tmem_ld16x256(taddr, v);
   tmem_wait_ld(v);
+}
+
+// They, times `scale`, rounded to bf16 rows `row_a`, `row_a + 8` (< n_rows) of an
+// output at `out`.
+__device__ __forceinline__ void store_tile(const uint32_t (&v)[32], float scale, __nv_bfloat16* out, long long stride,
+                                           int row_a, int n_rows, int t0) {
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
     const int col = 8 * r + 2 * t0;
@@ -192,7 +201,15 @@ __device__ __forceinline__ bool store_tile(uint32_t taddr, float scale, __nv_bfl
       *reinterpret_cast<uint32_t*>(out + (row_a + 8) * stride + col) =
           pack_bf16x2(__uint_as_float(v[4 * r + 2]) * scale, __uint_as_float(v[4 * r + 3]) * scale);
   }
-  return !any_nonfinite(v);
+}
+
+// They as fp32, rows of 128.
+__device__ __forceinline__ void store_partial(const uint32_t (&v)[32], float* out, int row_a, int t0) {
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    *reinterpret_cast<uint2*>(out + row_a * HD + 8 * r + 2 * t0) = make_uint2(v[4 * r], v[4 * r + 1]);
+    *reinterpret_cast<uint2*>(out + (row_a + 8) * HD + 8 * r + 2 * t0) = make_uint2(v[4 * r + 2], v[4 * r + 3]);
+  }
 }
 
 // Rounded values of this warp's 16 x 64 piece -> tensor memory, then one arrival.
@@ -223,12 +240,11 @@ constexpr uint32_t SMEM_BYTES = SMEM_MISC + 24 + 1024;
 constexpr uint32_t TMEM_S = 0, TMEM_DP = 128, TMEM_DV = 256, TMEM_DK = 384;
 }  // namespace dkdv
 
-// One CTA per (128 keys, K/V head, batch).
-__global__ void __launch_bounds__(THREADS, 1)
-dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const Params p) {
+// One block per (128 keys, K/V head, batch, part).
+__device__ __forceinline__ void dkdv_block(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                           const CUtensorMap& tm_do, const Params& p, uint8_t* smem_raw, int kt,
+                                           int kvh, int batch, int part) {
   using namespace dkdv;
-  extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw);
@@ -246,7 +262,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   volatile uint32_t* const again = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 16);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int k0 = blockIdx.x * BN, kvh = blockIdx.y, batch = blockIdx.z;
+  const int k0 = kt * BN;
   const uint64_t limit = p.wait_limit_ns;
   const int eslot = p.err_slot;
   const int4* const hulls = p.hull + static_cast<long long>(batch) * p.n_qt;
@@ -282,7 +298,19 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   }
   __syncthreads();
   const int qt0 = span[0], nt = span[1] - span[0] + 1;
-  if (span[1] < 0) {                             // no row sees these keys
+  // the steps (head, query tile) of this part, heads outermost
+  const int all = span[1] < 0 ? 0 : nt * p.group;
+  const int it0 = static_cast<int>(static_cast<long long>(all) * part / p.parts);
+  const int iters = static_cast<int>(static_cast<long long>(all) * (part + 1) / p.parts) - it0;
+  const int qt_first = all > 0 ? qt0 + it0 % nt : 0, head_first = kvh * p.group + (all > 0 ? it0 / nt : 0);
+  float* const sums = p.partial + ((((static_cast<long long>(part) * p.batch + batch) * p.n_kv_heads + kvh) * p.n_kt + kt) *
+                                   2) * BN * HD;      // parts > 1: dV, then dK
+  if (iters == 0) {                              // no row sees these keys
+    if (p.parts > 1) {
+      for (int i = threadIdx.x; i < 2 * BN * HD / 4; i += THREADS)
+        reinterpret_cast<uint4*>(sums)[i] = make_uint4(0u, 0u, 0u, 0u);
+      return;
+    }
     for (int i = threadIdx.x; i < BN * (HD / 8); i += THREADS) {
       const int key = k0 + i / (HD / 8), col = kvh * HD + 8 * (i % (HD / 8));
       if (key < p.n_k) {
@@ -293,7 +321,6 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
     return;
   }
-  const int iters = nt * p.group;
   // whether some row of query tile i does not see all of these keys
   auto edge_tile = [&](int i) { const int4 h = hulls[i]; return h.z > k0 || h.w < k0 + BN; };
   if (warp == W_MMA) {
@@ -311,7 +338,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       mbar_arrive_expect_tx(bar_kv, 2 * TILE_BYTES);
       load_tile(base + SMEM_K, &tm_k, bar_kv, kvh * HD, k0, batch);
       load_tile(base + SMEM_V, &tm_v, bar_kv, kvh * HD, k0, batch);
-      int issued_q = 0, issued_do = 0, qt = qt0, head = kvh * p.group;
+      int issued_q = 0, issued_do = 0, qt = qt_first, head = head_first;
       for (int it = 0; it < iters; ++it) {
         const int s = it & 1;
         const uint32_t par = ((it >> 1) - 1) & 1;
@@ -397,7 +424,7 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int key_a = k0 + lane16 + t1, key_b = key_a + 8;
     const float sl2 = p.scale_log2;
     bool ok = true;
-    int qt = qt0;
+    int qt = qt_first;
     for (int it = 0; ok && it < iters; ++it) {
       const int s = it & 1;
       // this thread's query columns: (lse, D) and intervals of two queries at a time
@@ -514,10 +541,19 @@ dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       tc_fence_after();
       const long long r0 = static_cast<long long>(batch) * p.n_k;
       const int col = kvh * HD + 64 * half;
-      bool finite = store_tile(tmem + lb + TMEM_DV + 64 * half, 1.f, p.dv + r0 * p.dv_stride + col, p.dv_stride,
-                               key_a, p.n_k, t0);
-      finite &= store_tile(tmem + lb + TMEM_DK + 64 * half, p.scale, p.dk + r0 * p.dk_stride + col, p.dk_stride,
-                           key_a, p.n_k, t0);
+      uint32_t v[32];
+      load_acc(tmem + lb + TMEM_DV + 64 * half, v);
+      bool finite = !any_nonfinite(v);
+      if (p.parts > 1)
+        store_partial(v, sums + 64 * half, lane16 + t1, t0);
+      else
+        store_tile(v, 1.f, p.dv + r0 * p.dv_stride + col, p.dv_stride, key_a, p.n_k, t0);
+      load_acc(tmem + lb + TMEM_DK + 64 * half, v);
+      finite &= !any_nonfinite(v);
+      if (p.parts > 1)
+        store_partial(v, sums + BN * HD + 64 * half, lane16 + t1, t0);
+      else
+        store_tile(v, p.scale, p.dk + r0 * p.dk_stride + col, p.dk_stride, key_a, p.n_k, t0);
       if (!finite && lane == 0) *again = 1u;
     }
   }
@@ -560,12 +596,11 @@ constexpr uint32_t SMEM_BYTES = SMEM_MISC + 8 + 1024;
 constexpr uint32_t TMEM_S = 0, TMEM_DP = 256, TMEM_DQ = 384;     // S in two buffers
 }  // namespace dq
 
-// One CTA per (128 query rows, head, batch), last rows first.
-__global__ void __launch_bounds__(THREADS, 1)
-dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const Params p) {
+// One block per (128 query rows, head, batch).
+__device__ __forceinline__ void dq_block(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                         const CUtensorMap& tm_do, const Params& p, uint8_t* smem_raw, int qt, int head,
+                                         int batch) {
   using namespace dq;
-  extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - raw);
@@ -580,7 +615,6 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
   volatile uint32_t* const abort_flag = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int qt = gridDim.x - 1 - blockIdx.x, head = blockIdx.y, batch = blockIdx.z;
   const int q_row0 = qt * BM, kv_col = head / p.group * HD;
   const uint64_t limit = p.wait_limit_ns;
   const int eslot = p.err_slot;
@@ -766,7 +800,9 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     }
     if (ok && warp_wait(bar_out, 0, abort_flag, limit, eslot)) {
       tc_fence_after();
-      store_tile(tmem + lb + TMEM_DQ + 64 * half, p.scale, out + 64 * half, p.dq_stride, q_row0 + ra, p.n_q, t0);
+      uint32_t v[32];
+      load_acc(tmem + lb + TMEM_DQ + 64 * half, v);
+      store_tile(v, p.scale, out + 64 * half, p.dq_stride, q_row0 + ra, p.n_q, t0);
     }
   }
   tc_fence_before();
@@ -775,6 +811,66 @@ dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------ launches ----
+
+constexpr uint32_t SMEM_BYTES = dkdv::SMEM_BYTES > dq::SMEM_BYTES ? dkdv::SMEM_BYTES : dq::SMEM_BYTES;
+
+// dkdv blocks first (they are longer), parts innermost; then the dq blocks, the last
+// rows first, since under a causal mask they see the most keys.
+__global__ void __launch_bounds__(THREADS, 1)
+backward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const unsigned n_dkdv = static_cast<unsigned>(p.n_kt) * p.parts * p.n_kv_heads * p.batch;
+  unsigned i = blockIdx.x;
+  if (i < n_dkdv) {
+    const int part = i % p.parts;
+    i /= p.parts;
+    const int kt = i % p.n_kt;
+    i /= p.n_kt;
+    dkdv_block(tm_q, tm_k, tm_v, tm_do, p, smem_raw, kt, i % p.n_kv_heads, i / p.n_kv_heads, part);
+  } else {
+    i -= n_dkdv;
+    const int qt = p.n_qt - 1 - static_cast<int>(i % p.n_qt);
+    i /= p.n_qt;
+    dq_block(tm_q, tm_k, tm_v, tm_do, p, smem_raw, qt, i % p.n_heads, i / p.n_heads);
+  }
+}
+
+// dV and dK of split walks: the parts' sums in order, four columns per thread.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ Params p) {
+  const long long tile_size = static_cast<long long>(2) * BN * HD;
+  const long long tiles = static_cast<long long>(p.batch) * p.n_kv_heads * p.n_kt;
+  const long long n = tiles * (tile_size / 4);
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n;
+       i += static_cast<long long>(gridDim.x) * 256) {
+    const long long tile = i / (tile_size / 4);
+    const int e = static_cast<int>(i % (tile_size / 4)) * 4;
+    const bool is_dk = e >= BN * HD;
+    const int row = (e % (BN * HD)) / HD, col = e % HD;
+    const int key = static_cast<int>(tile % p.n_kt) * BN + row;
+    if (key >= p.n_k) continue;
+    const long long bh = tile / p.n_kt;
+    const int kvh = static_cast<int>(bh % p.n_kv_heads), batch = static_cast<int>(bh / p.n_kv_heads);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* src = p.partial + tile * tile_size + e;
+#pragma unroll 4
+    for (int k = 0; k < p.parts; ++k, src += tiles * tile_size) {
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(src));
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    const float f = is_dk ? p.scale : 1.f;
+    __nv_bfloat16* out = is_dk ? p.dk : p.dv;
+    const long long stride = is_dk ? p.dk_stride : p.dv_stride;
+    *reinterpret_cast<uint2*>(out + (static_cast<long long>(batch) * p.n_k + key) * stride + kvh * HD + col) =
+        make_uint2(pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f));
   }
 }
 

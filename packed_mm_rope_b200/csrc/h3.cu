@@ -54,10 +54,8 @@ const DeviceState* device_state() {
                              static_cast<int>(h3::attn::SMEM_BYTES)) != cudaSuccess ||
         cudaFuncSetAttribute(h3::attn::attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(h3::attn::MASKED_SMEM_BYTES)) != cudaSuccess ||
-        cudaFuncSetAttribute(h3::attn_bwd::dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(h3::attn_bwd::dkdv::SMEM_BYTES)) != cudaSuccess ||
-        cudaFuncSetAttribute(h3::attn_bwd::dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(h3::attn_bwd::dq::SMEM_BYTES)) != cudaSuccess)
+        cudaFuncSetAttribute(h3::attn_bwd::backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(h3::attn_bwd::SMEM_BYTES)) != cudaSuccess)
       return nullptr;
     int n = 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0) st.sms = n;

@@ -217,19 +217,34 @@ h3_status check_attention(const h3_attn_shape* a, std::initializer_list<int64_t>
 }
 
 // Workspace of the backward call: (lse, D) per head and row, the rows'
-// intervals, and the hull of every query tile, each row count padded to tiles.
+// intervals, the hull of every query tile, each row count padded to tiles, and the
+// sums of split walks.
 struct AttentionWork {
-  int n_qt;
-  uint64_t rng, hull, bytes;             // offsets and total size; the (lse, D) pairs come first
+  int n_qt, n_kt, parts;
+  uint64_t rng, hull, partial, bytes;    // offsets and total size; the (lse, D) pairs come first
 };
+
+// Walks of key tiles are cut where there are fewer than two per SM (the dq blocks
+// behind them fill up what two or more leave): into enough parts for that, of at
+// least eight steps if every row sees every key.
+constexpr long long kWalkBlocks = 2 * 148;
+constexpr long long kWalkSteps = 8;
 
 AttentionWork attention_work(const h3_attn_shape* a) {
   AttentionWork w;
   w.n_qt = static_cast<int>((a->n_q + h3::attn::BM - 1) / h3::attn::BM);
+  w.n_kt = static_cast<int>((a->n_k + h3::attn::BN - 1) / h3::attn::BN);
+  const long long walks = static_cast<long long>(w.n_kt) * a->n_kv_heads * a->batch;
+  const long long steps = static_cast<long long>(w.n_qt) * (a->n_heads / a->n_kv_heads);
+  w.parts = walks == 0 || walks >= kWalkBlocks
+                ? 1
+                : static_cast<int>(std::max(1LL, std::min((kWalkBlocks + walks - 1) / walks, steps / kWalkSteps)));
   const uint64_t rows = static_cast<uint64_t>(w.n_qt) * h3::attn::BM * a->batch;
   w.rng = up256(rows * a->n_heads * 8u);
   w.hull = w.rng + up256(rows * 8u);
-  w.bytes = w.hull + up256(static_cast<uint64_t>(w.n_qt) * a->batch * 16u) + 256u;
+  w.partial = w.hull + up256(static_cast<uint64_t>(w.n_qt) * a->batch * 16u);
+  w.bytes = w.partial + 256u +
+            (w.parts > 1 ? static_cast<uint64_t>(w.parts) * walks * 2u * h3::attn::BN * h3::attn::HD * 4u : 0u);
   return w;
 }
 
@@ -352,6 +367,11 @@ h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const 
   p.dq_stride = st->dq;
   p.dk_stride = st->dk;
   p.dv_stride = st->dv;
+  p.n_kv_heads = a->n_kv_heads;
+  p.n_kt = w.n_kt;
+  p.batch = a->batch;
+  p.parts = w.parts;
+  p.partial = reinterpret_cast<float*>(base + w.partial);
   p.wait_limit_ns = g_wait_limit_ns.load();
   p.drain_limit_ns = kDrainLimitNs;
   p.err_slot = error_slot(stream);
@@ -359,13 +379,12 @@ h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const 
   h3::attn_bwd::prep_kernel<<<dim3(w.n_qt, heads, batch), 256, 0, s>>>(
       static_cast<const __nv_bfloat16*>(d_o), static_cast<const __nv_bfloat16*>(d_do), d_lse,
       reinterpret_cast<const int2*>(d_ranges), p.n_q, p.n_k, p.n_heads, w.n_qt, st->o, st->dout, stat, rng, hull);
-  if (keys) {
-    const unsigned n_kt = static_cast<unsigned>((a->n_k + h3::attn::BN - 1) / h3::attn::BN);
-    h3::attn_bwd::dkdv_kernel<<<dim3(n_kt, static_cast<unsigned>(a->n_kv_heads), batch), h3::attn_bwd::THREADS,
-                                h3::attn_bwd::dkdv::SMEM_BYTES, s>>>(tq, tk, tv, tdo, p);
-  }
-  h3::attn_bwd::dq_kernel<<<dim3(w.n_qt, heads, batch), h3::attn_bwd::THREADS, h3::attn_bwd::dq::SMEM_BYTES, s>>>(
+  const uint64_t blocks = static_cast<uint64_t>(w.n_kt) * w.parts * a->n_kv_heads * a->batch +
+                          static_cast<uint64_t>(w.n_qt) * heads * batch;
+  if (blocks >= (1ull << 31)) return H3_ERR_INVALID_ARG;
+  h3::attn_bwd::backward_kernel<<<static_cast<unsigned>(blocks), h3::attn_bwd::THREADS, h3::attn_bwd::SMEM_BYTES, s>>>(
       tq, tk, tv, tdo, p);
+  if (w.parts > 1) h3::attn_bwd::sum_parts_kernel<<<8 * sm_count(), 256, 0, s>>>(p);
   return launched();
 }
 
