@@ -148,9 +148,9 @@ struct Params {
   int group;                      // query heads per K/V head
 };
 
-template <bool V>
-struct Flag {
-  static constexpr bool value = V;
+template <int V>
+struct Kind {
+  static constexpr int value = V;
 };
 
 // Keys of the row's interval that exist: an empty interval is (0, 0).
@@ -226,10 +226,20 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int head = blockIdx.y;
-  const int batch = blockIdx.z;
-  // masked: the last rows first, since under a causal mask they see the most keys
-  const int q_row0 = (MASKED ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * (2 * BM);
+  // masked: a flat grid, heads fastest, so that the longest walks of all heads come
+  // first and the shortest last.  Under a causal mask the last rows see the most
+  // keys, with documents any may: the end of the sequence whose row sees more leads.
+  // (8,192 causal rows x 8 heads, 256 blocks: heads slowest leaves 1.5 times as long.)
+  const int n_tiles = (p.n_rows + 2 * BM - 1) / (2 * BM);
+  int head = blockIdx.y, batch = blockIdx.z, tile = blockIdx.x;
+  if constexpr (MASKED) {
+    head = blockIdx.x % p.n_heads;
+    tile = blockIdx.x / p.n_heads % n_tiles;
+    batch = blockIdx.x / p.n_heads / n_tiles;
+    const int2 a = clamp_range(p.ranges[0], p.n_keys), b = clamp_range(p.ranges[p.n_rows - 1], p.n_keys);
+    if (b.y - b.x >= a.y - a.x) tile = n_tiles - 1 - tile;
+  }
+  const int q_row0 = tile * (2 * BM);
   const uint64_t limit = p.wait_limit_ns;
   const int eslot = p.err_slot;
 
@@ -647,12 +657,13 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (lane == 0) mbar_arrive(bar_q_ready(wg));
     }
 
-    // One key tile.  EDGE (masked): the rows see what seen0, seen1 say of its halves
-    // or have no reference yet.  Otherwise each row has one and sees all of a half,
-    // or (bits of `none`: row a, row b of half 0, of half 1) nothing.
+    // One key tile.  Masked, EDGE: the rows see what seen0, seen1 say of its halves
+    // or have no reference yet.  WHOLE: each row has one and sees all of a half or
+    // (bits of `none`: row a, row b of half 0, of half 1) nothing.  PLAIN: all of it.
+    enum { PLAIN, WHOLE, EDGE_TILE };
     bool set_a = !MASKED, set_b = !MASKED;         // masked: the rows have a reference (else m is 0, and l)
-    auto step = [&](auto edge, int j, int seen0, int seen1, int none, const volatile uint32_t* bad) -> bool {
-      constexpr bool EDGE = decltype(edge)::value;
+    auto step = [&](auto kind, int j, int seen0, int seen1, int none, const volatile uint32_t* bad) -> bool {
+      constexpr bool EDGE = decltype(kind)::value == EDGE_TILE, SOME = decltype(kind)::value == WHOLE;
       const int key0 = (tile0 + j) * BN;
       const bool last = j == nkv - 1;
       // whether a row takes its reference from the 64 keys at `key`
@@ -661,7 +672,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int2 r = rng[i];
         return r.x < key + 64 && r.y > key;
       };
-      if (MASKED && seen0 == SEEN_NONE) {
+      if ((EDGE || SOME) && seen0 == SEEN_NONE) {
         const uint32_t pk[16] = {};
         store_p(0, pk);
       } else {
@@ -674,7 +685,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (EDGE && seen0 != SEEN_ALL) mask_logits(key0, bad, x);
         uint32_t pk[16];
         float sa, sb;
-        const bool na = MASKED && !EDGE && (none & 1), nb = MASKED && !EDGE && (none & 2);
+        const bool na = SOME && (none & 1), nb = SOME && (none & 2);
         exps(x, pk, sa, sb, na, nb);                // speculative against the references
         const bool first_a = EDGE ? first_of(set_a, 0, key0) : !MASKED && j == 0;
         const bool first_b = EDGE ? first_of(set_b, 8, key0) : !MASKED && j == 0;
@@ -691,7 +702,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         l_b += sb;
         store_p(0, pk);
       }
-      if (MASKED && seen1 == SEEN_NONE) {
+      if ((EDGE || SOME) && seen1 == SEEN_NONE) {
         const uint32_t pk[16] = {};
         store_p(1, pk);
       } else {
@@ -705,7 +716,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (EDGE && seen1 != SEEN_ALL) mask_logits(key0 + 64, bad != nullptr ? bad + 2 : bad, x);
         uint32_t pk[16];
         float sa, sb;
-        const bool na = MASKED && !EDGE && (none & 4), nb = MASKED && !EDGE && (none & 8);
+        const bool na = SOME && (none & 4), nb = SOME && (none & 8);
         exps(x, pk, sa, sb, na, nb);
         const bool first_a = EDGE && first_of(set_a, 0, key0 + 64);
         const bool first_b = EDGE && first_of(set_b, 8, key0 + 64);
@@ -729,46 +740,60 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       return true;
     };
     int edges = 0;                                 // masked, second run: tiles cleared so far
+    // masked: tiles that every row of the CTA sees in full, once all of the warp's rows have a reference
+    const int plain_end = MASKED ? min(nkv, full_hi / BN - tile0) : nkv;
+    bool refs = !MASKED;
     if (MASKED) m_a = m_b = 0.f;
-    for (int j = 0; ok && j < nkv; ++j) {
-      int seen0 = SEEN_ALL, seen1 = SEEN_ALL;       // masked: of the two halves of the tile, by the warp's rows
-      int none = 0;
-      bool plain = set_a && set_b;                  // no logit has to be masked, no reference found
-      const volatile uint32_t* bad = nullptr;
-      if (MASKED && edge_tile(j)) {
-        const int key0 = (tile0 + j) * BN;
-        if (run == 1) {
-          // all softmax warps clear V(j) together; PV(j) waits for P(j), hence for them
-          const int vidx = 2 * j + 1, vs = vidx % KV_STAGES;
-          if (!warp_wait(bar_kv_full(vs), (vidx / KV_STAGES) & 1, abort_flag, limit, eslot)) { ok = false; break; }
-          const uint2 rows = zero_nonfinite(gbase + SMEM_KV + vs * TILE_BYTES, 8 * warp, 8, lane);
-          if (lane == 0)
-            reinterpret_cast<volatile uint8_t*>(gbase + SMEM_MISC + 32 + 16 * (edges & 1))[warp] =
-                static_cast<uint8_t>(rows.x);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_v_clean);
-          if (!warp_wait(bar_v_clean, edges & 1, abort_flag, limit, eslot)) { ok = false; break; }
-          bad = unclean + 4 * (edges & 1);          // read before the next arrival: two sets are enough
-          ++edges;
+    int j = 0;
+    while (ok && j < nkv) {
+      if (refs && j < plain_end && !(MASKED && edge_tile(j))) {
+        for (; j < plain_end; ++j) {
+          if (!warp_wait(bar_s_full(wg), j & 1, abort_flag, limit, eslot)) { ok = false; break; }
+          tc_fence_after();
+          if (!step(Kind<PLAIN>{}, j, SEEN_ALL, SEEN_ALL, 0, nullptr)) { ok = false; break; }
         }
-        const int2 a = rng[0], b = rng[8];
-        auto nothing = [](int2 r, int key) { return r.x >= key + 64 || r.y <= key; };
-        auto all = [](int2 r, int key) { return r.x <= key && r.y >= key + 64; };
-        none = (nothing(a, key0) ? 1 : 0) | (nothing(b, key0) ? 2 : 0) | (nothing(a, key0 + 64) ? 4 : 0) |
-               (nothing(b, key0 + 64) ? 8 : 0);
-        plain = run == 0 && ((none & 1) || (set_a && all(a, key0))) && ((none & 2) || (set_b && all(b, key0))) &&
-                ((none & 4) || (set_a && all(a, key0 + 64))) && ((none & 8) || (set_b && all(b, key0 + 64)));
-        if (__all_sync(0xffffffffu, (none & 3) == 3)) seen0 = SEEN_NONE;
-        if (__all_sync(0xffffffffu, (none & 12) == 12)) seen1 = SEEN_NONE;
-        if (seen0 != SEEN_NONE) seen0 = SEEN_SOME;
-        if (seen1 != SEEN_NONE) seen1 = SEEN_SOME;
+        continue;
       }
-      if (!warp_wait(bar_s_full(wg), j & 1, abort_flag, limit, eslot)) { ok = false; break; }
-      tc_fence_after();
-      if (!MASKED || __all_sync(0xffffffffu, plain))
-        ok = step(Flag<false>{}, j, seen0, seen1, none, bad);
-      else
-        ok = step(Flag<true>{}, j, seen0, seen1, none, bad);
+      if constexpr (MASKED) {
+        int seen0 = SEEN_ALL, seen1 = SEEN_ALL;     // of the two halves of the tile, by the warp's rows
+        int none = 0;
+        bool plain = set_a && set_b;                // no logit has to be masked, no reference found
+        const volatile uint32_t* bad = nullptr;
+        if (edge_tile(j)) {
+          const int key0 = (tile0 + j) * BN;
+          if (run == 1) {
+            // all softmax warps clear V(j) together; PV(j) waits for P(j), hence for them
+            const int vidx = 2 * j + 1, vs = vidx % KV_STAGES;
+            if (!warp_wait(bar_kv_full(vs), (vidx / KV_STAGES) & 1, abort_flag, limit, eslot)) { ok = false; break; }
+            const uint2 rows = zero_nonfinite(gbase + SMEM_KV + vs * TILE_BYTES, 8 * warp, 8, lane);
+            if (lane == 0)
+              reinterpret_cast<volatile uint8_t*>(gbase + SMEM_MISC + 32 + 16 * (edges & 1))[warp] =
+                  static_cast<uint8_t>(rows.x);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_v_clean);
+            if (!warp_wait(bar_v_clean, edges & 1, abort_flag, limit, eslot)) { ok = false; break; }
+            bad = unclean + 4 * (edges & 1);        // read before the next arrival: two sets are enough
+            ++edges;
+          }
+          const int2 a = rng[0], b = rng[8];
+          auto nothing = [](int2 r, int key) { return r.x >= key + 64 || r.y <= key; };
+          auto all = [](int2 r, int key) { return r.x <= key && r.y >= key + 64; };
+          none = (nothing(a, key0) ? 1 : 0) | (nothing(b, key0) ? 2 : 0) | (nothing(a, key0 + 64) ? 4 : 0) |
+                 (nothing(b, key0 + 64) ? 8 : 0);
+          plain = run == 0 && ((none & 1) || (set_a && all(a, key0))) && ((none & 2) || (set_b && all(b, key0))) &&
+                  ((none & 4) || (set_a && all(a, key0 + 64))) && ((none & 8) || (set_b && all(b, key0 + 64)));
+          seen0 = __all_sync(0xffffffffu, (none & 3) == 3) ? SEEN_NONE : SEEN_SOME;
+          seen1 = __all_sync(0xffffffffu, (none & 12) == 12) ? SEEN_NONE : SEEN_SOME;
+        }
+        if (!warp_wait(bar_s_full(wg), j & 1, abort_flag, limit, eslot)) { ok = false; break; }
+        tc_fence_after();
+        if (__all_sync(0xffffffffu, plain))
+          ok = step(Kind<WHOLE>{}, j, seen0, seen1, none, bad);
+        else
+          ok = step(Kind<EDGE_TILE>{}, j, seen0, seen1, none, bad);
+        refs = __all_sync(0xffffffffu, set_a && set_b);
+        ++j;
+      }
     }
 
     // epilogue: O / l -> bf16 -> global; optional log-sum-exp

@@ -818,8 +818,9 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& tm_q, const CUtensor
 
 constexpr uint32_t SMEM_BYTES = dkdv::SMEM_BYTES > dq::SMEM_BYTES ? dkdv::SMEM_BYTES : dq::SMEM_BYTES;
 
-// dkdv blocks first (they are longer), parts innermost; then the dq blocks, the last
-// rows first, since under a causal mask they see the most keys.
+// dkdv blocks first (they are longer), then dq blocks; of each kind the heads
+// fastest and the tiles in the order of falling walks under a causal mask: the first
+// keys are seen most, the last rows see most.
 __global__ void __launch_bounds__(THREADS, 1)
 backward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -830,14 +831,14 @@ backward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   if (i < n_dkdv) {
     const int part = i % p.parts;
     i /= p.parts;
-    const int kt = i % p.n_kt;
-    i /= p.n_kt;
-    dkdv_block(tm_q, tm_k, tm_v, tm_do, p, smem_raw, kt, i % p.n_kv_heads, i / p.n_kv_heads, part);
+    const int kvh = i % p.n_kv_heads;
+    i /= p.n_kv_heads;
+    dkdv_block(tm_q, tm_k, tm_v, tm_do, p, smem_raw, i % p.n_kt, kvh, i / p.n_kt, part);
   } else {
     i -= n_dkdv;
-    const int qt = p.n_qt - 1 - static_cast<int>(i % p.n_qt);
-    i /= p.n_qt;
-    dq_block(tm_q, tm_k, tm_v, tm_do, p, smem_raw, qt, i % p.n_heads, i / p.n_heads);
+    const int head = i % p.n_heads;
+    i /= p.n_heads;
+    dq_block(tm_q, tm_k, tm_v, tm_do, p, smem_raw, p.n_qt - 1 - static_cast<int>(i % p.n_qt), head, i / p.n_qt);
   }
 }
 

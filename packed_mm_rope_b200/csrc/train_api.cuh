@@ -301,9 +301,10 @@ h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v,
   p.wait_limit_ns = g_wait_limit_ns.load();
   p.drain_limit_ns = kDrainLimitNs;
   p.err_slot = error_slot(stream);
-  const dim3 grid(static_cast<unsigned>((a->n_q + 2 * h3::attn::BM - 1) / (2 * h3::attn::BM)),
-                  static_cast<unsigned>(a->n_heads), static_cast<unsigned>(a->batch));
-  h3::attn::attention_kernel<true><<<grid, h3::attn::THREADS, h3::attn::MASKED_SMEM_BYTES, as_stream(stream)>>>(tq, tk, tv, p);
+  const uint64_t blocks = static_cast<uint64_t>((a->n_q + 2 * h3::attn::BM - 1) / (2 * h3::attn::BM)) *
+                          static_cast<uint64_t>(a->n_heads) * static_cast<uint64_t>(a->batch);
+  if (blocks >= (1ull << 31)) return H3_ERR_INVALID_ARG;
+  h3::attn::attention_kernel<true><<<static_cast<unsigned>(blocks), h3::attn::THREADS, h3::attn::MASKED_SMEM_BYTES, as_stream(stream)>>>(tq, tk, tv, p);
   return launched();
 }
 
