@@ -73,6 +73,11 @@
 // with masked pairs, and rows that do attend to such a key get a NaN logit there:
 // masked places cannot change a row, and what a row attends to is never hidden.  (Looking through V on every run, by the softmax warps or by two
 // warps of their own, made such tiles 1.5 to 2 times as long.)
+//
+// Where there are few blocks, `parts` CTAs of a cluster share a block's walk over the
+// keys.  Each leaves O, m and l of its keys in shared memory (the idle Q and K/V
+// slots); each then brings a share of the rows to their common reference, adds the
+// parts up out of the cluster's distributed shared memory, divides and stores.
 #pragma once
 
 #include "common.cuh"
@@ -103,7 +108,11 @@ constexpr int NUM_BARS = 2 + 2 * KV_STAGES + 2 + 4 + 2 + 2 + 1 + 2 + 1;
 constexpr uint32_t SMEM_MISC = SMEM_BAR + NUM_BARS * 8;       // tmem base, abort, hull, run again; two key sets
 constexpr uint32_t SMEM_RANGES = SMEM_MISC + 32 + 32;         // masked: intervals of the CTA's 256 rows
 constexpr uint32_t SMEM_BYTES = SMEM_MISC + 32 + 32 + 1024;   // + alignment slack
-constexpr uint32_t MASKED_SMEM_BYTES = SMEM_BYTES + 2 * BM * 8;
+constexpr uint32_t SMEM_ROW_ML = SMEM_RANGES + 2 * BM * 8;    // masked, parts > 1: (m, l) of the 256 rows
+constexpr uint32_t SMEM_ROW_F = SMEM_ROW_ML + 2 * BM * 8;     // and the parts' factors of the rows stored here
+constexpr uint32_t MASKED_SMEM_BYTES = SMEM_BYTES + 2 * BM * 8 + 2 * BM * 8 + 2 * BM * 4;
+constexpr int MERGE_STRIDE = HD + 4;   // floats per row of the exchanged O: rows 16 bytes apart in the banks
+static_assert(2 * BM * MERGE_STRIDE * 4 <= SMEM_BAR, "the exchanged rows must fit in the Q and K/V slots");
 static_assert(SMEM_MISC % 16 == 0, "the key sets are read 16 bytes at a time");
 
 constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, BN, false, false);   // Q, K both K-major
@@ -146,6 +155,7 @@ struct Params {
   const int2* ranges;             // [B][n_rows] key interval [lo, hi) of each query row
   int n_keys;
   int group;                      // query heads per K/V head
+  int parts;                      // CTAs (a cluster) that share a block's keys: 1, 2, 4 or 8
 };
 
 template <int V>
@@ -231,13 +241,17 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   // keys, with documents any may: the end of the sequence whose row sees more leads.
   // (8,192 causal rows x 8 heads, 256 blocks: heads slowest leaves 1.5 times as long.)
   const int n_tiles = (p.n_rows + 2 * BM - 1) / (2 * BM);
-  int head = blockIdx.y, batch = blockIdx.z, tile = blockIdx.x;
+  int head = blockIdx.y, batch = blockIdx.z, tile = blockIdx.x, part = 0;
   if constexpr (MASKED) {
-    head = blockIdx.x % p.n_heads;
-    tile = blockIdx.x / p.n_heads % n_tiles;
-    batch = blockIdx.x / p.n_heads / n_tiles;
-    const int2 a = clamp_range(p.ranges[0], p.n_keys), b = clamp_range(p.ranges[p.n_rows - 1], p.n_keys);
-    if (b.y - b.x >= a.y - a.x) tile = n_tiles - 1 - tile;
+    part = blockIdx.x % p.parts;       // the CTA's rank in its cluster
+    const int block = blockIdx.x / p.parts;
+    head = block % p.n_heads;
+    tile = block / p.n_heads % n_tiles;
+    batch = block / p.n_heads / n_tiles;
+    if (gridDim.x > 148u) {            // more than run at once on a B200
+      const int2 a = clamp_range(p.ranges[0], p.n_keys), b = clamp_range(p.ranges[p.n_rows - 1], p.n_keys);
+      if (b.y - b.x >= a.y - a.x) tile = n_tiles - 1 - tile;
+    }
   }
   const int q_row0 = tile * (2 * BM);
   const uint64_t limit = p.wait_limit_ns;
@@ -263,35 +277,48 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     mbar_fence_init();
   };
   volatile uint32_t* const again = reinterpret_cast<volatile uint32_t*>(gbase + SMEM_MISC + 24);   // masked
+  int* const hull = reinterpret_cast<int*>(gbase + SMEM_MISC + 8);                                 // masked
+  // masked: this thread's row's interval, on its way while the barriers are set up
+  int2 range = make_int2(0, 0x7fffffff);           // rows past the end see all and are never stored
+  if (MASKED && threadIdx.x < 2 * BM && q_row0 + threadIdx.x < p.n_rows)
+    range = p.ranges[static_cast<long long>(batch) * p.n_rows + q_row0 + threadIdx.x];
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
     *again = 0u;
+    hull[0] = hull[2] = 0x7fffffff;
+    hull[1] = hull[3] = 0;
     init_bars();
   }
+  auto load_q = [&] {                              // producer thread
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t dst = base + SMEM_Q + i * TILE_BYTES;
+      mbar_arrive_expect_tx(bar_q_full(i), TILE_BYTES);
+      tma_load_3d(dst, &tm_q, bar_q_full(i), head * HD, q_row0 + i * BM, batch);
+      tma_load_3d(dst + HALF_BYTES, &tm_q, bar_q_full(i), head * HD + 64, q_row0 + i * BM, batch);
+    }
+  };
   int nkv = p.n_kv_tiles;
   int tile0 = 0;                     // first key tile of this CTA
   int full_lo = 0, full_hi = 0;      // masked: keys [full_lo, full_hi) are seen by every row of the CTA
   if constexpr (MASKED) {
-    // hull of the rows' intervals, and the keys that all of them see
-    int* const hull = reinterpret_cast<int*>(gbase + SMEM_MISC + 8);
-    if (threadIdx.x == 0) {
-      hull[0] = hull[2] = 0x7fffffff;
-      hull[1] = hull[3] = 0;
+    // Q and tensor memory meanwhile
+    if (warp == W_MMA) {
+      tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+      tmem_relinquish();
     }
     __syncthreads();
+    if (warp == W_PROD && lane == 0) load_q();
+    // hull of the rows' intervals, and the keys that all of them see
     if (threadIdx.x < 2 * BM) {
-      const int row = q_row0 + threadIdx.x;
       int2 r = make_int2(0x7fffffff, 0);           // rows past the end: no say in the hull
       int all_lo = 0, all_hi = 0x7fffffff;
-      if (row < p.n_rows) {
-        r = clamp_range(p.ranges[static_cast<long long>(batch) * p.n_rows + row], p.n_keys);
+      if (q_row0 + threadIdx.x < p.n_rows) {
+        range = r = clamp_range(range, p.n_keys);
         all_lo = r.x;
         all_hi = r.y;
-        reinterpret_cast<int2*>(gbase + SMEM_RANGES)[threadIdx.x] = r;
         if (r.x >= r.y) r = make_int2(0x7fffffff, 0);
-      } else {
-        reinterpret_cast<int2*>(gbase + SMEM_RANGES)[threadIdx.x] = make_int2(0, 0x7fffffff);   // never stored
       }
+      reinterpret_cast<int2*>(gbase + SMEM_RANGES)[threadIdx.x] = range;
       const int lo = __reduce_min_sync(0xffffffffu, r.x), hi = __reduce_max_sync(0xffffffffu, r.y);
       all_hi = __reduce_min_sync(0xffffffffu, all_hi);
       all_lo = __reduce_max_sync(0xffffffffu, all_lo);
@@ -302,7 +329,9 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         atomicMax(&hull[3], all_lo);
       }
     }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
     full_hi = hull[2];
     full_lo = hull[3];
     nkv = 0;
@@ -311,46 +340,52 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       nkv = (hull[1] + BN - 1) / BN - tile0;
     }
     if (nkv == 0) {                                // no row attends to anything
-      for (int i = threadIdx.x; i < 2 * BM * (HD / 8); i += THREADS) {
-        const int row = q_row0 + i / (HD / 8);
-        if (row < p.n_rows)
-          *reinterpret_cast<uint4*>(p.o + batch * p.o_batch_stride + static_cast<long long>(row) * p.o_row_stride +
-                                    head * HD + 8 * (i % (HD / 8))) = make_uint4(0u, 0u, 0u, 0u);
+      if (part == 0) {
+        for (int i = threadIdx.x; i < 2 * BM * (HD / 8); i += THREADS) {
+          const int row = q_row0 + i / (HD / 8);
+          if (row < p.n_rows)
+            *reinterpret_cast<uint4*>(p.o + batch * p.o_batch_stride + static_cast<long long>(row) * p.o_row_stride +
+                                      head * HD + 8 * (i % (HD / 8))) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (p.lse != nullptr && threadIdx.x < 2 * BM && q_row0 + threadIdx.x < p.n_rows)
+          p.lse[(static_cast<long long>(batch) * p.n_heads + head) * p.n_rows + q_row0 + threadIdx.x] = -INFINITY;
       }
-      if (p.lse != nullptr && threadIdx.x < 2 * BM && q_row0 + threadIdx.x < p.n_rows)
-        p.lse[(static_cast<long long>(batch) * p.n_heads + head) * p.n_rows + q_row0 + threadIdx.x] = -INFINITY;
+      if (warp == W_PROD && lane == 0) {           // Q's copies end before the CTA does
+        volatile uint32_t never = 0u;
+        for (int i = 0; i < 2; ++i) mbar_wait_bounded(bar_q_full(i), 0, &never, p.drain_limit_ns, eslot);
+      }
+      if (warp == W_MMA) tmem_dealloc(*tmem_slot, TMEM_COLS);
       return;
     }
+    const int j0 = nkv * part / p.parts;           // this CTA's share of the key tiles, maybe none
+    nkv = nkv * (part + 1) / p.parts - j0;
+    tile0 += j0;
   }
-  if (warp == W_MMA) {
-    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
-    tmem_relinquish();
+  if constexpr (!MASKED) {
+    if (warp == W_MMA) {
+      tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+      tmem_relinquish();
+    }
+    if (warp == W_PROD && lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
   }
-  if (warp == W_PROD && lane == 0) {
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   // masked: whether some row of the CTA does not see all of the j-th key tile
   auto edge_tile = [&](int j) { return (tile0 + j) * BN < full_lo || (tile0 + j + 1) * BN > full_hi; };
 
-  for (int run = 0; run < (MASKED ? 2 : 1); ++run) {
+  for (int run = 0; run < (MASKED ? 2 : 1) && nkv > 0; ++run) {
   if (warp == W_PROD) {
     // ------------------------------------------------------------ TMA ----
     if (lane == 0) {
-      const int col0 = head * HD;
-      const int kv_col0 = MASKED ? head / p.group * HD : col0;
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t dst = base + SMEM_Q + i * TILE_BYTES;
-        mbar_arrive_expect_tx(bar_q_full(i), TILE_BYTES);
-        tma_load_3d(dst, &tm_q, bar_q_full(i), col0, q_row0 + i * BM, batch);
-        tma_load_3d(dst + HALF_BYTES, &tm_q, bar_q_full(i), col0 + 64, q_row0 + i * BM, batch);
-      }
+      const int kv_col0 = (MASKED ? head / p.group : head) * HD;
+      if (!MASKED || run > 0) load_q();
       int issued = 0;
       for (int idx = 0; idx < 2 * nkv; ++idx) {
         const int s = idx % KV_STAGES;
@@ -804,34 +839,51 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
       l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
       l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
-      // masked: a row without keys has l = 0 and O = 0
-      const bool empty_a = MASKED && rng[0].x >= rng[0].y, empty_b = MASKED && rng[8].x >= rng[8].y;
-      const float inv_a = empty_a ? 0.f : 1.f / l_a, inv_b = empty_b ? 0.f : 1.f / l_b;
-      __nv_bfloat16* orow_a = p.o + batch * p.o_batch_stride + static_cast<long long>(row_a) * p.o_row_stride + head * HD;
-      __nv_bfloat16* orow_b = orow_a + 8 * p.o_row_stride;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        uint32_t o[32];
-        __syncwarp();
-        tmem_ld16x256(t_o + 64 * h, o);
-        tmem_wait_ld(o);
-        if (MASKED && run == 0 && any_nonfinite(o) && (edge_tile(0) || edge_tile(nkv - 1))) *again = 1u;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int col = 64 * h + 8 * q + 2 * t0;
-          if (row_a < p.n_rows)
-            *reinterpret_cast<uint32_t*>(orow_a + col) =
-                pack_bf16x2(__uint_as_float(o[4 * q]) * inv_a, __uint_as_float(o[4 * q + 1]) * inv_a);
-          if (row_b < p.n_rows)
-            *reinterpret_cast<uint32_t*>(orow_b + col) =
-                pack_bf16x2(__uint_as_float(o[4 * q + 2]) * inv_b, __uint_as_float(o[4 * q + 3]) * inv_b);
+      if (MASKED && p.parts > 1) {
+        // the parts' rows are joined below
+        if (t0 == 0) {
+          float2* ml = reinterpret_cast<float2*>(gbase + SMEM_ROW_ML) + wg * BM + lane16 + t1;
+          ml[0] = make_float2(set_a ? m_a : -INFINITY, l_a);
+          ml[8] = make_float2(set_b ? m_b : -INFINITY, l_b);
         }
-      }
-      if (p.lse != nullptr && t0 == 0) {
-        float* lrow = p.lse + (static_cast<long long>(batch) * p.n_heads + head) * p.n_rows;
-        // masked: without keys m = l = 0 and log 0 = -inf
-        if (row_a < p.n_rows) lrow[row_a] = (m_a + __log2f(l_a)) * 0.69314718055994530942f;
-        if (row_b < p.n_rows) lrow[row_b] = (m_b + __log2f(l_b)) * 0.69314718055994530942f;
+#pragma unroll 1
+        for (int h = 0; run == 0 && h < 2; ++h) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld16x256(t_o + 64 * h, o);
+          tmem_wait_ld(o);
+          if (any_nonfinite(o) && (edge_tile(0) || edge_tile(nkv - 1))) *again = 1u;
+        }
+      } else {
+        // masked: a row without keys has l = 0 and O = 0
+        const bool empty_a = MASKED && rng[0].x >= rng[0].y, empty_b = MASKED && rng[8].x >= rng[8].y;
+        const float inv_a = empty_a ? 0.f : 1.f / l_a, inv_b = empty_b ? 0.f : 1.f / l_b;
+        __nv_bfloat16* orow_a = p.o + batch * p.o_batch_stride + static_cast<long long>(row_a) * p.o_row_stride + head * HD;
+        __nv_bfloat16* orow_b = orow_a + 8 * p.o_row_stride;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld16x256(t_o + 64 * h, o);
+          tmem_wait_ld(o);
+          if (MASKED && run == 0 && any_nonfinite(o) && (edge_tile(0) || edge_tile(nkv - 1))) *again = 1u;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int col = 64 * h + 8 * q + 2 * t0;
+            if (row_a < p.n_rows)
+              *reinterpret_cast<uint32_t*>(orow_a + col) =
+                  pack_bf16x2(__uint_as_float(o[4 * q]) * inv_a, __uint_as_float(o[4 * q + 1]) * inv_a);
+            if (row_b < p.n_rows)
+              *reinterpret_cast<uint32_t*>(orow_b + col) =
+                  pack_bf16x2(__uint_as_float(o[4 * q + 2]) * inv_b, __uint_as_float(o[4 * q + 3]) * inv_b);
+          }
+        }
+        if (p.lse != nullptr && t0 == 0) {
+          float* lrow = p.lse + (static_cast<long long>(batch) * p.n_heads + head) * p.n_rows;
+          // masked: without keys m = l = 0 and log 0 = -inf
+          if (row_a < p.n_rows) lrow[row_a] = (m_a + __log2f(l_a)) * 0.69314718055994530942f;
+          if (row_b < p.n_rows) lrow[row_b] = (m_b + __log2f(l_b)) * 0.69314718055994530942f;
+        }
       }
     }
   }
@@ -855,6 +907,82 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __syncthreads();
     tc_fence_after();
   }
+  }
+  if (MASKED && p.parts > 1) {
+    float2* const ml = reinterpret_cast<float2*>(gbase + SMEM_ROW_ML);
+    float* const factors = reinterpret_cast<float*>(gbase + SMEM_ROW_F);   // [parts][rows stored here]
+    const int per = 2 * BM / p.parts;              // rows that each CTA stores
+    if (nkv == 0) {
+      for (int i = threadIdx.x; i < 2 * BM; i += THREADS) ml[i] = make_float2(-INFINITY, 0.f);
+      if (warp == W_PROD && lane == 0) {           // Q's copies end here: nothing else waited for them
+        volatile uint32_t never = 0u;
+        for (int i = 0; i < 2; ++i) mbar_wait_bounded(bar_q_full(i), 0, &never, p.drain_limit_ns, eslot);
+      }
+    } else if (warp < SOFTMAX_WARPS) {
+      const int wg = warp >> 3, t0 = lane & 3, t1 = lane >> 2;
+      const int lane16 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
+      float* const to = reinterpret_cast<float*>(gbase) + (wg * BM + lane16 + t1) * MERGE_STRIDE + 2 * t0;
+      tc_fence_after();
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld16x256(tmem + (static_cast<uint32_t>(lane16) << 16) + TMEM_O0 + wg * 128 + 64 * h, o);
+        tmem_wait_ld(o);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          *reinterpret_cast<uint2*>(to + 64 * h + 8 * q) = make_uint2(o[4 * q], o[4 * q + 1]);
+          *reinterpret_cast<uint2*>(to + 8 * MERGE_STRIDE + 64 * h + 8 * q) = make_uint2(o[4 * q + 2], o[4 * q + 3]);
+        }
+      }
+      tc_fence_before();
+    }
+    __syncwarp();
+    cluster_sync();                                // every part's O, m and l are there
+    if (threadIdx.x < per) {
+      const int row = part * per + threadIdx.x;
+      float2 v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = q < p.parts ? ld_dsmem(base + SMEM_ROW_ML + row * 8, q) : make_float2(-INFINITY, 0.f);
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m = fmaxf(m, v[q].x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (v[q].y != 0.f) l += v[q].y * ex2_approx(v[q].x - m);   // a part that saw no key of the row has l = 0
+      const int2 r = reinterpret_cast<const int2*>(gbase + SMEM_RANGES)[row];
+      const float inv = r.x >= r.y ? 0.f : 1.f / l;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < p.parts) factors[q * per + threadIdx.x] = v[q].y != 0.f ? inv * ex2_approx(v[q].x - m) : -1.f;
+      if (p.lse != nullptr && q_row0 + row < p.n_rows)
+        p.lse[(static_cast<long long>(batch) * p.n_heads + head) * p.n_rows + q_row0 + row] =
+            (m + __log2f(l)) * 0.69314718055994530942f;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < per * (HD / 4); i += THREADS) {
+      const int r = i / (HD / 4), c = 4 * (i % (HD / 4)), row = q_row0 + part * per + r;
+      if (row >= p.n_rows) continue;
+      const uint32_t at = base + static_cast<uint32_t>(((part * per + r) * MERGE_STRIDE + c) * 4);
+      float4 v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < p.parts) v[q] = ld_dsmem4(at, q);
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float f = q < p.parts ? factors[q * per + r] : -1.f;
+        if (f == -1.f) continue;                   // nothing seen there (an O of zeros, or none at all)
+        sum.x = fmaf(v[q].x, f, sum.x);
+        sum.y = fmaf(v[q].y, f, sum.y);
+        sum.z = fmaf(v[q].z, f, sum.z);
+        sum.w = fmaf(v[q].w, f, sum.w);
+      }
+      *reinterpret_cast<uint2*>(p.o + batch * p.o_batch_stride + static_cast<long long>(row) * p.o_row_stride + head * HD +
+                                c) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+    }
+    __syncwarp();
+    cluster_sync();                                // no CTA ends while another reads its rows
   }
   if (warp == W_MMA) {
     __syncwarp();

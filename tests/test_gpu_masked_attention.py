@@ -118,14 +118,18 @@ def test_forward_without_keys_or_queries(h3):
 
 
 def test_forward_equals_the_unmasked_call(h3):
-    """Where every row sees every key the arithmetic is that of packed_attention, bit for bit."""
-    for n in (1, 82, 384, 1000):
-        q, k, v = (randn(s, n, 3, 128) for s in (1, 2, 3))
+    """Where every row sees every key the arithmetic is that of packed_attention, bit for bit, unless several CTAs
+    share a row's keys (few rows and heads, many keys: the sums are joined in another order)."""
+    for n, h, shared in ((1, 3, False), (82, 3, False), (384, 3, False), (1000, 3, True), (1000, 80, False)):
+        q, k, v = (randn(s, n, h, 128) for s in (1, 2, 3))
         ranges = torch.tensor([0, n], dtype=torch.int32, device="cuda").repeat(n, 1)
-        lse = torch.empty(3, n, device="cuda")
+        lse = torch.empty(h, n, device="cuda")
         want = h3.packed_attention(q, k, v, lse=lse)
         got = _run(h3, q, k, v, ranges)
-        assert torch.equal(want, got["o"]) and torch.equal(lse, got["lse"])
+        if shared:
+            check_attention(got, attend(q, k, v, ranges), ("o", "lse"))
+        else:
+            assert torch.equal(want, got["o"]) and torch.equal(lse, got["lse"])
 
 
 @pytest.mark.parametrize("scale", [0.02, 0.5, 3.0])
@@ -220,3 +224,34 @@ def test_masked_binding_refuses(h3):
             f()
     with pytest.raises(h3.H3Error):
         A(q, k, k, r, softmax_scale=float("nan"))
+
+
+@pytest.mark.parametrize("nq,nk,h,kv", [(1, 20000, 1, 1), (5, 4099, 6, 2), (300, 5000, 2, 2), (700, 1500, 4, 1),
+                                        (1100, 1100, 16, 16), (2000, 2000, 20, 5)])
+def test_forward_shared_walks(h3, nq, nk, h, kv):
+    """Few query rows against many keys: several CTAs share a walk; parts without a visible key for a row too."""
+    q, k, v = randn(1, nq, h, 128), randn(2, nk, kv, 128), randn(3, nk, kv, 128)
+    full = torch.tensor([0, nk], dtype=torch.int32, device="cuda").repeat(nq, 1)
+    narrow = _intervals(nq, nk, 7)
+    narrow[: nq // 2, 1] = narrow[: nq // 2, 0].clamp(min=0) + 3           # three keys somewhere
+    for ranges in (full, _intervals(nq, nk, nq + nk), narrow):
+        got = _run(h3, q, k, v, ranges)
+        check_attention(got, attend(q, k, v, ranges), ("o", "lse"))
+        again = _run(h3, q, k, v, ranges)
+        assert torch.equal(got["o"], again["o"]) and torch.equal(got["lse"], again["lse"])
+
+
+def test_forward_shared_walks_with_bad_keys(h3):
+    """As above with inf and NaN in masked places of K and V: the rows that do not see them keep their bits."""
+    nq, nk = 200, 6000
+    q, k, v = randn(1, nq, 2, 128), randn(2, nk, 1, 128), randn(3, nk, 1, 128)
+    ranges = torch.tensor([100, 5000], dtype=torch.int32, device="cuda").repeat(nq, 1)
+    ranges[77] = torch.tensor([0, 6000])
+    clean = _run(h3, q, k, v, ranges)
+    for t in (k, v):
+        t[5100:5300] = float("nan")
+        t[3, 0, 9] = float("inf")
+    got = _run(h3, q, k, v, ranges)
+    keep = torch.arange(nq, device="cuda") != 77
+    assert torch.equal(got["o"][keep], clean["o"][keep]) and torch.equal(got["lse"][:, keep], clean["lse"][:, keep])
+    assert not bool(torch.isfinite(got["o"][77]).any())
