@@ -85,9 +85,9 @@ struct Params {
 
 // ------------------------------------------------------------------ prep ----
 
-// One block per (query tile, head, batch): 16 lanes per row, 16 rows at a time.
-// Blocks of head 0 also write the tile's intervals and hull.  Bound by the
-// reads of O and dO.
+// One block per (query tile, head, batch): 16 lanes per row, 16 rows at a time, four
+// such steps' loads in flight.  Blocks of head 0 also write the tile's intervals and
+// hull.  Bound by the reads of O and dO.
 __global__ void __launch_bounds__(256) prep_kernel(const __nv_bfloat16* __restrict__ o,
                                                    const __nv_bfloat16* __restrict__ dout,
                                                    const float* __restrict__ lse, const int2* __restrict__ ranges,
@@ -95,38 +95,43 @@ __global__ void __launch_bounds__(256) prep_kernel(const __nv_bfloat16* __restri
                                                    long long do_stride, float2* __restrict__ stat,
                                                    int2* __restrict__ rng, int4* __restrict__ hull) {
   const int tile = blockIdx.x, head = blockIdx.y, batch = blockIdx.z;
-  const int sub = threadIdx.x & 15;
+  const int sub = threadIdx.x & 15, first = tile * BM + (threadIdx.x >> 4);
   const long long bh = static_cast<long long>(batch) * n_heads + head;
+  const long long row0 = static_cast<long long>(batch) * n_q;
+  int2 range = make_int2(0, 0);
+  if (head == 0 && threadIdx.x < BM && tile * BM + threadIdx.x < n_q) range = ranges[row0 + tile * BM + threadIdx.x];
 #pragma unroll
-  for (int it = 0; it < BM / 16; ++it) {
-    const int row = tile * BM + it * 16 + (threadIdx.x >> 4);
-    float d = 0.f;
-    if (row < n_q) {
-      const long long r = static_cast<long long>(batch) * n_q + row;
-      const uint4 a = *reinterpret_cast<const uint4*>(o + r * o_stride + head * HD + 8 * sub);
-      const uint4 b = *reinterpret_cast<const uint4*>(dout + r * do_stride + head * HD + 8 * sub);
-      const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+  for (int half = 0; half < 2; ++half) {
+    uint4 a[4], b[4];
+    float l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = min(first + (4 * half + i) * 16, n_q - 1);   // rows past the end: read, not used
+      a[i] = __ldcs(reinterpret_cast<const uint4*>(o + (row0 + row) * o_stride + head * HD + 8 * sub));
+      b[i] = *reinterpret_cast<const uint4*>(dout + (row0 + row) * do_stride + head * HD + 8 * sub);
+      l[i] = lse[bh * n_q + row];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = first + (4 * half + i) * 16;
+      const uint32_t wa[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, wb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
       float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int m = 0; m < 4; ++m)
         s = __ffma2_rn(make_float2(__uint_as_float(wa[m] << 16), __uint_as_float(wa[m] & 0xffff0000u)),
                        make_float2(__uint_as_float(wb[m] << 16), __uint_as_float(wb[m] & 0xffff0000u)), s);
-      d = s.x + s.y;
-    }
+      float d = s.x + s.y;
 #pragma unroll
-    for (int k = 8; k > 0; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
-    if (sub == 0) {
+      for (int k = 8; k > 0; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
       // rows without keys (lse = -inf) are masked everywhere
-      const float l = row < n_q ? lse[bh * n_q + row] * 1.4426950408889634f : 0.f;
-      stat[bh * n_qt * BM + row] = make_float2(l, d);
+      if (sub == 0)
+        stat[bh * n_qt * BM + row] = row < n_q ? make_float2(l[i] * 1.4426950408889634f, d) : make_float2(0.f, 0.f);
     }
   }
   if (head == 0) {
     __shared__ int part[4][4];
     if (threadIdx.x < BM) {
-      const int row = tile * BM + threadIdx.x;
-      const int2 r = row < n_q ? attn::clamp_range(ranges[static_cast<long long>(batch) * n_q + row], n_k)
-                               : make_int2(0, 0);
+      const int2 r = attn::clamp_range(range, n_k);
       rng[(static_cast<long long>(batch) * n_qt + tile) * BM + threadIdx.x] = make_int2(r.x, r.y - r.x);
       const bool some = r.x < r.y;
       const int lo = __reduce_min_sync(0xffffffffu, some ? r.x : 0x7fffffff);
