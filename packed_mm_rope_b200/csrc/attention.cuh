@@ -61,9 +61,9 @@
 // head).  The CTA visits the key tiles of the hull of its rows' intervals.  In
 // tiles that some row does not see in full, each warp tells by votes whether none
 // of its 16 rows sees any of a 64-key half (P = 0 without a look at S), or each
-// row sees all of it or nothing (the code above with a reference of +inf, hence
-// numerators of 0, for the latter), or an interval ends inside: then logits
-// outside a row's interval become -inf.  A row takes
+// row sees all of it or nothing (a reference of +inf, hence numerators of 0, for
+// the latter), or an interval ends inside: then logits outside a row's interval
+// become -inf.  A row takes
 // its reference m from its first half with a visible key; a row without one ends
 // with l = 0, O = 0 and a log-sum-exp of -inf.
 // P = 0 does not hide a V row that holds inf or NaN (0 x inf = NaN on the tensor
@@ -158,9 +158,9 @@ struct Params {
   int parts;                      // CTAs (a cluster) that share a block's keys: 1, 2, 4 or 8
 };
 
-template <int V>
-struct Kind {
-  static constexpr int value = V;
+template <bool V>
+struct Flag {
+  static constexpr bool value = V;
 };
 
 // Keys of the row's interval that exist: an empty interval is (0, 0).
@@ -547,7 +547,6 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
       }
     };
-    enum { SEEN_NONE, SEEN_SOME, SEEN_ALL };       // what a warp's 16 rows see of 64 keys
     auto mask_logits = [&](int key0, const volatile uint32_t* bad, float (&x)[32]) {
       const int2 a = rng[0], b = rng[8];
       const unsigned len_a = a.y - a.x, len_b = b.y - b.x;
@@ -692,22 +691,13 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (lane == 0) mbar_arrive(bar_q_ready(wg));
     }
 
-    // One key tile.  Masked, EDGE: the rows see what seen0, seen1 say of its halves
-    // or have no reference yet.  WHOLE: each row has one and sees all of a half or
-    // (bits of `none`: row a, row b of half 0, of half 1) nothing.  PLAIN: all of it.
-    enum { PLAIN, WHOLE, EDGE_TILE };
-    bool set_a = !MASKED, set_b = !MASKED;         // masked: the rows have a reference (else m is 0, and l)
-    auto step = [&](auto kind, int j, int seen0, int seen1, int none, const volatile uint32_t* bad) -> bool {
-      constexpr bool EDGE = decltype(kind)::value == EDGE_TILE, SOME = decltype(kind)::value == WHOLE;
-      const int key0 = (tile0 + j) * BN;
+    // One key tile, references set (unmasked: from its first half on).  SOME (masked):
+    // each row sees all of a half or (bits of `none`: row a, row b of half 0, of half
+    // 1) nothing; otherwise all of the tile.
+    auto plain_step = [&](auto some, int j, int none) -> bool {
+      constexpr bool SOME = decltype(some)::value;
       const bool last = j == nkv - 1;
-      // whether a row takes its reference from the 64 keys at `key`
-      auto first_of = [&](bool set, int i, int key) {
-        if (set) return false;
-        const int2 r = rng[i];
-        return r.x < key + 64 && r.y > key;
-      };
-      if ((EDGE || SOME) && seen0 == SEEN_NONE) {
+      if (SOME && __all_sync(0xffffffffu, (none & 3) == 3)) {
         const uint32_t pk[16] = {};
         store_p(0, pk);
       } else {
@@ -717,18 +707,15 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tmem_wait_ld(r);
         float x[32];
         to_logits(r, 0, last, x);
-        if (EDGE && seen0 != SEEN_ALL) mask_logits(key0, bad, x);
         uint32_t pk[16];
         float sa, sb;
         const bool na = SOME && (none & 1), nb = SOME && (none & 2);
         exps(x, pk, sa, sb, na, nb);                // speculative against the references
-        const bool first_a = EDGE ? first_of(set_a, 0, key0) : !MASKED && j == 0;
-        const bool first_b = EDGE ? first_of(set_b, 8, key0) : !MASKED && j == 0;
-        const bool need = first_a || first_b || !(sa <= PART_LIMIT) || !(sb <= PART_LIMIT);
+        const bool first = !MASKED && j == 0;
+        const bool need = first || !(sa <= PART_LIMIT) || !(sb <= PART_LIMIT);
         if (__any_sync(0xffffffffu, need)) {
           float fa, fb;
-          new_reference(x, first_a, first_b, sa, sb, fa, fb);
-          if (EDGE) set_a |= first_a, set_b |= first_b;
+          new_reference(x, first, first, sa, sb, fa, fb);
           __syncwarp();
           if (j > 0) rescale_o(fa, fb);   // O holds PV(j-1); PV(j) has not started
           exps(x, pk, sa, sb, na, nb);
@@ -737,7 +724,7 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         l_b += sb;
         store_p(0, pk);
       }
-      if ((EDGE || SOME) && seen1 == SEEN_NONE) {
+      if (SOME && __all_sync(0xffffffffu, (none & 12) == 12)) {
         const uint32_t pk[16] = {};
         store_p(1, pk);
       } else {
@@ -748,22 +735,18 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tmem_wait_ld(r);
         float x[32];
         to_logits(r, 64, last, x);
-        if (EDGE && seen1 != SEEN_ALL) mask_logits(key0 + 64, bad != nullptr ? bad + 2 : bad, x);
         uint32_t pk[16];
         float sa, sb;
         const bool na = SOME && (none & 4), nb = SOME && (none & 8);
         exps(x, pk, sa, sb, na, nb);
-        const bool first_a = EDGE && first_of(set_a, 0, key0 + 64);
-        const bool first_b = EDGE && first_of(set_b, 8, key0 + 64);
-        const bool need = first_a || first_b || !(sa <= PART_LIMIT) || !(sb <= PART_LIMIT);
+        const bool need = !(sa <= PART_LIMIT) || !(sb <= PART_LIMIT);
         if (__any_sync(0xffffffffu, need)) {
           // the first half of PV(j) may be in flight: let it land, then rescale
           // O (which now includes it) together with the running sums
           if (!warp_wait(bar_pva_done(wg), j & 1, abort_flag, limit, eslot)) return false;
           tc_fence_after();
           float fa, fb;
-          new_reference(x, first_a, first_b, sa, sb, fa, fb);
-          if (EDGE) set_a |= first_a, set_b |= first_b;
+          new_reference(x, false, false, sa, sb, fa, fb);
           __syncwarp();
           rescale_o(fa, fb);
           exps(x, pk, sa, sb, na, nb);
@@ -774,10 +757,77 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       return true;
     };
+    bool set_a = !MASKED, set_b = !MASKED;         // masked: the rows have a reference (else m is 0, and l)
     int edges = 0;                                 // masked, second run: tiles cleared so far
-    // masked: tiles that every row of the CTA sees in full, once all of the warp's rows have a reference
+    // what a row sees of the 64 keys from `key` on
+    auto nothing = [](int2 r, int key) { return r.x >= key + 64 || r.y <= key; };
+    auto all = [](int2 r, int key) { return r.x <= key && r.y >= key + 64; };
+    // masked: the same where an interval ends inside a half, where a row has no
+    // reference yet, and in the second run; the halves in a loop, since this code runs a
+    // few times per CTA, often from a cold instruction cache
+    auto edge_step = [&](int j) -> bool {
+      const volatile uint32_t* bad = nullptr;       // second run: the keys that had inf or NaN in V
+      if (run == 1 && edge_tile(j)) {
+        // all softmax warps clear V(j) together; PV(j) waits for P(j), hence for them
+        const int vidx = 2 * j + 1, vs = vidx % KV_STAGES;
+        if (!warp_wait(bar_kv_full(vs), (vidx / KV_STAGES) & 1, abort_flag, limit, eslot)) return false;
+        const uint2 rows = zero_nonfinite(gbase + SMEM_KV + vs * TILE_BYTES, 8 * warp, 8, lane);
+        if (lane == 0)
+          reinterpret_cast<volatile uint8_t*>(gbase + SMEM_MISC + 32 + 16 * (edges & 1))[warp] =
+              static_cast<uint8_t>(rows.x);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_v_clean);
+        if (!warp_wait(bar_v_clean, edges & 1, abort_flag, limit, eslot)) return false;
+        bad = unclean + 4 * (edges & 1);            // read before the next arrival: two sets are enough
+        ++edges;
+      }
+      if (!warp_wait(bar_s_full(wg), j & 1, abort_flag, limit, eslot)) return false;
+      tc_fence_after();
+      const int2 ra = rng[0], rb = rng[8];
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const int key0 = (tile0 + j) * BN + 64 * h;
+        const bool none_a = nothing(ra, key0), none_b = nothing(rb, key0);
+        uint32_t pk[16];
+        if (__all_sync(0xffffffffu, none_a && none_b)) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = 0u;
+        } else {
+          const bool cut = !(none_a || all(ra, key0)) || !(none_b || all(rb, key0));
+          const bool mask = run == 1 || __any_sync(0xffffffffu, cut);   // logit by logit
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld16x256(t_s + 64 * h, r);
+          tmem_wait_ld(r);
+          float x[32];
+          to_logits(r, 0, false, x);
+          if (mask) mask_logits(key0, bad != nullptr ? bad + 2 * h : bad, x);
+          float sa, sb;
+          exps(x, pk, sa, sb, !mask && none_a, !mask && none_b);
+          const bool first_a = !set_a && !none_a, first_b = !set_b && !none_b;
+          if (__any_sync(0xffffffffu, first_a || first_b || !(sa <= PART_LIMIT) || !(sb <= PART_LIMIT))) {
+            if (h == 1) {
+              if (!warp_wait(bar_pva_done(wg), j & 1, abort_flag, limit, eslot)) return false;
+              tc_fence_after();
+            }
+            float fa, fb;
+            new_reference(x, first_a, first_b, sa, sb, fa, fb);
+            set_a |= first_a;
+            set_b |= first_b;
+            __syncwarp();
+            if (j + h > 0) rescale_o(fa, fb);
+            exps(x, pk, sa, sb, !mask && none_a, !mask && none_b);
+          }
+          l_a += sa;
+          l_b += sb;
+        }
+        store_p(h, pk);
+      }
+      return true;
+    };
+    // masked: up to here tiles are seen in full by every row of the CTA, from some tile on
     const int plain_end = MASKED ? min(nkv, full_hi / BN - tile0) : nkv;
-    bool refs = !MASKED;
+    bool refs = !MASKED;                           // masked: all rows of the warp have a reference
     if (MASKED) m_a = m_b = 0.f;
     int j = 0;
     while (ok && j < nkv) {
@@ -785,48 +835,25 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (; j < plain_end; ++j) {
           if (!warp_wait(bar_s_full(wg), j & 1, abort_flag, limit, eslot)) { ok = false; break; }
           tc_fence_after();
-          if (!step(Kind<PLAIN>{}, j, SEEN_ALL, SEEN_ALL, 0, nullptr)) { ok = false; break; }
+          if (!plain_step(Flag<false>{}, j, 0)) { ok = false; break; }
         }
-        continue;
-      }
-      if constexpr (MASKED) {
-        int seen0 = SEEN_ALL, seen1 = SEEN_ALL;     // of the two halves of the tile, by the warp's rows
-        int none = 0;
-        bool plain = set_a && set_b;                // no logit has to be masked, no reference found
-        const volatile uint32_t* bad = nullptr;
-        if (edge_tile(j)) {
-          const int key0 = (tile0 + j) * BN;
-          if (run == 1) {
-            // all softmax warps clear V(j) together; PV(j) waits for P(j), hence for them
-            const int vidx = 2 * j + 1, vs = vidx % KV_STAGES;
-            if (!warp_wait(bar_kv_full(vs), (vidx / KV_STAGES) & 1, abort_flag, limit, eslot)) { ok = false; break; }
-            const uint2 rows = zero_nonfinite(gbase + SMEM_KV + vs * TILE_BYTES, 8 * warp, 8, lane);
-            if (lane == 0)
-              reinterpret_cast<volatile uint8_t*>(gbase + SMEM_MISC + 32 + 16 * (edges & 1))[warp] =
-                  static_cast<uint8_t>(rows.x);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_v_clean);
-            if (!warp_wait(bar_v_clean, edges & 1, abort_flag, limit, eslot)) { ok = false; break; }
-            bad = unclean + 4 * (edges & 1);        // read before the next arrival: two sets are enough
-            ++edges;
+      } else if constexpr (MASKED) {
+        const int key0 = (tile0 + j) * BN;
+        const int2 a = rng[0], b = rng[8];
+        const int none = (nothing(a, key0) ? 1 : 0) | (nothing(b, key0) ? 2 : 0) | (nothing(a, key0 + 64) ? 4 : 0) |
+                         (nothing(b, key0 + 64) ? 8 : 0);
+        const bool some = ((none & 1) || (set_a && all(a, key0))) && ((none & 2) || (set_b && all(b, key0))) &&
+                          ((none & 4) || (set_a && all(a, key0 + 64))) && ((none & 8) || (set_b && all(b, key0 + 64)));
+        if (run == 0 && __all_sync(0xffffffffu, some)) {
+          ok = warp_wait(bar_s_full(wg), j & 1, abort_flag, limit, eslot);
+          if (ok) {
+            tc_fence_after();
+            ok = plain_step(Flag<true>{}, j, none);
           }
-          const int2 a = rng[0], b = rng[8];
-          auto nothing = [](int2 r, int key) { return r.x >= key + 64 || r.y <= key; };
-          auto all = [](int2 r, int key) { return r.x <= key && r.y >= key + 64; };
-          none = (nothing(a, key0) ? 1 : 0) | (nothing(b, key0) ? 2 : 0) | (nothing(a, key0 + 64) ? 4 : 0) |
-                 (nothing(b, key0 + 64) ? 8 : 0);
-          plain = run == 0 && ((none & 1) || (set_a && all(a, key0))) && ((none & 2) || (set_b && all(b, key0))) &&
-                  ((none & 4) || (set_a && all(a, key0 + 64))) && ((none & 8) || (set_b && all(b, key0 + 64)));
-          seen0 = __all_sync(0xffffffffu, (none & 3) == 3) ? SEEN_NONE : SEEN_SOME;
-          seen1 = __all_sync(0xffffffffu, (none & 12) == 12) ? SEEN_NONE : SEEN_SOME;
+        } else {
+          ok = edge_step(j);
+          refs = __all_sync(0xffffffffu, set_a && set_b);
         }
-        if (!warp_wait(bar_s_full(wg), j & 1, abort_flag, limit, eslot)) { ok = false; break; }
-        tc_fence_after();
-        if (__all_sync(0xffffffffu, plain))
-          ok = step(Kind<WHOLE>{}, j, seen0, seen1, none, bad);
-        else
-          ok = step(Kind<EDGE_TILE>{}, j, seen0, seen1, none, bad);
-        refs = __all_sync(0xffffffffu, set_a && set_b);
         ++j;
       }
     }
