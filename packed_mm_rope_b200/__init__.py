@@ -268,57 +268,28 @@ def adaln_modulate(x, timestep_index, token_tag, table, out=None, eps: float = 1
 # ------------------------------------------------ masks, grouped heads, training --
 #
 # These calls are short against a Python interpreter (some kernels take 2 us), so
-# the checks below read each attribute of a tensor once.
+# their checks and allocations are compiled (csrc/binding.cpp); the functions below
+# carry the defaults and the documentation.
 
 MASK_MODES = {"document": _lib.H3_MASK_DOCUMENT, "prefix_causal": _lib.H3_MASK_PREFIX_CAUSAL,
               "prefix_block": _lib.H3_MASK_PREFIX_BLOCK}
 
-
-def _empty(stream, *args, **kw):
-    """torch.empty for use on ``stream`` (None: the current one)."""
-    import torch
-    if stream is None:
-        return torch.empty(*args, **kw)
-    with torch.cuda.stream(stream):
-        return torch.empty(*args, **kw)
+_compiled = None
 
 
-def _empty_like(x, stream):
-    """A contiguous tensor shaped as ``x`` for use on ``stream`` (None: the current one)."""
-    import torch
-    if stream is None:
-        return torch.empty_like(x, memory_format=torch.contiguous_format)
-    with torch.cuda.stream(stream):
-        return torch.empty_like(x, memory_format=torch.contiguous_format)
-
-
-def _heads(x, dev: int, what: str):
-    """(batch, n_rows, n_heads, row_stride) of a [.., N, H, 128] bf16 view on device ``dev``."""
-    import torch
-    shape, stride = x.shape, x.stride()
-    if x.dtype is not torch.bfloat16 or x.get_device() != dev:
-        raise TypeError(f"{what} must be a bf16 tensor on the current CUDA device")
-    if len(shape) == 3:
-        n, h, d = shape
-        rs, hs, ds = stride
-        b = 1
-    elif len(shape) == 4:
-        b, n, h, d = shape
-        bs, rs, hs, ds = stride
-        if b > 1 and bs != n * rs:
-            raise ValueError(f"{what}: the batch stride must be n_rows * row_stride")
-    else:
-        raise ValueError(f"{what} must be [N, H, 128] or [B, N, H, 128]")
-    if d != 128 or ds != 1 or hs != 128:
-        raise ValueError(f"{what} must be [N, H, 128] or [B, N, H, 128] with heads contiguous")
-    return b, n, h, (rs if n > 1 or b > 1 else max(rs, 128 * h))
-
-
-def _plain(t, dev: int, dtype, numel: int, what: str) -> int:
-    """data_ptr of a contiguous tensor of ``numel`` elements of ``dtype`` on device ``dev``."""
-    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {numel} elements on the current CUDA device")
-    return t.data_ptr()
+def _binding():
+    """The compiled tensor binding (built by ``python -m packed_mm_rope_b200.build``)."""
+    global _compiled
+    if _compiled is None:
+        load()
+        import torch  # noqa: F401  (its libraries, which the binding links against)
+        try:
+            from . import _tensors as mod
+        except ImportError as e:
+            raise ImportError(f"_tensors.so not built or stale (run python -m packed_mm_rope_b200.build): {e}") from e
+        mod.set_error(H3Error)
+        _compiled = mod
+    return _compiled
 
 
 def mmrope_rotate(q, k, coords, q_out=None, k_out=None, inverse: bool = False, theta=10000.0,
@@ -329,34 +300,8 @@ def mmrope_rotate(q, k, coords, q_out=None, k_out=None, inverse: bool = False, t
     may be None.  ``inverse`` rotates back: it maps the gradients of the rotated
     Q and K to those of the unrotated ones.  Pass q_out=q, k_out=k for in place.
     """
-    import torch
-    dev = torch.cuda.current_device()
-    rows = None
-    ptr, out_ptr, heads, stride, out_stride, outs = [0, 0], [0, 0], [0, 0], [0, 0], [0, 0], [None, None]
-    for i, (x, out) in enumerate(((q, q_out), (k, k_out))):
-        if x is None:
-            if out is not None:
-                raise ValueError("an output without its input")
-            continue
-        b, n, h, stride[i] = _heads(x, dev, "q and k")
-        if rows is not None and rows != (b, n):
-            raise ValueError("q and k differ in their rows")
-        rows = (b, n)
-        if out is None:
-            out = _empty_like(x, stream)
-            out_stride[i] = 128 * h
-        else:
-            ob, on, oh, out_stride[i] = _heads(out, dev, "outputs")
-            if (ob, on, oh) != (b, n, h):
-                raise ValueError("outputs must have the inputs' shape")
-        ptr[i], out_ptr[i], heads[i], outs[i] = x.data_ptr(), out.data_ptr(), h, out
-    if rows is None:
-        raise ValueError("neither q nor k given")
-    n = rows[0] * rows[1]
-    h3_mmrope_rotate(ptr[0], ptr[1], out_ptr[0], out_ptr[1], _plain(coords, dev, torch.float32, 3 * n, "coords"), n,
-                     heads[0], heads[1], stride[0], stride[1], out_stride[0], out_stride[1],
-                     rope_cfg(theta, 128, sections, pair_layout, freq_rule), inverse, _stream(stream))
-    return outs[0], outs[1]
+    return (_compiled or _binding()).rotate(q, k, coords, q_out, k_out, inverse, theta, sections[0], sections[1],
+                                            sections[2], pair_layout, freq_rule, stream)
 
 
 def build_key_ranges(doc_starts, n_rows: int, mode: str = "document", prefix=None, out=None, stream=None):
@@ -367,37 +312,10 @@ def build_key_ranges(doc_starts, n_rows: int, mode: str = "document", prefix=Non
     document), "prefix_causal" (the prefix, then rows up to itself) or "prefix_block" (prefix rows
     attend to the prefix, the others to the whole document).  Rows in no document get (0, 0).
     """
-    import torch
     code = MASK_MODES.get(mode)
     if code is None:
         raise ValueError(f"mode must be one of {sorted(MASK_MODES)}")
-    dev = torch.cuda.current_device()
-    n_docs = doc_starts.numel() - 1
-    if n_docs < 0 or doc_starts.dim() != 1:
-        raise ValueError("doc_starts must be a contiguous int32 [documents + 1] tensor")
-    starts = _plain(doc_starts, dev, torch.int32, n_docs + 1, "doc_starts")
-    lengths = _plain(prefix, dev, torch.int32, n_docs, "prefix") if prefix is not None else 0
-    if out is None:
-        out = _empty(stream, (n_rows, 2), dtype=torch.int32, device=doc_starts.device)
-    h3_build_key_ranges(starts, lengths, n_docs, n_rows, code, _plain(out, dev, torch.int32, 2 * n_rows, "out"),
-                        _stream(stream))
-    return out
-
-
-def _masked_shape(q, k, v, key_ranges, softmax_scale, dev: int):
-    """(shape struct, strides of q, k, v, pointer of key_ranges) of a masked attention problem, checked."""
-    import torch
-    b, n, h, qs = _heads(q, dev, "q")
-    kb, nk, hk, ks = _heads(k, dev, "k")
-    vb, nv, hv, vs = _heads(v, dev, "v")
-    if vb != kb or nv != nk or hv != hk or kb != b:
-        raise ValueError("k and v must have one shape and q's batch")
-    if h < 1 or hk < 1 or h % hk:
-        raise ValueError("the query heads must be a multiple of the K/V heads")
-    if key_ranges.dim() < 2 or key_ranges.shape[-1] != 2:
-        raise ValueError("key_ranges must be contiguous int32 [rows, 2]")
-    r = _plain(key_ranges, dev, torch.int32, 2 * b * n, "key_ranges")
-    return h3_attn_shape(n, nk, b, h, hk, 128, softmax_scale), qs, ks, vs, r
+    return (_compiled or _binding()).key_ranges(doc_starts, n_rows, code, prefix, out, stream)
 
 
 def masked_attention(q, k, v, key_ranges, out=None, lse=None, softmax_scale: float = 0.0, stream=None):
@@ -408,20 +326,7 @@ def masked_attention(q, k, v, key_ranges, out=None, lse=None, softmax_scale: flo
     intervals.  Rows that attend to nothing give O = 0 and lse = -inf.  lse: fp32 [B, H, Nq], written
     if given (``masked_attention_backward`` needs it).
     """
-    import torch
-    dev = torch.cuda.current_device()
-    shape, qs, ks, vs, r = _masked_shape(q, k, v, key_ranges, softmax_scale, dev)
-    b, n, h = shape.batch, shape.n_q, shape.n_heads
-    if out is None:
-        out, os_ = _empty_like(q, stream), 128 * h
-    else:
-        ob, on, oh, os_ = _heads(out, dev, "out")
-        if (ob, on, oh) != (b, n, h):
-            raise ValueError("output must have q's shape")
-    lp = _plain(lse, dev, torch.float32, b * h * n, "lse") if lse is not None else 0
-    h3_masked_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, r, shape, qs, ks, vs, os_,
-                        _stream(stream))
-    return out
+    return (_compiled or _binding()).attention(q, k, v, key_ranges, out, lse, softmax_scale, stream)
 
 
 def masked_attention_backward(dout, q, k, v, out, lse, key_ranges, dq=None, dk=None, dv=None,
@@ -431,58 +336,8 @@ def masked_attention_backward(dout, q, k, v, out, lse, key_ranges, dq=None, dk=N
     out, lse: what the forward call gave for the same q, k, v, key_ranges and scale.  workspace: uint8,
     ``h3_masked_attention_backward_workspace_bytes`` bytes, one per call that may overlap in time.
     """
-    import torch
-    dev = torch.cuda.current_device()
-    shape, qs, ks, vs, r = _masked_shape(q, k, v, key_ranges, softmax_scale, dev)
-    b, n, h, nk, hk = shape.batch, shape.n_q, shape.n_heads, shape.n_k, shape.n_kv_heads
-
-    def grad(t, x, rows, heads, what):
-        if t is None:
-            return _empty_like(x, stream), 128 * heads
-        tb, tn, th, ts = _heads(t, dev, what)
-        if (tb, tn, th) != (b, rows, heads):
-            raise ValueError(f"{what} must be shaped as the tensor it belongs to")
-        return t, ts
-
-    _, dos = grad(dout, q, n, h, "dout")
-    _, os_ = grad(out, q, n, h, "out")
-    dq, dqs = grad(dq, q, n, h, "dq")
-    dk, dks = grad(dk, k, nk, hk, "dk")
-    dv, dvs = grad(dv, v, nk, hk, "dv")
-    lp = _plain(lse, dev, torch.float32, b * h * n, "lse")
-    workspace = _workspace(workspace, h3_masked_attention_backward_workspace_bytes(shape), q.device, stream)
-    h3_masked_attention_backward(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, r,
-                                 dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), shape,
-                                 h3_attn_strides(qs, ks, vs, os_, dos, dqs, dks, dvs), _stream(stream))
-    return dq, dk, dv
-
-
-def _dtype_code(dtype, what: str) -> int:
-    import torch
-    code = (_lib.H3_DTYPE_BF16 if dtype is torch.bfloat16 else _lib.H3_DTYPE_F32 if dtype is torch.float32
-            else _lib.H3_DTYPE_F16 if dtype is torch.float16 else None)
-    if code is None:
-        raise ValueError(f"{what} must be bf16, fp16 or fp32")
-    return code
-
-
-def _norm_rows(t, n: int, c: int, dtype, dev: int, what: str) -> int:
-    """Row stride of an [n, c] tensor with unit inner stride."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not dtype or len(shape) != 2 or shape[0] != n or shape[1] != c or (c > 1 and stride[1] != 1) \
-            or (n > 1 and stride[0] < c) or t.get_device() != dev:
-        raise ValueError(f"{what} must be a {dtype} [{n}, {c}] tensor with unit inner stride on the current CUDA device")
-    return stride[0] if n > 1 else max(c, stride[0])
-
-
-def _workspace(workspace, need: int, device, stream):
-    import torch
-    if workspace is None:
-        return _empty(stream, need, dtype=torch.uint8, device=device)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.numel() < need:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes")
-    _on_device(workspace, "workspace")
-    return workspace
+    return (_compiled or _binding()).attention_backward(dout, q, k, v, out, lse, key_ranges, dq, dk, dv, softmax_scale,
+                                                        workspace, stream)
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None, stream=None):
@@ -491,71 +346,25 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None
     x, y: bf16, fp16 or fp32; weight, bias: [C] of x's type or fp32 (both alike), or None; mean, rstd:
     fp32 [N], the input of ``layer_norm_backward``.  Pass out=x for in place.
     """
-    import torch
-    if x.dim() != 2:
-        raise ValueError("x must be [N, C]")
-    dev = torch.cuda.current_device()
-    n, c = x.shape
-    dtype = x.dtype
-    dt = pdt = _dtype_code(dtype, "x")
-    xs = _norm_rows(x, n, c, dtype, dev, "x")
-    wp = bp = 0
-    if weight is not None:
-        pdt = _dtype_code(weight.dtype, "weight")
-        wp = _plain(weight, dev, weight.dtype, c, "weight")
-    if bias is not None:
-        pdt = _dtype_code(bias.dtype, "bias")
-        bp = _plain(bias, dev, bias.dtype if weight is None else weight.dtype, c, "bias")
-    if out is None:
-        out, ys = _empty_like(x, stream), c
-    else:
-        ys = _norm_rows(out, n, c, dtype, dev, "out")
-    if mean is None:
-        mean = _empty(stream, n, dtype=torch.float32, device=x.device)
-    if rstd is None:
-        rstd = _empty(stream, n, dtype=torch.float32, device=x.device)
-    h3_layernorm(x.data_ptr(), out.data_ptr(), wp, bp, _plain(mean, dev, torch.float32, n, "mean"),
-                 _plain(rstd, dev, torch.float32, n, "rstd"), n, c, xs, ys, dt, pdt, eps, _stream(stream))
-    return out, mean, rstd
+    return (_compiled or _binding()).layer_norm(x, weight, bias, eps, out, mean, rstd, stream)
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, param_dtype=None, dx=None, workspace=None,
                         param_grads: bool = True, stream=None):
     """(dx, dweight, dbias) of ``layer_norm``; dweight and dbias are None without ``param_grads``.
 
-    The parameter gradients have the weight's type (``param_dtype``, or fp32, without a weight).
-    Pass dx=dy (or x) for in place.
+    The parameter gradients have the weight's type; without a weight ``param_dtype`` (x's type or
+    fp32, the default).  Pass dx=dy (or x) for in place.
     """
-    import torch
-    if x.dim() != 2:
-        raise ValueError("x must be [N, C]")
-    dev = torch.cuda.current_device()
-    n, c = x.shape
-    dtype = x.dtype
-    dt = _dtype_code(dtype, "x")
-    xs, dys = _norm_rows(x, n, c, dtype, dev, "x"), _norm_rows(dy, n, c, dtype, dev, "dy")
-    mp, rp = _plain(mean, dev, torch.float32, n, "mean"), _plain(rstd, dev, torch.float32, n, "rstd")
-    wp = 0
-    if weight is not None:
-        param_dtype = weight.dtype
-        wp = _plain(weight, dev, param_dtype, c, "weight")
-    elif param_dtype is None:
-        param_dtype = torch.float32
-    pdt = _dtype_code(param_dtype, "weight")
-    if dx is None:
-        dx, dxs = _empty_like(x, stream), c
-    else:
-        dxs = _norm_rows(dx, n, c, dtype, dev, "dx")
-    dw = db = None
-    dwp = dbp = work = 0
-    if param_grads:
-        dw = _empty(stream, c, dtype=param_dtype, device=x.device)
-        db = _empty(stream, c, dtype=param_dtype, device=x.device)
-        workspace = _workspace(workspace, h3_layernorm_backward_workspace_bytes(n, c), x.device, stream)
-        dwp, dbp, work = dw.data_ptr(), db.data_ptr(), workspace.data_ptr()
-    h3_layernorm_backward(dy.data_ptr(), x.data_ptr(), mp, rp, wp, dx.data_ptr(), dwp, dbp, work, n, c, dys, xs, dxs,
-                          dt, pdt, _stream(stream))
-    return dx, dw, db
+    code = _lib.H3_DTYPE_F32
+    if param_dtype is not None and weight is None:
+        import torch
+        codes = {torch.bfloat16: _lib.H3_DTYPE_BF16, torch.float16: _lib.H3_DTYPE_F16, torch.float32: _lib.H3_DTYPE_F32}
+        if param_dtype not in codes:
+            raise ValueError("param_dtype must be bf16, fp16 or fp32")
+        code = codes[param_dtype]
+    return (_compiled or _binding()).layer_norm_backward(dy, x, mean, rstd, weight, code, dx, workspace, param_grads,
+                                                         stream)
 
 
 def adaln_modulate_backward(dy, x, timestep_index, token_tag, table, eps: float = 1e-6, dx=None, dtable=None,
@@ -565,29 +374,5 @@ def adaln_modulate_backward(dy, x, timestep_index, token_tag, table, eps: float 
     Takes what the forward call took, with the same eps; the rows' statistics are
     computed again from x.  Pass dx=dy (or x) for in place.
     """
-    import torch
-    if x.dim() != 2 or table.dim() != 3:
-        raise ValueError("x must be [N, C] and table [E, 2, C]")
-    dev = torch.cuda.current_device()
-    n, c = x.shape
-    e, two, tc = table.shape
-    if two != 2 or tc != c:
-        raise ValueError("table must be [E, 2, C]")
-    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
-    xs, dys = _norm_rows(x, n, c, bf16, dev, "x"), _norm_rows(dy, n, c, bf16, dev, "dy")
-    ts, tags = _plain(timestep_index, dev, i32, n, "timestep_index"), _plain(token_tag, dev, i32, n, "token_tag")
-    tp = _plain(table, dev, f32, 2 * e * c, "table")
-    need = h3_adaln_backward_workspace_bytes(n, c, e)
-    if need == 0:
-        raise ValueError("hidden must be a multiple of 8 up to 8192, with 1 to 8192 table entries")
-    if dx is None:
-        dx, dxs = _empty_like(x, stream), c
-    else:
-        dxs = _norm_rows(dx, n, c, bf16, dev, "dx")
-    if dtable is None:
-        dtable = _empty(stream, (e, 2, c), dtype=f32, device=x.device)
-    workspace = _workspace(workspace, need, x.device, stream)
-    h3_adaln_modulate_backward(dy.data_ptr(), x.data_ptr(), ts, tags, tp, dx.data_ptr(),
-                               _plain(dtable, dev, f32, 2 * e * c, "dtable"), workspace.data_ptr(), e, n, c, dys, xs,
-                               dxs, eps, _stream(stream))
-    return dx, dtable
+    return (_compiled or _binding()).adaln_backward(dy, x, timestep_index, token_tag, table, eps, dx, dtable, workspace,
+                                                    stream)

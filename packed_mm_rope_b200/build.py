@@ -1,10 +1,11 @@
-"""Build libh3.so in-tree for sm_100a with nvcc.
+"""Build libh3.so in-tree for sm_100a with nvcc, and its tensor binding with the host compiler.
 
     python -m packed_mm_rope_b200.build          # or build_library()
 
 The library is one translation unit (csrc/h3.cu includes the kernels), linked
 against the static CUDA runtime; the driver's tensor-map encoder is looked up
-at run time, so no libcuda link is needed.
+at run time, so no libcuda link is needed.  _tensors.so (csrc/binding.cpp) is a
+Python module over the library's C ABI, linked against it and PyTorch.
 """
 from __future__ import annotations
 
@@ -13,12 +14,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libh3.so")
 CSRC = os.path.join(HERE, "csrc")
 HEADER = os.path.join(ROOT, "include", "h3.h")
+BINDING = os.path.join(HERE, "_tensors.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 
 def sources() -> list:
@@ -41,24 +45,48 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def up_to_date(target: str = LIB) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(s) <= t for s in sources() + [__file__])
+    t = os.path.getmtime(target)
+    made_from = sources() if target == LIB else [BINDING_SOURCE, HEADER]
+    return all(os.path.getmtime(s) <= t for s in made_from + [__file__])
+
+
+def _run(cmd: list, target: str, verbose: bool) -> None:
+    r = subprocess.run(cmd + ["-o", target + ".tmp"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n" + r.stdout + r.stderr)
+    os.replace(target + ".tmp", target)
+    if verbose:
+        sys.stdout.write(r.stderr)
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    if not force and up_to_date(BINDING):
+        return BINDING
+    import torch
+    from torch.utils import cpp_extension
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("no C++ compiler found")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [sysconfig.get_path("include"), *cpp_extension.include_paths(), os.path.join(cuda, "include")]
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for path in include:
+        cmd += ["-isystem", path]
+    cmd += [BINDING_SOURCE, "-L", HERE, "-lh3", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
+            "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    _run(cmd, BINDING, verbose)
+    return BINDING
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"),
-           os.path.join(CSRC, "h3.cu"), "-o", LIB + ".tmp"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
-    os.replace(LIB + ".tmp", LIB)
-    if verbose:
-        sys.stdout.write(r.stderr)
+    if force or not up_to_date():
+        _run([nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), os.path.join(CSRC, "h3.cu")], LIB, verbose)
+    build_binding(force, verbose)
     return LIB
 
 
