@@ -166,13 +166,14 @@ struct GroupedRope {
 // As rope_kernel, over the heads of Q followed by those of K: the items of a
 // row are those of both tensors in a row, so a lane still meets the same pairs
 // in every item.  The rotation back (the gradient) is the same kernel with a
-// table of negated frequencies.
-template <int LAYOUT>
-__global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS_PER_SM) rope_grouped_kernel(
+// table of negated frequencies.  B items per lane are in flight: 14 (8 chunk pairs)
+// for wide rows; 4 (2) and twice the blocks per SM for rows of few heads, whose time
+// is the latency of the trigonometry.
+template <int LAYOUT, int B, int CTAS_PER_SM>
+__global__ void __launch_bounds__(ROPE_THREADS, CTAS_PER_SM) rope_grouped_kernel(
     const GroupedRope p, const float* __restrict__ coords, long long n_rows, const RopeTable tab) {
   constexpr int IPH = LAYOUT == 0 ? 16 : 8;        // work items per head
   constexpr int PPI = LAYOUT == 0 ? 4 : 8;         // rotary pairs per item
-  constexpr int B = LAYOUT == 0 ? 14 : 8;          // items per lane in flight
   const int lane = threadIdx.x & 31;
   const int sub = lane % IPH;                      // item index within the head
   const long long gw = (static_cast<long long>(blockIdx.x) * ROPE_THREADS + threadIdx.x) >> 5;
@@ -186,7 +187,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS_PER_SM) rope_grouped_k
     uint4* const kd = p.dst[1] + r * p.dst_stride[1] + sub;
     float2 cs[PPI];
     bool first = true;
-    for (int i0 = lane; i0 < items; i0 += 32 * B) {
+    for (int base = 0; base < items; base += 32 * B) {   // the same steps for all lanes
+      const int i0 = base + lane;
       uint4 a[B], b[B];
 #pragma unroll
       for (int u = 0; u < B; ++u) {
@@ -198,9 +200,17 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS_PER_SM) rope_grouped_k
         }
       }
       if (first) {
+        // 32 / IPH lanes meet the same PPI pairs: each computes two of them
         const float* crd = coords + 3 * r;
+        float2 own[2];
 #pragma unroll
-        for (int m = 0; m < PPI; ++m) cs[m] = rope_cos_sin(tab, crd, PPI * sub + m);
+        for (int m = 0; m < 2; ++m) own[m] = rope_cos_sin(tab, crd, PPI * sub + 2 * (lane / IPH) + m);
+#pragma unroll
+        for (int m = 0; m < PPI; ++m) {
+          const int from = sub + IPH * (m / 2);
+          cs[m].x = __shfl_sync(0xffffffffu, own[m & 1].x, from);
+          cs[m].y = __shfl_sync(0xffffffffu, own[m & 1].y, from);
+        }
         first = false;
       }
 #pragma unroll

@@ -444,13 +444,16 @@ h3_status h3_mmrope_rotate(const void* d_q, const void* d_k, void* d_q_out, void
   p.heads[1] = n_kv_heads;
   const long long warps_per_cta = h3::ROPE_THREADS / 32;
   const long long nblk = (n_rows + warps_per_cta - 1) / warps_per_cta;
-  const long long cap = 2LL * h3::ROPE_CTAS_PER_SM * sm_count();
-  const int grid = static_cast<int>(nblk < cap ? nblk : cap);
-  if (cfg->pair_layout == 0)
-    h3::rope_grouped_kernel<0><<<grid, h3::ROPE_THREADS, 0, as_stream(stream)>>>(p, d_coords, n_rows, tab);
-  else
-    h3::rope_grouped_kernel<1><<<grid, h3::ROPE_THREADS, 0, as_stream(stream)>>>(p, d_coords, n_rows, tab);
-  return launched();
+  auto go = [&](auto kernel, int ctas) {
+    const long long grid = std::min<long long>(nblk, 2LL * ctas * sm_count());
+    kernel<<<static_cast<unsigned>(grid), h3::ROPE_THREADS, 0, as_stream(stream)>>>(p, d_coords, n_rows, tab);
+    return launched();
+  };
+  // up to 16 heads a lane has at most 8 chunks of a row
+  if (n_heads + n_kv_heads <= 16)
+    return cfg->pair_layout == 0 ? go(h3::rope_grouped_kernel<0, 4, 4>, 4) : go(h3::rope_grouped_kernel<1, 2, 4>, 4);
+  return cfg->pair_layout == 0 ? go(h3::rope_grouped_kernel<0, 14, h3::ROPE_CTAS_PER_SM>, h3::ROPE_CTAS_PER_SM)
+                               : go(h3::rope_grouped_kernel<1, 8, h3::ROPE_CTAS_PER_SM>, h3::ROPE_CTAS_PER_SM);
 }
 
 h3_status h3_layernorm(const void* d_x, void* d_y, const void* d_weight, const void* d_bias, float* d_mean,
