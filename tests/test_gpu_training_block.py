@@ -1,0 +1,152 @@
+"""The training-direction calls together, as a block uses them: modulate, project, rotate, attend, normalise, and back."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests.test_gpu_masked_attention import starts_of
+from tests.train_util import randn
+
+pytestmark = pytest.mark.gpu
+
+N, C, H, KV = 330, 256, 4, 2
+DOCS, PREFIX = [150, 0, 120, 31], [20, 0, 7, 31]
+
+
+@pytest.fixture(scope="module")
+def h3():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import packed_mm_rope_b200 as lib
+    return lib
+
+
+def _inputs():
+    width = (H + 2 * KV) * 128
+    t = {"x": randn(1, N, C), "wqkv": randn(2, width, C, scale=C ** -0.5), "wo": randn(3, C, H * 128, scale=0.05),
+         "table": randn(4, 6, 2, C, dtype=torch.float32, scale=0.2), "gain": randn(5, C, dtype=torch.float32, shift=1.0, scale=0.1),
+         "bias": randn(6, C, dtype=torch.float32, scale=0.1)}
+    r = torch.arange(N, device="cuda")
+    t["coords"] = torch.stack([r * (20 / 3), r % 7, r % 11], 1).float().contiguous()
+    t["level"], t["tags"] = (r % 2).int(), (r % 3).int()
+    t["dy"] = randn(7, N, C)
+    t["starts"], t["prefix"] = starts_of(DOCS), torch.tensor(PREFIX, dtype=torch.int32, device="cuda")
+    return t
+
+
+def _ranges(h3, t):
+    return h3.build_key_ranges(t["starts"], N, "prefix_causal", prefix=t["prefix"])
+
+
+def _step(h3, t):
+    """Forward and backward by the library's calls (the projections by torch in bf16)."""
+    h = h3.adaln_modulate(t["x"], t["level"], t["tags"], t["table"])
+    qkv = (h @ t["wqkv"].T).view(N, H + 2 * KV, 128)
+    q, k, v = qkv[:, :H], qkv[:, H:H + KV], qkv[:, H + KV:]
+    qr, kr = h3.mmrope_rotate(q, k, t["coords"])
+    ranges = _ranges(h3, t)
+    lse = torch.empty(H, N, device="cuda")
+    o = h3.masked_attention(qr, kr, v, ranges, lse=lse)
+    z = o.view(N, H * 128) @ t["wo"].T
+    y, mean, rstd = h3.layer_norm(z, t["gain"], t["bias"])
+
+    dz, dgain, dbias = h3.layer_norm_backward(t["dy"], z, mean, rstd, t["gain"])
+    dwo = dz.T @ o.view(N, H * 128)
+    do = (dz @ t["wo"]).view(N, H, 128)
+    dqkv = torch.empty_like(qkv)
+    dq, dk, _ = h3.masked_attention_backward(do, qr, kr, v, o, lse, ranges, dv=dqkv[:, H + KV:])
+    h3.mmrope_rotate(dq, dk, t["coords"], q_out=dqkv[:, :H], k_out=dqkv[:, H:H + KV], inverse=True)
+    dwqkv = dqkv.view(N, -1).T @ h
+    dh = dqkv.view(N, -1) @ t["wqkv"]
+    dx, dtable = h3.adaln_modulate_backward(dh, t["x"], t["level"], t["tags"], t["table"])
+    return {"y": y, "dx": dx, "dwqkv": dwqkv, "dwo": dwo, "dgain": dgain, "dbias": dbias, "dtable": dtable}
+
+
+def _reference(t, ranges):
+    """The same block in 64 bits, gradients by automatic differentiation."""
+    f = {k: (v.double().requires_grad_() if k in ("x", "wqkv", "wo", "table", "gain", "bias") else v)
+         for k, v in t.items()}
+
+    def norm(x, eps):
+        m = x.mean(-1, keepdim=True)
+        return (x - m) / torch.sqrt(((x - m) ** 2).mean(-1, keepdim=True) + eps)
+
+    e = t["level"].long() * 3 + t["tags"].long()
+    h = norm(f["x"], 1e-6) * (1 + f["table"][e, 1]) + f["table"][e, 0]
+    qkv = (h @ f["wqkv"].T).view(N, H + 2 * KV, 128)
+    parts = [t["coords"].double()[:, a:a + 1] * 10000.0 ** (-torch.arange(0, d, 2, device="cuda").double() / d)
+             for a, d in enumerate((32, 48, 48))]
+    turn = torch.polar(torch.ones(N, 64, dtype=torch.float64, device="cuda"), torch.cat(parts, 1))[:, None]
+
+    def rotate(x):
+        return torch.view_as_real(torch.view_as_complex(x.unflatten(-1, (64, 2)).contiguous()) * turn).flatten(-2)
+
+    q, k = rotate(qkv[:, :H]), rotate(qkv[:, H:H + KV]).repeat_interleave(H // KV, 1)
+    v = qkv[:, H + KV:].repeat_interleave(H // KV, 1)
+    key = torch.arange(N, device="cuda")
+    sees = (key[None] >= ranges[:, :1]) & (key[None] < ranges[:, 1:])
+    s = torch.einsum("qhd,khd->hqk", q, k) * 128 ** -0.5
+    p = torch.softmax(s.masked_fill(~sees, -1e300), -1) * sees
+    o = torch.einsum("hqk,khd->qhd", p, v).reshape(N, H * 128)
+    y = norm(o @ f["wo"].T, 1e-5) * f["gain"] + f["bias"]
+    y.backward(t["dy"].double())
+    return {"y": y.detach(), "dx": f["x"].grad, "dwqkv": f["wqkv"].grad, "dwo": f["wo"].grad, "dgain": f["gain"].grad,
+            "dbias": f["bias"].grad, "dtable": f["table"].grad}
+
+
+def test_block_against_64_bits(h3):
+    """Every tensor passed on is rounded to bf16 (2^-8 relative at most, in the 2-norm about 2^-9.8): forward six
+    of them in a row (h, qkv, rotation, P with O, z, y), backward seven more (dz, do, dS with dq, rotation, dh,
+    dx, and the rounded operands of the forward pass again).  In the 2-norm independent roundings add up like
+    sqrt(13) 2^-9.8 = 0.4 %; rows of y with no key (the padding and z = 0) have the norm of a zero row amplified by
+    1 / sqrt(eps) = 316 at most, and it is exactly 0 here.  The layer norm divides by the deviation of z, whose
+    relative error it keeps.  2 % leaves a factor five for correlated roundings."""
+    t = _inputs()
+    got = _step(h3, t)
+    assert h3.h3_check_device_error() == h3.H3_OK
+    want = _reference(t, _ranges(h3, t))
+    for name, w in want.items():
+        rel = float((got[name].double() - w).norm() / w.norm())
+        assert rel <= 0.02, (name, rel)
+
+
+def test_block_repeats_and_replays(h3):
+    """The same bits on every run, and from a captured graph whose inputs have changed."""
+    t = _inputs()
+    first = _step(h3, t)
+    again = _step(h3, t)
+    assert all(torch.equal(first[k], again[k]) for k in first)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _step(h3, t)                                  # library handles of torch's products
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for _ in range(2):                                # two graphs with workspaces of their own
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(_step(h3, t))
+        graphs.append(g)
+    t["x"].copy_(randn(21, N, C))
+    for g in graphs:
+        g.replay()
+    want = _step(h3, t)
+    for out in outs:
+        assert all(torch.equal(want[k], out[k]) for k in want)
+
+
+def test_prefix_rows_can_be_reused(h3):
+    """Under the block-prefix mask the prefix rows' outputs do not depend on the rest, and fresh query rows against
+    all keys give the rows of the whole call: K and V of a prefix are computed once."""
+    n, p = 500, 180
+    q, k, v = randn(1, n, H, 128), randn(2, n, KV, 128), randn(3, n, KV, 128)
+    s, pre = starts_of([n]), torch.tensor([p], dtype=torch.int32, device="cuda")
+    ranges = h3.build_key_ranges(s, n, "prefix_block", prefix=pre)
+    whole = h3.masked_attention(q, k, v, ranges)
+    fresh = h3.masked_attention(q[p:], k, v, ranges[p:].contiguous())
+    alone = h3.masked_attention(q[:p], k[:p], v[:p], ranges[:p].contiguous())
+    bound = 2 * 2.0 ** -8 * v.double().abs().amax()   # two roundings of the same value each
+    assert float((whole[p:].double() - fresh.double()).abs().max()) <= bound
+    assert float((whole[:p].double() - alone.double()).abs().max()) <= bound
+    k2, v2 = k.clone(), v.clone()
+    k2[p:], v2[p:] = randn(8, n - p, KV, 128), randn(9, n - p, KV, 128)
+    assert torch.equal(h3.masked_attention(q, k2, v2, ranges)[:p], whole[:p])
