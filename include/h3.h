@@ -398,6 +398,8 @@ typedef struct {
  *   d_work             h3_masked_attention_backward_workspace_bytes() bytes,
  *                      256-byte aligned, contents undefined before and after; calls
  *                      that may overlap in time need their own
+ * D_i of a row with at most 32 keys is formed as sum_j P_ij dO_i.V_j: it does not
+ * take the rounding of O into such rows' gradients.
  * Every row of the outputs is written: queries with an empty interval and keys
  * that no row sees get 0.  What lies outside a row's interval changes no gradient
  * through it, inf and NaN included.

@@ -6,18 +6,19 @@
 //   dQ_i = scale sum_j dS_ij k_j   dK_j  = scale sum_i dS_ij q_i
 // and the query heads that share a K/V head add up in its dK and dV.
 //
-// `prep` forms D (one pass over O and dO) and lays the rows' (lse, D), intervals
-// and their hulls per 128-row tile out in the workspace, padded to whole tiles.  The
-// main kernel then runs two kinds of blocks: `dkdv` owns 128 keys of a K/V head and
-// walks the query tiles that see them, over all heads of the group; `dq` owns 128
-// query rows of a head and walks their key tiles.  Both recompute S and dP, 7
-// products of 128 x 128 x 128 per pair of tiles where one walk would need 5: the
-// price of sums that stay in tensor memory, need no atomics and come out the same on
-// every run.  The kinds share a launch so that the shorter dq blocks fill the SMs
-// that the dkdv blocks leave (1,127 rows x 8 heads: 72 blocks of each kind side by
-// side).  Where there are few key tiles, a tile's walk is cut into `parts`, whose
-// fp32 sums go to the workspace and are added in order by a third kernel
-// (9,001 + 5,097 rows, 14 heads over 2 K/V heads: 222 walks of up to 777 steps).
+// `prep` forms D (one pass over O and dO; for rows of few keys anew from P and dP,
+// since there the rounding of O to bf16 weighs as much as that of dS) and lays the
+// rows' (lse, D), intervals and their hulls per 128-row tile out in the workspace,
+// padded to whole tiles.  The main kernel then runs two kinds of blocks: `dkdv` owns
+// 128 keys of a K/V head and walks the query tiles that see them, over all heads of
+// the group; `dq` owns 128 query rows of a head and walks their key tiles.  Both
+// recompute S and dP, 7 products of 128 x 128 x 128 per pair of tiles where one walk
+// would need 5: the price of sums that stay in tensor memory, need no atomics and
+// come out the same on every run.  The kinds share a launch so that the shorter dq
+// blocks fill the SMs that the dkdv blocks leave (1,127 rows x 8 heads: 72 blocks of
+// each kind side by side).  Where there are few key tiles, a tile's walk is cut into
+// `parts`, whose fp32 sums go to the workspace and are added in order by a third
+// kernel (9,001 + 5,097 rows, 14 heads over 2 K/V heads: 222 walks of up to 777 steps).
 //
 // dkdv works on S^T = K Q^T and dP^T = V dO^T (keys on the 128 TMEM lanes), so
 // that P^T and dS^T are, rounded to bf16 in place, the A operands of
@@ -85,21 +86,127 @@ struct Params {
 
 // ------------------------------------------------------------------ prep ----
 
+// D (16 x 8) += A (16 x 16) B (16 x 8): one warp, bf16 operands, fp32 sums.
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint4 a, const uint2 b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y));
+}
+
+// D of rows with at most this many keys comes from P and dP.  Against 64 bits that
+// takes the error of dQ and dK, which the roundings of dS and of the outputs alone
+// make 1.41 times that of the outputs' rounding, from 1.45 - 1.6 down to 1.44 of it at
+// most (documents of 20 to 2,000 rows, causal and full).
+constexpr int SHORT_ROW = 32;
+
+struct PrepInputs {
+  const __nv_bfloat16 *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  int group;
+  float scale_log2;
+};
+
+struct ShortRows {
+  int2 range[BM];            // {0, 0} for the others
+  float lse_log2[BM];
+  float part[BM][8];         // [row][warp]
+};
+
+// The block: D_i = sum_j P_ij (dO_i . v_j) of the tile's short rows, into sm.part.
+// 16 rows against 8 keys at a time on a warp's matrix unit, the steps dealt to the
+// warps in turn (of a causal mask only 32 rows are short: 8 steps of the whole tile).
+// Lane t of four holds elements 8 t .. 8 t + 7 of 32, one 16-byte load, for both
+// operands: the order of a product's terms is free.
+__device__ __forceinline__ void short_rows(ShortRows& sm, const PrepInputs& in, const __nv_bfloat16* dout,
+                                           long long do_stride, int n_q, int n_k, int batch, int head, int tile) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int kv_col = head / in.group * HD + 8 * t;
+  int step = 0;
+  for (int row0 = 0; row0 < BM; row0 += 16) {
+    const int2 r[2] = {sm.range[row0 + g], sm.range[row0 + g + 8]};
+    auto next_key = [&](int from) {                // the first key from `from` on that a short row sees
+      int k = 0x7fffffff;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (r[h].y > from) k = min(k, max(r[h].x, from));
+      return __reduce_min_sync(0xffffffffu, k);
+    };
+    float d[2] = {0.f, 0.f};
+    for (int key0 = next_key(0); key0 != 0x7fffffff; key0 = next_key(key0 + 8)) {
+      if ((step++ & 7) != warp) continue;
+      const long long kv = static_cast<long long>(batch) * n_k + min(key0 + g, n_k - 1);
+      const __nv_bfloat16 *kr = in.k + kv * in.k_stride + kv_col, *vr = in.v + kv * in.v_stride + kv_col;
+      const long long q0 = static_cast<long long>(batch) * n_q + min(tile * BM + row0 + g, n_q - 1);
+      const long long q1 = static_cast<long long>(batch) * n_q + min(tile * BM + row0 + g + 8, n_q - 1);
+      const int col = head * HD + 8 * t;
+      const __nv_bfloat16 *qa = in.q + q0 * in.q_stride + col, *qb = in.q + q1 * in.q_stride + col;
+      const __nv_bfloat16 *da = dout + q0 * do_stride + col, *db = dout + q1 * do_stride + col;
+      auto load = [](const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); };
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, dp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int c = 0; c < HD; c += 64) {
+        uint4 w[2][6];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          w[u][0] = load(qa + c + 32 * u);
+          w[u][1] = load(qb + c + 32 * u);
+          w[u][2] = load(kr + c + 32 * u);
+          w[u][3] = load(da + c + 32 * u);
+          w[u][4] = load(db + c + 32 * u);
+          w[u][5] = load(vr + c + 32 * u);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint4(&x)[6] = w[u];
+          mma_16x8x16(s, {x[0].x, x[1].x, x[0].y, x[1].y}, {x[2].x, x[2].y});
+          mma_16x8x16(dp, {x[3].x, x[4].x, x[3].y, x[4].y}, {x[5].x, x[5].y});
+          mma_16x8x16(s, {x[0].z, x[1].z, x[0].w, x[1].w}, {x[2].z, x[2].w});
+          mma_16x8x16(dp, {x[3].z, x[4].z, x[3].w, x[4].w}, {x[5].z, x[5].w});
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {                // row g + 8 (e / 2), key 2 t + e % 2
+        const int h = e >> 1, key = key0 + 2 * t + (e & 1);
+        if (key >= r[h].x && key < r[h].y)
+          d[h] = fmaf(ex2_approx(fmaf(s[e], in.scale_log2, -sm.lse_log2[row0 + g + 8 * h])), dp[e], d[h]);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      d[h] += __shfl_xor_sync(0xffffffffu, d[h], 1);
+      d[h] += __shfl_xor_sync(0xffffffffu, d[h], 2);
+      if (t == 0) sm.part[row0 + g + 8 * h][warp] = d[h];
+    }
+  }
+}
+
 // One block per (query tile, head, batch): 16 lanes per row, 16 rows at a time, four
 // such steps' loads in flight.  Blocks of head 0 also write the tile's intervals and
-// hull.  Bound by the reads of O and dO.
-__global__ void __launch_bounds__(256) prep_kernel(const __nv_bfloat16* __restrict__ o,
-                                                   const __nv_bfloat16* __restrict__ dout,
-                                                   const float* __restrict__ lse, const int2* __restrict__ ranges,
-                                                   int n_q, int n_k, int n_heads, int n_qt, long long o_stride,
-                                                   long long do_stride, float2* __restrict__ stat,
-                                                   int2* __restrict__ rng, int4* __restrict__ hull) {
+// hull.  Bound by the reads of O and dO (14,098 rows x 14 heads 18.0 us, 0.87 of the
+// copy rate); with few blocks by the two round trips to memory, and a third and a
+// fourth where there are short rows (1,127 rows x 8 heads 4.1, with them 6.9 us).
+__global__ void __launch_bounds__(256, 3) prep_kernel(const __grid_constant__ PrepInputs in,
+                                                      const __nv_bfloat16* __restrict__ o,
+                                                      const __nv_bfloat16* __restrict__ dout,
+                                                      const float* __restrict__ lse, const int2* __restrict__ ranges,
+                                                      int n_q, int n_k, int n_heads, int n_qt, long long o_stride,
+                                                      long long do_stride, float2* __restrict__ stat,
+                                                      int2* __restrict__ rng, int4* __restrict__ hull) {
   const int tile = blockIdx.x, head = blockIdx.y, batch = blockIdx.z;
   const int sub = threadIdx.x & 15, first = tile * BM + (threadIdx.x >> 4);
   const long long bh = static_cast<long long>(batch) * n_heads + head;
   const long long row0 = static_cast<long long>(batch) * n_q;
+  __shared__ ShortRows few;
   int2 range = make_int2(0, 0);
-  if (head == 0 && threadIdx.x < BM && tile * BM + threadIdx.x < n_q) range = ranges[row0 + tile * BM + threadIdx.x];
+  bool is_short = false;
+  if (threadIdx.x < BM && tile * BM + threadIdx.x < n_q) {
+    range = attn::clamp_range(ranges[row0 + tile * BM + threadIdx.x], n_k);
+    is_short = range.x < range.y && range.y - range.x <= SHORT_ROW;
+    few.lse_log2[threadIdx.x] = lse[bh * n_q + tile * BM + threadIdx.x] * 1.4426950408889634f;
+  }
+  if (threadIdx.x < BM) few.range[threadIdx.x] = is_short ? range : make_int2(0, 0);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint4 a[4], b[4];
@@ -128,10 +235,20 @@ __global__ void __launch_bounds__(256) prep_kernel(const __nv_bfloat16* __restri
         stat[bh * n_qt * BM + row] = row < n_q ? make_float2(l[i] * 1.4426950408889634f, d) : make_float2(0.f, 0.f);
     }
   }
+  if (__syncthreads_or(is_short)) {                // over what was written above
+    short_rows(few, in, dout, do_stride, n_q, n_k, batch, head, tile);
+    __syncthreads();
+    if (is_short) {
+      float d = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) d += few.part[threadIdx.x][w];
+      stat[bh * n_qt * BM + tile * BM + threadIdx.x].y = d;
+    }
+  }
   if (head == 0) {
     __shared__ int part[4][4];
     if (threadIdx.x < BM) {
-      const int2 r = attn::clamp_range(range, n_k);
+      const int2 r = range;
       rng[(static_cast<long long>(batch) * n_qt + tile) * BM + threadIdx.x] = make_int2(r.x, r.y - r.x);
       const bool some = r.x < r.y;
       const int lo = __reduce_min_sync(0xffffffffu, some ? r.x : 0x7fffffff);

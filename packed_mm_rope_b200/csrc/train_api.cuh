@@ -400,8 +400,16 @@ h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const 
   p.drain_limit_ns = kDrainLimitNs;
   p.err_slot = error_slot(stream);
   const unsigned batch = static_cast<unsigned>(a->batch), heads = static_cast<unsigned>(a->n_heads);
+  const h3::attn_bwd::PrepInputs in{static_cast<const __nv_bfloat16*>(d_q),
+                                    static_cast<const __nv_bfloat16*>(d_k),
+                                    static_cast<const __nv_bfloat16*>(d_v),
+                                    st->q,
+                                    st->k,
+                                    st->v,
+                                    p.group,
+                                    p.scale_log2};
   h3::attn_bwd::prep_kernel<<<dim3(w.n_qt, heads, batch), 256, 0, s>>>(
-      static_cast<const __nv_bfloat16*>(d_o), static_cast<const __nv_bfloat16*>(d_do), d_lse,
+      in, static_cast<const __nv_bfloat16*>(d_o), static_cast<const __nv_bfloat16*>(d_do), d_lse,
       reinterpret_cast<const int2*>(d_ranges), p.n_q, p.n_k, p.n_heads, w.n_qt, st->o, st->dout, stat, rng, hull);
   const uint64_t blocks = static_cast<uint64_t>(w.n_kt) * w.parts * a->n_kv_heads * a->batch +
                           static_cast<uint64_t>(w.n_qt) * heads * batch;

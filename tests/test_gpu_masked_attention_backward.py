@@ -45,6 +45,21 @@ def test_any_intervals(h3, nq, nk):
     check_attention(_grads(h3, do, q, k, v, ranges), attend(q, k, v, ranges, do=do), NAMES)
 
 
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("h,kv,heads_like", [(2, 2, False), (6, 2, True)])
+def test_rows_of_few_keys(h3, mode, h, kv, heads_like):
+    """Documents around 32 rows, where O's rounding does not enter the gradients; values with a common part
+    (a mean of 3), which makes dO.O large beside dP - D."""
+    docs = [1, 20, 32, 33, 2, 31, 64, 7, 16, 100, 3]
+    n = sum(docs) + 5
+    q, k, v, do = randn(1, n, h, 128), randn(2, n, kv, 128), randn(3, n, kv, 128), randn(4, n, h, 128)
+    v, do = (v.float() + 3).to(v.dtype), (do.float() + 3).to(do.dtype)
+    if heads_like:                                     # views of one buffer, rows further apart
+        q, k, v = torch.cat([q, k, v], 1).split([h, kv, kv], 1)
+    ranges = python_ranges(docs, [min(5, d) for d in docs], n, mode, 2)
+    check_attention(_grads(h3, do, q, k, v, ranges), attend(q, k, v, ranges, do=do), NAMES)
+
+
 @pytest.mark.parametrize("scale", [0.02, 0.5])
 def test_scales(h3, scale):
     n = 700

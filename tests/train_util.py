@@ -117,8 +117,11 @@ def attend(q, k, v, ranges, scale=None, do=None, chunk_heads=8):
         dp = dd @ vv.T
         edp = 300 * U * (dd.abs() @ vv.abs().T)
         delta = (dd * o).sum(1, keepdim=True)
-        # delta comes from the rounded O: its error enters every dS of the row
+        # delta comes from the rounded O, whose error enters every dS of the row; for rows of at most 32 keys
+        # from P and dP in fp32 (an approximate exp2, sums of 32 terms)
         edelta = (dd.abs() * (eo + h16 * o.abs())).sum(1, keepdim=True) + 40 * U * (dd * o).abs().sum(1, keepdim=True)
+        few = (p * (edp + (2 * es + 2.0 ** -20) * dp.abs())).sum(1, keepdim=True)
+        edelta = torch.where(sees.sum(1, keepdim=True) <= 32, few, edelta)
         ds = p * (dp - delta)
         eds = p * (edp + edelta + (2 * es + 4 * U) * (dp - delta).abs()) + (h16 + acc) * ds.abs()
         dq, edq = ds @ kk * scale, eds @ kk.abs() * scale
