@@ -301,14 +301,15 @@ enum { H3_DTYPE_BF16 = 0, H3_DTYPE_F16 = 1, H3_DTYPE_F32 = 2 };
  * head counts and row strides (grouped heads), and its gradient.
  *
  *   d_q, d_q_out       device bf16 [n_rows][n_heads][128], strides q_stride,
- *                      q_out_stride (elements); d_q_out may be d_q
+ *                      q_out_stride (elements); d_q_out may be d_q with its stride
  *   d_k, d_k_out       device bf16 [n_rows][n_kv_heads][128], k_stride, k_out_stride
  *                      either tensor may be absent (NULL, 0 heads)
  *   inverse            0: rotate by the rows' angles a (as h3_mmrope_qk, same
  *                      values); 1: rotate by -a.  A rotation's transpose is its
  *                      inverse, so this maps the gradients of the rotated Q and
  *                      K to those of the unrotated ones.
- * Arithmetic, other arguments and errors as h3_mmrope_qk.
+ * Arithmetic, other arguments and errors as h3_mmrope_qk; H3_ERR_INVALID_ARG for
+ * an output that shares memory with anything but its own input, exactly.
  */
 h3_status h3_mmrope_rotate(const void* d_q, const void* d_k, void* d_q_out, void* d_k_out, const float* d_coords,
                            int64_t n_rows, int32_t n_heads, int32_t n_kv_heads, int64_t q_stride, int64_t k_stride,
@@ -372,7 +373,8 @@ typedef struct {
  * a key whose V holds inf or NaN becomes non-finite (at least in the columns
  * concerned, in a tile at an interval's edge in all of them).
  * Arithmetic and bounded waits as h3_packed_attention.
- * Errors: H3_ERR_INVALID_ARG (sizes, heads, strides, NULL pointers);
+ * Errors: H3_ERR_INVALID_ARG (sizes, heads, strides, NULL pointers, d_o sharing
+ * memory with an input; columns of one buffer with one row stride share none);
  * H3_ERR_UNSUPPORTED (head_dim != 128, misaligned pointer or stride).
  */
 h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v, void* d_o, float* d_lse,
@@ -406,7 +408,8 @@ typedef struct {
  * Arithmetic: bf16 tensor-core products with fp32 accumulation, P and dS rounded
  * to bf16 as operands, P and dS themselves fp32, outputs rounded to bf16; the
  * same values on every run.  Bounded waits as h3_packed_attention.
- * Errors: as h3_masked_attention; H3_ERR_INVALID_ARG for a missing workspace.
+ * Errors: as h3_masked_attention; H3_ERR_INVALID_ARG for a missing workspace or a
+ * gradient that shares memory with an input or another gradient.
  */
 uint64_t h3_masked_attention_backward_workspace_bytes(const h3_attn_shape* shape);
 h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const void* d_k, const void* d_v,
@@ -421,13 +424,15 @@ h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const 
  *   d_x, d_y           device [n_rows][hidden] of `dtype`, row strides in elements;
  *                      any hidden from 1 to 16384, stride and alignment (rows that
  *                      are 16-byte aligned and a multiple of 8 long go in 16-byte
- *                      pieces); d_y may be d_x
+ *                      pieces); d_y may be d_x with its stride
  *   d_weight, d_bias   device [hidden] of `param_dtype` (dtype or H3_DTYPE_F32);
  *                      NULL = ones, zeros
  *   d_mean, d_rstd     device float[n_rows], the rows' statistics for
  *                      h3_layernorm_backward, or NULL
- * Arithmetic: fp32, y rounded once.
- * Errors: H3_ERR_INVALID_ARG (sizes, strides, dtypes, NULL d_x or d_y, eps < 0);
+ * Arithmetic: fp32, y rounded once.  Rows of more than 1,024 elements in 16-byte
+ * pieces are brought in by copies with bounded waits (h3_set_wait_limit_ns).
+ * Errors: H3_ERR_INVALID_ARG (sizes, strides, dtypes, NULL d_x or d_y, eps < 0, d_y
+ * sharing memory with d_x otherwise than in place);
  * H3_ERR_UNSUPPORTED (hidden > 16384, another param_dtype).
  */
 h3_status h3_layernorm(const void* d_x, void* d_y, const void* d_weight, const void* d_bias, float* d_mean,
@@ -449,7 +454,8 @@ h3_status h3_layernorm(const void* d_x, void* d_y, const void* d_weight, const v
  *                      aligned, contents undefined before and after; calls that may
  *                      overlap in time need their own (NULL when neither parameter
  *                      gradient is wanted)
- * Column sums are fp32, added in an order that depends on the sizes alone.
+ * Column sums are fp32, added in an order that depends on sizes and alignment
+ * alone.  Bounded waits as h3_layernorm.
  * Errors: as h3_layernorm; H3_ERR_INVALID_ARG for a missing workspace.
  */
 uint64_t h3_layernorm_backward_workspace_bytes(int64_t n_rows, int32_t hidden);
@@ -476,9 +482,9 @@ h3_status h3_layernorm_backward(const void* d_dy, const void* d_x, const float* 
  *                      are computed again from x
  * A row whose e falls outside [0, n_entries) gets a dx of NaN, adds to no entry and
  * raises H3_ERR_DEVICE_INPUT.  Sums are fp32, in an order that depends on the sizes
- * and indices alone.
- * Errors: as h3_adaln_modulate; H3_ERR_INVALID_ARG for a missing workspace or
- * n_rows >= 2^31; H3_ERR_UNSUPPORTED for n_entries > 8192.
+ * and indices alone.  Bounded waits as h3_layernorm.
+ * Errors: as h3_adaln_modulate; H3_ERR_INVALID_ARG for a missing workspace, a d_dx
+ * sharing memory with d_dy or d_x otherwise than in place, or n_rows >= 2^31; H3_ERR_UNSUPPORTED for n_entries > 8192.
  */
 uint64_t h3_adaln_backward_workspace_bytes(int64_t n_rows, int32_t hidden, int32_t n_entries);
 h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const int32_t* d_timestep_index,
@@ -590,8 +596,8 @@ h3_status h3_check_device_error(void* stream);
 
 /*
  * Limit, in nanoseconds of device global time, of every bounded wait inside
- * the attention kernel (process-wide; default 2e9 = 2 s).  0 restores the
- * default.  Used by tests to force the timeout path.
+ * the attention, layer norm and AdaLN gradient kernels (process-wide; default
+ * 2e9 = 2 s).  0 restores the default.  Used by tests to force the timeout path.
  */
 h3_status h3_set_wait_limit_ns(uint64_t ns);
 

@@ -78,7 +78,11 @@ class Call {
     if (v == -1.0 && PyErr_Occurred()) throw_pending();
     return v;
   }
-  bool flag(int i) const { return PyObject_IsTrue(args_[i]) == 1; }
+  bool flag(int i) const {
+    const int v = PyObject_IsTrue(args_[i]);
+    if (v < 0) throw_pending();
+    return v == 1;
+  }
 
   int device() const { return dev_; }
   void* stream() const { return stream_; }
@@ -136,10 +140,11 @@ Heads heads_of(const Call& c, const at::Tensor& t, const char* what) {
   const auto size = t.sizes();
   const auto stride = t.strides();
   Heads h{d == 4 ? size[0] : 1, size[d - 3], size[d - 2], stride[d - 3], static_cast<char*>(t.data_ptr())};
-  if (size[d - 1] != 128 || stride[d - 1] != 1 || stride[d - 2] != 128)
+  if (size[d - 1] != 128 || stride[d - 1] != 1 || (h.heads > 1 && stride[d - 2] != 128))
     refuse(std::string(what) + " must be [N, H, 128] or [B, N, H, 128] with heads contiguous");
-  if (h.rows <= 1 && h.batch <= 1) h.stride = std::max(h.stride, 128 * h.heads);
-  if (d == 4 && h.batch > 1 && stride[0] != h.rows * h.stride)
+  if (h.rows * h.batch <= 1) h.stride = 128 * h.heads;         // no second row
+  else if (h.rows == 1) h.stride = stride[0];
+  if (h.rows > 1 && h.batch > 1 && stride[0] != h.rows * h.stride)
     refuse(std::string(what) + ": the batch stride must be n_rows * row_stride");
   return h;
 }
@@ -161,7 +166,7 @@ int64_t row_stride(const Call& call, const at::Tensor& t, int64_t n, int64_t c, 
     refuse(std::string(what) + " must be a " + c10::toString(dtype) + " [" + std::to_string(n) + ", " +
            std::to_string(c) + "] tensor with unit inner stride");
   call.on_device(t, what);
-  return n > 1 ? t.stride(0) : std::max(c, t.stride(0));
+  return n > 1 ? t.stride(0) : c;
 }
 
 int32_t dtype_code(at::ScalarType t, const char* what) {

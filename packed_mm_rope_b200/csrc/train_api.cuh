@@ -20,6 +20,33 @@ bool vector_rows(const void* p, int64_t stride, int32_t dtype) {
   return aligned16(p) && (stride * dtype_size(dtype)) % 16 == 0;
 }
 
+// Rows of `width` elements, `stride` elements apart.
+struct RowSpan {
+  const void* p;
+  int64_t rows, stride, width;
+  int size;                            // bytes of an element
+};
+
+// Whether two tensors share memory.  Columns of one buffer (equal strides) do not;
+// overlapping spans with different strides count as shared.
+bool overlap(const RowSpan& a, const RowSpan& b) {
+  if (a.p == nullptr || b.p == nullptr || a.rows < 1 || b.rows < 1) return false;
+  auto end = [](const RowSpan& r) {
+    return reinterpret_cast<uintptr_t>(r.p) + static_cast<uint64_t>((r.rows - 1) * r.stride + r.width) * r.size;
+  };
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  if (a0 >= end(b) || b0 >= end(a)) return false;
+  const int64_t sa = (a.rows == 1 ? b.stride : a.stride) * a.size, sb = (b.rows == 1 ? a.stride : b.stride) * b.size;
+  if (sa != sb || sa == 0) return true;
+  const int64_t apart = a0 <= b0 ? static_cast<int64_t>((b0 - a0) % sa) : (sa - static_cast<int64_t>((a0 - b0) % sa)) % sa;
+  return apart < a.width * a.size || sa - apart < b.width * b.size;
+}
+
+// For calls that may work in place: `out` is exactly `in`, or apart from it.
+bool in_place_or_apart(const RowSpan& out, const RowSpan& in) {
+  return (out.p == in.p && (out.stride == in.stride || out.rows == 1)) || !overlap(out, in);
+}
+
 template <typename T>
 struct TypeTag {
   using type = T;
@@ -260,6 +287,14 @@ int attention_parts(uint64_t blocks, int64_t n_k) {
   return parts;
 }
 
+RowSpan q_rows(const h3_attn_shape* a, const void* p, int64_t stride) {
+  return {p, a->batch * a->n_q, stride, a->n_heads * 128LL, 2};
+}
+
+RowSpan kv_rows(const h3_attn_shape* a, const void* p, int64_t stride) {
+  return {p, a->batch * a->n_k, stride, a->n_kv_heads * 128LL, 2};
+}
+
 float attention_scale(const h3_attn_shape* a) {
   return a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / std::sqrt(128.0f);
 }
@@ -292,6 +327,10 @@ h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v,
   if (!aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) || !aligned16(d_o) ||
       (reinterpret_cast<uintptr_t>(d_ranges) & 7u))
     return H3_ERR_UNSUPPORTED;
+  const RowSpan out = q_rows(a, d_o, o_stride);
+  if (overlap(out, q_rows(a, d_q, q_stride)) || overlap(out, kv_rows(a, d_k, k_stride)) ||
+      overlap(out, kv_rows(a, d_v, v_stride)))
+    return H3_ERR_INVALID_ARG;
   CUtensorMap tq, tk, tv;
   if (!make_qkv_map(&tq, d_q, a->batch, a->n_q, a->n_heads, q_stride, 128)) return H3_ERR_CUDA;
   tk = tv = tq;                          // without keys every row is empty and K, V are never read
@@ -351,6 +390,14 @@ h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const 
                           static_cast<const void*>(d_dv)})
     if (!aligned16(ptr)) return H3_ERR_UNSUPPORTED;
   if (reinterpret_cast<uintptr_t>(d_ranges) & 7u) return H3_ERR_UNSUPPORTED;
+  const RowSpan ins[] = {q_rows(a, d_do, st->dout), q_rows(a, d_q, st->q), q_rows(a, d_o, st->o),
+                         kv_rows(a, d_k, st->k), kv_rows(a, d_v, st->v)};
+  const RowSpan outs[] = {q_rows(a, d_dq, st->dq), kv_rows(a, d_dk, st->dk), kv_rows(a, d_dv, st->dv)};
+  for (int i = 0; i < 3; ++i) {
+    for (const RowSpan& in : ins)
+      if (overlap(outs[i], in)) return H3_ERR_INVALID_ARG;
+    if (overlap(outs[i], outs[(i + 1) % 3])) return H3_ERR_INVALID_ARG;
+  }
   if (!queries && !keys) return H3_OK;
   cudaStream_t s = as_stream(stream);
   if (!queries) {                          // no row reads the keys
@@ -370,6 +417,9 @@ h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const 
     return H3_ERR_CUDA;
   if (device_state() == nullptr) return H3_ERR_CUDA;
   const AttentionWork w = attention_work(a);
+  const uint64_t blocks = static_cast<uint64_t>(w.n_kt) * w.parts * a->n_kv_heads * a->batch +
+                          static_cast<uint64_t>(w.n_qt) * a->n_heads * a->batch;
+  if (blocks >= (1ull << 31)) return H3_ERR_INVALID_ARG;
   uint8_t* base = static_cast<uint8_t*>(d_work);
   h3::attn_bwd::Params p{};
   p.n_q = static_cast<int>(a->n_q);
@@ -411,9 +461,6 @@ h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const 
   h3::attn_bwd::prep_kernel<<<dim3(w.n_qt, heads, batch), 256, 0, s>>>(
       in, static_cast<const __nv_bfloat16*>(d_o), static_cast<const __nv_bfloat16*>(d_do), d_lse,
       reinterpret_cast<const int2*>(d_ranges), p.n_q, p.n_k, p.n_heads, w.n_qt, st->o, st->dout, stat, rng, hull);
-  const uint64_t blocks = static_cast<uint64_t>(w.n_kt) * w.parts * a->n_kv_heads * a->batch +
-                          static_cast<uint64_t>(w.n_qt) * heads * batch;
-  if (blocks >= (1ull << 31)) return H3_ERR_INVALID_ARG;
   h3::attn_bwd::backward_kernel<<<static_cast<unsigned>(blocks), h3::attn_bwd::THREADS, h3::attn_bwd::SMEM_BYTES, s>>>(
       tq, tk, tv, tdo, p);
   if (w.parts > 1) h3::attn_bwd::sum_parts_kernel<<<8 * sm_count(), 256, 0, s>>>(p);
@@ -436,6 +483,12 @@ h3_status h3_mmrope_rotate(const void* d_q, const void* d_k, void* d_q_out, void
   if ((q_stride | k_stride | q_out_stride | k_out_stride) % 8 != 0 || !aligned16(d_q) || !aligned16(d_k) ||
       !aligned16(d_q_out) || !aligned16(d_k_out))
     return H3_ERR_UNSUPPORTED;
+  const RowSpan qi{d_q, n_rows, q_stride, q_row, 2}, ki{d_k, n_rows, k_stride, k_row, 2};
+  const RowSpan qo{n_heads > 0 ? d_q_out : nullptr, n_rows, q_out_stride, q_row, 2};
+  const RowSpan ko{n_kv_heads > 0 ? d_k_out : nullptr, n_rows, k_out_stride, k_row, 2};
+  if (!in_place_or_apart(qo, qi) || !in_place_or_apart(ko, ki) || overlap(qo, ki) || overlap(ko, qi) ||
+      overlap(qo, ko))
+    return H3_ERR_INVALID_ARG;
   h3::RopeTable tab = make_rope_table(cfg);
   if (inverse)   // the rotation by -a: cos is even and sin odd, exactly
     for (double& f : tab.inv_freq) f = -f;
@@ -474,6 +527,9 @@ h3_status h3_layernorm(const void* d_x, void* d_y, const void* d_weight, const v
   if (hidden > h3::norm::MAX_HIDDEN || (param_dtype != dtype && param_dtype != H3_DTYPE_F32)) return H3_ERR_UNSUPPORTED;
   if (n_rows == 0) return H3_OK;
   if (!d_x || !d_y) return H3_ERR_INVALID_ARG;
+  if (!in_place_or_apart({d_y, n_rows, y_row_stride, hidden, dtype_size(dtype)},
+                         {d_x, n_rows, x_row_stride, hidden, dtype_size(dtype)}))
+    return H3_ERR_INVALID_ARG;
   const bool vec = hidden % 8 == 0 && vector_rows(d_x, x_row_stride, dtype) && vector_rows(d_y, y_row_stride, dtype) &&
                    aligned16(d_weight) && aligned16(d_bias);
   const int sms = sm_count();
@@ -526,6 +582,10 @@ h3_status h3_layernorm_backward(const void* d_dy, const void* d_x, const float* 
   const bool params = d_dweight != nullptr || d_dbias != nullptr;
   if (params && (d_work == nullptr || !aligned256(d_work))) return H3_ERR_INVALID_ARG;
   if (n_rows > 0 && (!d_dy || !d_x || !d_mean || !d_rstd || !d_dx)) return H3_ERR_INVALID_ARG;
+  const RowSpan dx{d_dx, n_rows, dx_row_stride, hidden, dtype_size(dtype)};
+  if (!in_place_or_apart(dx, {d_dy, n_rows, dy_row_stride, hidden, dtype_size(dtype)}) ||
+      !in_place_or_apart(dx, {d_x, n_rows, x_row_stride, hidden, dtype_size(dtype)}))
+    return H3_ERR_INVALID_ARG;
   const bool vec = hidden % 8 == 0 && vector_rows(d_dy, dy_row_stride, dtype) && vector_rows(d_x, x_row_stride, dtype) &&
                    vector_rows(d_dx, dx_row_stride, dtype) && aligned16(d_weight);
   float* partials = params ? static_cast<float*>(d_work) : nullptr;
@@ -595,6 +655,10 @@ h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const in
   if (n_rows > 0 && (!vector_rows(d_dy, dy_row_stride, H3_DTYPE_BF16) || !vector_rows(d_x, x_row_stride, H3_DTYPE_BF16) ||
                      !vector_rows(d_dx, dx_row_stride, H3_DTYPE_BF16) || !aligned16(d_table)))
     return H3_ERR_UNSUPPORTED;
+  const RowSpan dx{d_dx, n_rows, dx_row_stride, hidden, 2};
+  if (!in_place_or_apart(dx, {d_dy, n_rows, dy_row_stride, hidden, 2}) ||
+      !in_place_or_apart(dx, {d_x, n_rows, x_row_stride, hidden, 2}))
+    return H3_ERR_INVALID_ARG;
   cudaStream_t s = as_stream(stream);
   if (n_rows == 0)
     return cudaMemsetAsync(d_dtable, 0, static_cast<size_t>(n_entries) * 2u * hidden * 4u, s) == cudaSuccess

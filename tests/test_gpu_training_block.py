@@ -150,3 +150,113 @@ def test_prefix_rows_can_be_reused(h3):
     k2, v2 = k.clone(), v.clone()
     k2[p:], v2[p:] = randn(8, n - p, KV, 128), randn(9, n - p, KV, 128)
     assert torch.equal(h3.masked_attention(q, k2, v2, ranges)[:p], whole[:p])
+
+
+def test_offsets_past_32_bits(h3):
+    """Rows 2^30 elements apart: the last of three lies past element 2^31.  Each call gives what it gives packed."""
+    apart, rows = 1 << 30, 3
+    buf = torch.empty((rows - 1) * apart + 4096, dtype=torch.bfloat16, device="cuda")
+    used = [0]
+
+    def far(t):
+        t = t.view(rows, -1)
+        at = used[0]
+        used[0] += (t.shape[1] + 7) // 8 * 8
+        view = buf.as_strided((rows, t.shape[1]), (apart, 1), at)
+        view.copy_(t)
+        return view
+
+    def heads(t):
+        f = far(t)
+        return f.as_strided((rows, f.shape[1] // 128, 128), (apart, 128, 1), f.storage_offset())
+
+    q, do = randn(1, rows, 4, 128), randn(4, rows, 4, 128)
+    k, v = randn(2, rows, 2, 128), randn(3, rows, 2, 128)
+    ranges = torch.tensor([[0, 1], [0, 2], [1, 3]], dtype=torch.int32, device="cuda")
+    fq, fk, fv, fdo = (heads(t) for t in (q, k, v, do))
+    lse, flse = torch.empty(4, rows, device="cuda"), torch.empty(4, rows, device="cuda")
+    o = h3.masked_attention(q, k, v, ranges, lse=lse)
+    fo = h3.masked_attention(fq, fk, fv, ranges, out=heads(torch.zeros_like(q)), lse=flse)
+    assert torch.equal(o, fo) and torch.equal(lse, flse)
+    want = h3.masked_attention_backward(do, q, k, v, o, lse, ranges)
+    got = h3.masked_attention_backward(fdo, fq, fk, fv, fo, flse, ranges, *(heads(torch.zeros_like(t)) for t in want))
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    used[0] = 0
+    fq, fk = heads(q), heads(k)
+    coords = randn(5, rows, 3, dtype=torch.float32, scale=30.0)
+    want = h3.mmrope_rotate(q, k, coords)
+    got = h3.mmrope_rotate(fq, fk, coords, q_out=fq, k_out=fk)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    for c in (256, 1280):                              # a warp per row, a ring of rows
+        used[0] = 0
+        x, dy = randn(6, rows, c), randn(7, rows, c)
+        fx, fdy = far(x), far(dy)
+        y, mean, rstd = h3.layer_norm(x)
+        fy, _, _ = h3.layer_norm(fx, out=far(torch.zeros_like(x)))
+        assert torch.equal(y, fy)
+        table = randn(8, 2, 2, c, dtype=torch.float32)
+        level, tag = torch.tensor([0, 0, 0], device="cuda").int(), torch.tensor([1, 0, 1], device="cuda").int()
+        want = h3.adaln_modulate_backward(dy, x, level, tag, table)
+        got = h3.adaln_modulate_backward(fdy, fx, level, tag, table, dx=fy)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        want = h3.layer_norm_backward(dy, x, mean, rstd)
+        got = h3.layer_norm_backward(fdy, fx, mean, rstd, dx=fdy)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert h3.h3_check_device_error() == h3.H3_OK
+
+
+def test_calls_at_once_on_two_streams(h3):
+    """Two blocks whose calls interleave on two streams give what they give alone."""
+    t, u = _inputs(), _inputs()
+    u["x"], u["dy"] = randn(31, N, C), randn(32, N, C)
+    want = _step(h3, t), _step(h3, u)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    here = torch.cuda.current_stream()
+    for _ in range(5):
+        got = []
+        for s, inputs in zip(streams, (t, u)):
+            s.wait_stream(here)
+            with torch.cuda.stream(s):
+                got.append(_step(h3, inputs))
+        for s in streams:
+            here.wait_stream(s)
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(g[k], w[k]) for k in w)
+    for s in streams:
+        assert h3.h3_check_device_error(s.cuda_stream) == h3.H3_OK
+
+
+def test_single_rows_and_heads_of_larger_tensors(h3):
+    """Sizes of one: their strides say nothing."""
+    q, k, v = randn(1, 3, 5, 4, 128), randn(2, 3, 5, 2, 128), randn(3, 3, 5, 2, 128)
+    one = torch.tensor([[0, 5]] * 3, dtype=torch.int32, device="cuda").view(3, 1, 2)
+    row = h3.masked_attention(q[:, 2:3], k, v, one)    # one row of each batch entry
+    for b in range(3):
+        assert torch.equal(row[b], h3.masked_attention(q[b, 2:3].contiguous(), k[b], v[b], one[b]))
+    x = randn(4, 7, 128).t().contiguous().t()          # [7, 128] with columns apart: refused as it is
+    with pytest.raises(ValueError):
+        h3.masked_attention(x[:, None], x[:, None], x[:, None], one.view(3, 2))
+    y = randn(5, 7, 128)
+    r = torch.tensor([[0, 7]] * 7, dtype=torch.int32, device="cuda")
+    head = y.as_strided((7, 1, 128), (128, 999, 1))
+    assert torch.equal(h3.masked_attention(head, head, head, r), h3.masked_attention(*[y[:, None]] * 3, r))
+    empty = h3.masked_attention(q[:, :0], k, v, one[:, :0])
+    assert empty.shape == (3, 0, 4, 128)
+
+
+def test_views_of_one_buffer(h3):
+    """Columns of one buffer as inputs and outputs of one call."""
+    n = 200
+    buf = torch.zeros(n, 3 * H, 128, dtype=torch.bfloat16, device="cuda")
+    buf[:, :2 * H] = randn(1, n, 2 * H, 128)
+    q, k, out = buf.split(H, 1)
+    r = _full(n)
+    want = h3.masked_attention(q.contiguous(), k.contiguous(), k.contiguous(), r)
+    assert torch.equal(h3.masked_attention(q, k, k, r, out=out), want)
+    with pytest.raises(h3.H3Error):
+        h3.masked_attention(q, k, k, r, out=q)
+
+
+def _full(n):
+    return torch.tensor([[0, n]] * n, dtype=torch.int32, device="cuda")

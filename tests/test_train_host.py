@@ -156,3 +156,54 @@ def test_masked_attention_backward():
     for kw in (dict(batch=0), dict(n_heads=5), dict(n_q=1 << 31), dict(n_k=-1), dict(softmax_scale=float("nan"))):
         assert _err(B, *ptrs, _shape(**kw), S(**ok)) == INV, kw
     assert _err(B, *ptrs, _shape(head_dim=64), S(**ok)) == UNS
+
+
+def _apart(n, step=1 << 20):
+    """n distinct 256-byte aligned addresses, far from one another."""
+    return [0x1000000 + i * step for i in range(n)]
+
+
+def test_outputs_apart_from_inputs():
+    """An output may not share memory with an input, except exactly in place where the call allows it."""
+    # masked attention: out inside q, k or v
+    q, k, v, o, r = _apart(5)
+    strides = (512, 256, 256, 512)
+    for bad in (q, k, v, q + 1024 * 3, k - 1024, v + 512 * 3):
+        assert _err(h3.h3_masked_attention, q, k, v, bad, 0, r, _shape(), *strides) == INV, hex(bad)
+    # an input's columns with another row stride
+    assert _err(h3.h3_masked_attention, q, k, v, q + 1024, 0, r, _shape(), 1024, 256, 256, 512) == INV
+
+    p = _apart(11)                                     # dout q k v o lse ranges dq dk dv work
+    S = h3.h3_attn_strides(q=512, k=256, v=256, o=512, dout=512, dq=512, dk=256, dv=256)
+    for i in (7, 8, 9):
+        for j in (0, 1, 2, 3, 4, 7, 8, 9):
+            if i == j:
+                continue
+            a = list(p)
+            a[i] = a[j]
+            assert _err(h3.h3_masked_attention_backward, *a, _shape(), S) == INV, (i, j)
+
+    # rotation: across tensors, or shifted in its own
+    q, k, qo, ko, c = _apart(5)
+    tail = (c, 4, 2, 1, 256, 128, 256, 128, h3.rope_cfg())
+    for a in ((q, k, k, ko), (q, k, qo, q), (q, k, qo, qo), (q, k, q + 512, ko), (q, k, qo, k - 256)):
+        assert _err(h3.h3_mmrope_rotate, *a, *tail) == INV
+    assert _err(h3.h3_mmrope_rotate, q, k, q, ko, c, 4, 2, 1, 256, 128, 512, 128, h3.rope_cfg()) == INV
+
+    x, y, m, rs, w = _apart(5)
+    assert _err(h3.h3_layernorm, x, x + 128, 0, 0, m, rs, 4, 64, 64, 64) == INV
+    assert _err(h3.h3_layernorm, x, x, 0, 0, m, rs, 4, 64, 64, 128) == INV
+    dy, dx = y, x + (1 << 24)
+    for bad, sy, sx, sd in ((x + 128, 64, 64, 64), (dy - 128, 64, 64, 64), (x, 64, 64, 72), (dy, 72, 64, 64)):
+        assert _err(h3.h3_layernorm_backward, dy, x, m, rs, 0, bad, 0, 0, 0, 4, 64, sy, sx, sd) == INV
+    t, tag, tab, dtab = _apart(9)[5:]
+    for bad in (x + 128, dy - 128):
+        assert _err(h3.h3_adaln_modulate_backward, dy, x, t, tag, tab, bad, dtab, w, 3, 4, 64, 64, 64, 64) == INV
+
+
+def test_binding_is_built():
+    """The compiled binding imports without a GPU and offers the calls of the package."""
+    mod = h3._binding()
+    for name in ("rotate", "key_ranges", "attention", "attention_backward", "layer_norm", "layer_norm_backward",
+                 "adaln_backward"):
+        assert callable(getattr(mod, name))
