@@ -355,6 +355,24 @@ __device__ __forceinline__ void store_partial(float* out, int t, int chunks, int
   }
 }
 
+// The same for hidden a multiple of 8.
+template <int G, int CH>
+__device__ __forceinline__ void store_partial_chunks(float* out, int t, int chunks, int hidden, const float2 (&dw)[CH][4],
+                                                     const float2 (&db)[CH][4]) {
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = t + G * i;
+    if (c >= chunks) continue;
+    float4* w = reinterpret_cast<float4*>(out) + 2 * c;
+    float4* b = reinterpret_cast<float4*>(out + hidden) + 2 * c;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      w[m] = make_float4(dw[i][2 * m].x, dw[i][2 * m].y, dw[i][2 * m + 1].x, dw[i][2 * m + 1].y);
+      b[m] = make_float4(db[i][2 * m].x, db[i][2 * m].y, db[i][2 * m + 1].x, db[i][2 * m + 1].y);
+    }
+  }
+}
+
 // Group (block, g) takes rows group, group + groups, ... and leaves its column
 // sums in partial row `group` of `partials` [groups][2][hidden].  dx may be dy or
 // x (a group has read its whole row before it writes any of it).
@@ -775,7 +793,7 @@ __global__ void __launch_bounds__(G + 32, MINB) layernorm_backward_ring_kernel(
     ring.release(at);
   }
   if (partials != nullptr)
-    store_partial<G, CH>(partials + static_cast<long long>(blockIdx.x) * 2 * hidden, t, chunks, hidden, dw, db);
+    store_partial_chunks<G, CH>(partials + static_cast<long long>(blockIdx.x) * 2 * hidden, t, chunks, hidden, dw, db);
 }
 
 // ------------------------------------------------- sums of partial rows ----
@@ -993,107 +1011,121 @@ __global__ void __launch_bounds__(G > THREADS ? G : THREADS) adaln_backward_kern
     store_partial<G, CH>(partials + (group + entry) * 2 * hidden, t, chunks, hidden, dw, db);
 }
 
-// R rows of the AdaLN backward pass whose means are known, as ring_backward_rows:
-// one reduction joins the squared deviations with sum(g) and sum(g (x - mean)).
-template <int G, int CH, int R, typename Dst>
-__device__ __forceinline__ void ring_adaln_rows(const uint8_t* at, const uint8_t* at_d, uint32_t row_bytes,
-                                                const float (&mean)[R], unsigned active, const float2 (&w)[CH][4],
-                                                float inv_n, float eps, float* buf, int& parity, Dst dst, int chunks,
-                                                int hidden, float2 (&dw)[CH][4], float2 (&db)[CH][4]) {
+// Long rows, one block of G + 32 (S + 1) threads per SM and group: a warp copies
+// rows of x and dy into a ring of shared memory, S warps each take a whole row there
+// and find its statistics, and G threads with CH chunks each turn rows into dx and
+// column sums, with the entry's weights in registers while it lasts.  No step needs a
+// barrier of the block: a row's statistics are shuffles of one warp, and rows pass
+// from warp to warp by one mbarrier each way.
+constexpr int ADALN_SLOTS = 10;
+
+struct RowTerms {            // dx = (dy w) rstd + x b + c, xhat = x rstd + shift
+  float rstd, shift, b, c;
+};
+
+// Terms of a row in shared memory by one warp; lane 0 holds the result.
+__device__ __forceinline__ RowTerms adaln_row_terms(const uint8_t* x, const uint8_t* dy, const float* scale, int chunks,
+                                                    float inv_n, float eps, int lane) {
   using T = __nv_bfloat16;
-  const int t = threadIdx.x;
-  float s[3 * R];
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int c = lane; c < chunks; c += 32) {
+    const Chunk<T> u = ring_chunk<T>(x, c);
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float2 a0 = make_float2(0.f, 0.f), a1 = a0, a2 = a0;
-    if (active >> r & 1u) {
-      const float2 nm = make_float2(-mean[r], -mean[r]);
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = t + G * i;
-        if (c >= chunks) continue;
-        const Chunk<T> ux = ring_chunk<T>(at + r * row_bytes, c), ud = ring_chunk<T>(at_d + r * row_bytes, c);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const float2 xc = __fadd2_rn(pair_of(ux, m), nm);
-          const float2 g = __fmul2_rn(pair_of(ud, m), w[i][m]);
-          a0 = __ffma2_rn(xc, xc, a0);
-          a1 = __fadd2_rn(a1, g);
-          a2 = __ffma2_rn(g, xc, a2);
-        }
-      }
-    }
-    s[3 * r] = a0.x + a0.y;
-    s[3 * r + 1] = a1.x + a1.y;
-    s[3 * r + 2] = a2.x + a2.y;
+    for (int m = 0; m < 4; ++m) s = __fadd2_rn(s, pair_of(u, m));
   }
-  BlockSum<G, 3 * R>::sum(s, buf, parity, false);
+  float mean = s.x + s.y;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (!(active >> r & 1u)) continue;
-    const float rstd = rsqrtf(fmaf(s[3 * r], inv_n, eps));
-    const float mr = -mean[r] * rstd;
-    const float cb = -s[3 * r + 2] * inv_n * rstd * rstd * rstd;
-    const float cc = fmaf(-mean[r], cb, -s[3 * r + 1] * inv_n * rstd);
-    const float2 rs = make_float2(rstd, rstd), nm = make_float2(mr, mr), b2 = make_float2(cb, cb);
-    const float2 c0 = make_float2(cc, cc);
-    T* dxr = dst(r);
+  for (int o = 16; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+  mean *= inv_n;
+  const float2 nm = make_float2(-mean, -mean);
+  float2 a0 = make_float2(0.f, 0.f), a1 = a0, a2 = a0;   // (x - mean)^2, g, g (x - mean)
+#pragma unroll 2
+  for (int c = lane; c < chunks; c += 32) {
+    const Chunk<T> ux = ring_chunk<T>(x, c), ud = ring_chunk<T>(dy, c);
+    const float4 w0 = __ldg(reinterpret_cast<const float4*>(scale) + 2 * c);
+    const float4 w1 = __ldg(reinterpret_cast<const float4*>(scale) + 2 * c + 1);
+    const float2 w[4] = {{w0.x, w0.y}, {w0.z, w0.w}, {w1.x, w1.y}, {w1.z, w1.w}};
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = t + G * i;
-      if (c >= chunks) continue;
-      const Chunk<T> ux = ring_chunk<T>(at + r * row_bytes, c), ud = ring_chunk<T>(at_d + r * row_bytes, c);
-      Chunk<T> o;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float2 x = pair_of(ux, m), d = pair_of(ud, m);
-        dw[i][m] = __ffma2_rn(d, __ffma2_rn(x, rs, nm), dw[i][m]);
-        db[i][m] = __fadd2_rn(db[i][m], d);
-        set_pair(o, m, __ffma2_rn(__fmul2_rn(d, w[i][m]), rs, __ffma2_rn(x, b2, c0)));
-      }
-      store_chunk<T, true>(dxr, 8 * c, hidden, o);
+    for (int m = 0; m < 4; ++m) {
+      const float2 xc = __fadd2_rn(pair_of(ux, m), nm), d = pair_of(ud, m);
+      const float2 g = __ffma2_rn(d, w[m], d);
+      a0 = __ffma2_rn(xc, xc, a0);
+      a1 = __fadd2_rn(a1, g);
+      a2 = __ffma2_rn(g, xc, a2);
     }
   }
+  float var = a0.x + a0.y, sg = a1.x + a1.y, sgx = a2.x + a2.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    var += __shfl_xor_sync(0xffffffffu, var, o);
+    sg += __shfl_xor_sync(0xffffffffu, sg, o);
+    sgx += __shfl_xor_sync(0xffffffffu, sgx, o);
+  }
+  RowTerms r;
+  r.rstd = rsqrtf(fmaf(var, inv_n, eps));
+  r.shift = -mean * r.rstd;
+  r.b = -sgx * inv_n * r.rstd * r.rstd * r.rstd;
+  r.c = fmaf(-mean, r.b, -sg * inv_n * r.rstd);
+  return r;
 }
 
-// The same by rings of (x, dy) rows, one block per group; the entry's weights
-// stay in registers while it lasts.
-template <int G, int CH, int R, int MINB>
-__global__ void __launch_bounds__(G + 32, MINB) adaln_backward_ring_kernel(
+template <int G, int CH, int S>
+__global__ void __launch_bounds__(G + 32 * (S + 1), 1) adaln_backward_ring_kernel(
     const __nv_bfloat16* dy, const __nv_bfloat16* x, const float* __restrict__ table, const int2* __restrict__ order,
     __nv_bfloat16* dx, float* __restrict__ partials, int n_entries, long long n_rows, long long per, int hidden,
     long long dy_stride, long long x_stride, long long dx_stride, float eps, int slots, unsigned long long limit,
     int err_slot) {
   using T = __nv_bfloat16;
   extern __shared__ __align__(128) uint8_t rows[];
-  __shared__ uint64_t bars[2 * MAX_SLOTS];
+  __shared__ uint64_t bars[3 * ADALN_SLOTS];
+  __shared__ RowTerms terms[ADALN_SLOTS];
   __shared__ uint32_t abort_word;
-  __shared__ float buf1[BlockSum<G, R>::SIZE];
-  __shared__ float buf2[BlockSum<G, 3 * R>::SIZE];
-  const int t = threadIdx.x, chunks = hidden / 8;
-  const uint32_t row_bytes = static_cast<uint32_t>(hidden * sizeof(T));
-  const Ring ring{smem_u32(bars), smem_u32(bars + MAX_SLOTS), smem_u32(rows), row_bytes, 2 * R * row_bytes, slots,
+  const int t = threadIdx.x, lane = t & 31, chunks = hidden / 8;
+  const uint32_t row_bytes = static_cast<uint32_t>(hidden * sizeof(T)), ready = smem_u32(bars + 2 * ADALN_SLOTS);
+  const Ring ring{smem_u32(bars), smem_u32(bars + ADALN_SLOTS), smem_u32(rows), row_bytes, 2 * row_bytes, slots,
                   &abort_word, limit, err_slot};
   const long long group = blockIdx.x, first = group * per;
   const long long last = first + per < n_rows ? first + per : n_rows;
-  const int n_pos = last > first ? static_cast<int>(last - first) : 0;
-  const int count = (n_pos + R - 1) / R;
-  auto n_of = [&](int i) { return n_pos - i * R < R ? n_pos - i * R : R; };
+  const int count = last > first ? static_cast<int>(last - first) : 0;
   order += first;
   if (t == 0) {
     abort_word = 0u;
+    for (int s = 0; s < slots; ++s) mbar_init(ready + 8u * s, 1);
     ring.init(G / 32);
   }
   __syncthreads();
-  if (t >= G) {
-    if (t == G)
-      ring.produce<R, 2>(count, n_of, [&](int tensor, int i, int r) {
-        const long long row = order[i * R + r].x;
+  if (t >= G + 32 * S) {
+    if (lane == 0)
+      ring.produce<1, 2>(count, [](int) { return 1; }, [&](int tensor, int i, int) {
+        const long long row = order[i].x;
         return tensor == 0 ? x + row * x_stride : dy + row * dy_stride;
       });
     return;
   }
   const float inv_n = 1.f / static_cast<float>(hidden);
+  if (t >= G) {
+    const int warps = S < slots ? S : slots, mine = (t - G) >> 5;
+    for (int i = mine; i < count && mine < warps; i += warps) {
+      const RingAt at{i % slots, static_cast<uint32_t>(i / slots) & 1u};
+      const int e = order[i].y;
+      // the step before in this slot has to be over: copies may land out of order, and the
+      // wait for a copy tells two phases of its slot apart, not three
+      if (i >= slots && !__all_sync(0xffffffffu, mbar_wait_bounded(ring.empty + 8u * at.slot, at.phase ^ 1u, &abort_word,
+                                                                   limit, err_slot)))
+        break;
+      if (!__all_sync(0xffffffffu, ring.wait(at))) break;
+      const uint8_t* in = rows + at.slot * ring.slot_bytes;
+      if (e < n_entries) {
+        const RowTerms r =
+            adaln_row_terms(in, in + row_bytes, table + (2LL * e + 1) * hidden, chunks, inv_n, eps, lane);
+        if (lane == 0) terms[at.slot] = r;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ready + 8u * at.slot);
+    }
+    return;
+  }
   float2 w[CH][4], dw[CH][4], db[CH][4];
   auto clear = [&] {
 #pragma unroll
@@ -1102,70 +1134,61 @@ __global__ void __launch_bounds__(G + 32, MINB) adaln_backward_ring_kernel(
       for (int m = 0; m < 4; ++m) dw[i][m] = db[i][m] = make_float2(0.f, 0.f);
   };
   clear();
-  int parity1 = 0, parity2 = 0, entry = -1;
-  int2 next[R];                                    // (row, entry) of the next step's positions
-  auto look = [&](int i) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) next[r] = i * R + r < n_pos ? order[i * R + r] : make_int2(0, -1);
-  };
-  look(0);
+  int entry = -1;
+  int2 next = count > 0 ? order[0] : make_int2(0, 0);
   RingAt at;
   for (int i = 0; i < count; ++i, at.next(slots)) {
-    int2 here[R];
+    const int2 here = next;                        // (row, entry)
+    if (i + 1 < count) next = order[i + 1];
+    if (here.y != entry) {
+      if (entry >= 0 && entry < n_entries)
+        store_partial_chunks<G, CH>(partials + (group + entry) * 2 * hidden, t, chunks, hidden, dw, db);
+      entry = here.y;
+      clear();
+      if (entry < n_entries) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) here[r] = next[r];
-    look(i + 1);
-    const bool landed = ring.wait(at);
-    const uint8_t* in = rows + at.slot * ring.slot_bytes;
-    float mean[R];
-    if (ring_means<T, G, CH, R>(in, row_bytes, chunks, inv_n, buf1, parity1, !landed, mean)) break;
-    // entries ascend: the rows of one entry at a time (nearly always all R)
-    unsigned left = (1u << n_of(i)) - 1u;
-    while (left != 0u) {
-      int e = 0;
-      unsigned active = 0u;
+        for (int k = 0; k < CH; ++k) {
+          if (t + G * k >= chunks) continue;
+          load_param<float, true>(table + (2LL * entry + 1) * hidden, 8 * (t + G * k), hidden, 0.f, w[k]);
 #pragma unroll
-      for (int r = R - 1; r >= 0; --r)
-        if (left >> r & 1u) e = here[r].y;
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if ((left >> r & 1u) && here[r].y == e) active |= 1u << r;
-      left &= ~active;
-      if (e != entry) {
-        if (entry >= 0 && entry < n_entries)
-          store_partial<G, CH>(partials + (group + entry) * 2 * hidden, t, chunks, hidden, dw, db);
-        entry = e;
-        clear();
-        if (entry < n_entries) {
-#pragma unroll
-          for (int k = 0; k < CH; ++k) {
-            if (t + G * k >= chunks) continue;
-            load_param<float, true>(table + (2LL * entry + 1) * hidden, 8 * (t + G * k), hidden, 0.f, w[k]);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) w[k][m] = __fadd2_rn(w[k][m], make_float2(1.f, 1.f));
-          }
+          for (int m = 0; m < 4; ++m) w[k][m] = __fadd2_rn(w[k][m], make_float2(1.f, 1.f));
         }
       }
-      auto dst = [&](int r) { return dx + here[r].x * dx_stride; };
-      if (entry == n_entries) {            // no such table entry: NaN, as the forward call gives
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(ready + 8u * at.slot, at.phase, &abort_word, limit, err_slot)))
+      break;
+    const uint8_t* in = rows + at.slot * ring.slot_bytes;
+    T* out = dx + here.x * dx_stride;
+    if (entry == n_entries) {              // no such table entry: NaN, as the forward call gives
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          if (!(active >> r & 1u)) continue;
+      for (int k = 0; k < CH; ++k) {
+        const Chunk<T> nan = {{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u}};
+        if (t + G * k < chunks) store_chunk<T, true>(out, 8 * (t + G * k), hidden, nan);
+      }
+    } else {
+      const RowTerms r = terms[at.slot];
+      const float2 rs = make_float2(r.rstd, r.rstd), nm = make_float2(r.shift, r.shift), b2 = make_float2(r.b, r.b);
+      const float2 c0 = make_float2(r.c, r.c);
 #pragma unroll
-          for (int k = 0; k < CH; ++k) {
-            const Chunk<T> nan = {{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u}};
-            if (t + G * k < chunks) store_chunk<T, true>(dst(r), 8 * (t + G * k), hidden, nan);
-          }
+      for (int k = 0; k < CH; ++k) {
+        const int c = t + G * k;
+        if (c >= chunks) continue;
+        const Chunk<T> ux = ring_chunk<T>(in, c), ud = ring_chunk<T>(in + row_bytes, c);
+        Chunk<T> o;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float2 xv = pair_of(ux, m), d = pair_of(ud, m);
+          dw[k][m] = __ffma2_rn(d, __ffma2_rn(xv, rs, nm), dw[k][m]);
+          db[k][m] = __fadd2_rn(db[k][m], d);
+          set_pair(o, m, __ffma2_rn(__fmul2_rn(d, w[k][m]), rs, __ffma2_rn(xv, b2, c0)));
         }
-      } else {
-        ring_adaln_rows<G, CH, R>(in, in + R * row_bytes, row_bytes, mean, active, w, inv_n, eps, buf2, parity2, dst,
-                                  chunks, hidden, dw, db);
+        store_chunk<T, true>(out, 8 * c, hidden, o);
       }
     }
     ring.release(at);
   }
   if (entry >= 0 && entry < n_entries)
-    store_partial<G, CH>(partials + (group + entry) * 2 * hidden, t, chunks, hidden, dw, db);
+    store_partial_chunks<G, CH>(partials + (group + entry) * 2 * hidden, t, chunks, hidden, dw, db);
 }
 
 // d_table[e][0] = sum of dy (shift), [e][1] = sum of dy xhat (scale)

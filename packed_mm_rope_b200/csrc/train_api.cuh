@@ -196,7 +196,23 @@ long long backward_groups(int64_t n_rows, int hidden) {
   return ring_takes(hidden) ? std::max<long long>(groups, std::min<long long>(2LL * kRingSms, n_rows)) : groups;
 }
 
-// ---- AdaLN backward: workspace ----
+// ---- AdaLN backward ----
+
+// Threads that apply the rows' terms (see the kernel) and their chunks of a row.
+template <typename F>
+h3_status with_adaln_ring(int hidden, F f) {
+  const int chunks = hidden / 8;
+  if (chunks <= 224) return f(RingShape<224, 1, 1>{});
+  if (chunks <= 448) return f(RingShape<224, 2, 1>{});
+  if (chunks <= 672) return f(RingShape<224, 3, 1>{});
+  return f(RingShape<352, 3, 1>{});
+}
+
+// Warps that find the terms of rows, and the ring's size: what it leaves of an SM's 256 KB
+// caches the table entry that these warps read.  28,196 x 5,376: 4, 5, 6, 7 warps with 150 KB
+// 184, 172, 172, 173 us; 6 warps with 129, 150, 172 KB 179, 172, 177 us.
+constexpr int kAdalnWarps = 6;
+constexpr uint64_t kAdalnSmem = 160u << 10;
 
 struct AdalnWork {
   long long groups, per;               // row groups, sorted positions per group
@@ -208,10 +224,7 @@ AdalnWork adaln_work(int64_t n_rows, int hidden, int32_t n_entries) {
   AdalnWork w;
   w.groups = std::max<long long>(1, backward_groups(n_rows, hidden));
   if (ring_takes(hidden))              // the rows are always aligned: one group per block of the ring kernel
-    with_backward_ring(hidden, [&](auto shape) {
-      w.groups = std::max<long long>(1, std::min<long long>(decltype(shape)::CTAS * kRingSms, n_rows));
-      return H3_OK;
-    });
+    w.groups = std::max<long long>(1, std::min<long long>(kRingSms, n_rows));
   w.per = std::max<long long>(1, (n_rows + w.groups - 1) / w.groups);
   w.blocks = static_cast<int>((n_rows + h3::norm::SORT_ROWS - 1) / h3::norm::SORT_ROWS);
   w.order = 0;
@@ -678,19 +691,18 @@ h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const in
   h3_status st = launched();
   if (st != H3_OK) return st;
   if (ring_takes(hidden))
-    st = with_backward_ring(hidden, [&](auto shape) {
+    st = with_adaln_ring(hidden, [&](auto shape) {
       using S = decltype(shape);
-      RingPlan plan = ring_plan(n_rows, 2u * hidden, 2, S::CTAS, {1, 2});
-      plan.blocks = w.groups;
-      auto go = [&](auto rows) {
-        return launch_ring<h3::norm::adaln_backward_ring_kernel<S::G, S::CH, decltype(rows)::value, S::CTAS>>(
-            plan, S::G + 32, s, static_cast<const __nv_bfloat16*>(d_dy), static_cast<const __nv_bfloat16*>(d_x),
-            d_table, static_cast<const int2*>(order), static_cast<__nv_bfloat16*>(d_dx), partials, n_entries,
-            static_cast<long long>(n_rows), w.per, hidden, static_cast<long long>(dy_row_stride),
-            static_cast<long long>(x_row_stride), static_cast<long long>(dx_row_stride), eps, plan.slots,
-            static_cast<unsigned long long>(g_wait_limit_ns.load()), error_slot(stream));
-      };
-      return plan.rows == 2 ? go(IntTag<2>{}) : go(IntTag<1>{});
+      RingPlan plan{1, 0, w.groups, 0};
+      plan.slots = static_cast<int>(std::min<uint64_t>(h3::norm::ADALN_SLOTS, kAdalnSmem / (4u * hidden)));
+      plan.smem = static_cast<size_t>(plan.slots) * 4u * hidden;
+      return launch_ring<h3::norm::adaln_backward_ring_kernel<S::G, S::CH, kAdalnWarps>>(
+          plan, S::G + 32 * (kAdalnWarps + 1), s, static_cast<const __nv_bfloat16*>(d_dy),
+          static_cast<const __nv_bfloat16*>(d_x), d_table, static_cast<const int2*>(order),
+          static_cast<__nv_bfloat16*>(d_dx), partials, n_entries, static_cast<long long>(n_rows), w.per, hidden,
+          static_cast<long long>(dy_row_stride), static_cast<long long>(x_row_stride),
+          static_cast<long long>(dx_row_stride), eps, plan.slots,
+          static_cast<unsigned long long>(g_wait_limit_ns.load()), error_slot(stream));
     });
   else
     st = with_backward_shape(hidden, [&](auto shape) {
@@ -708,7 +720,7 @@ h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const in
   if (st != H3_OK) return st;
   // many partial rows per entry are added by 16 rows of threads, few by 2
   const dim3 rgrid((hidden + 255) / 256, 2 * n_entries);
-  if (w.groups >= 32LL * n_entries)
+  if (w.groups >= 8LL * n_entries)
     h3::norm::adaln_reduce_kernel<16><<<rgrid, 64 * 16, 0, s>>>(partials, starts, w.per, hidden, d_dtable);
   else
     h3::norm::adaln_reduce_kernel<2><<<rgrid, 64 * 2, 0, s>>>(partials, starts, w.per, hidden, d_dtable);

@@ -179,7 +179,8 @@ def _rows(n, levels, shuffled, seed=0):
 
 @pytest.mark.parametrize("n,c,levels,shuffled", [(1, 64, 1, False), (82, 128, 2, True), (33, 8, 3, False),
                                                  (2049, 256, 40, True), (700, 1032, 7, True), (4584, 5376, 2, True),
-                                                 (1500, 5376, 31, False), (300, 8192, 100, True), (5000, 64, 2730, True)])
+                                                 (1500, 5376, 31, False), (300, 8192, 100, True), (5000, 64, 2730, True),
+                                                 (2000, 8192, 5, True), (9000, 1288, 3, True), (3000, 4096, 900, True)])
 def test_adaln_backward(h3, n, c, levels, shuffled):
     x, dy = randn(1, n, c, scale=1.5, shift=0.5), randn(2, n, c)
     ts, tags = _rows(n, levels, shuffled)
