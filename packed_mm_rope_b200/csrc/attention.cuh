@@ -71,13 +71,20 @@
 // O is not finite then.  In that case the CTA runs a second time: logits are masked
 // one by one, the softmax warps first clear such elements of V from every tile
 // with masked pairs, and rows that do attend to such a key get a NaN logit there:
-// masked places cannot change a row, and what a row attends to is never hidden.  (Looking through V on every run, by the softmax warps or by two
-// warps of their own, made such tiles 1.5 to 2 times as long.)
+// masked places cannot change a row, and what a row attends to is never hidden.
+// (Looking through V on every run, by the softmax warps or by two warps of their
+// own, made such tiles 1.5 to 2 times as long.)
 //
 // Where there are few blocks, `parts` CTAs of a cluster share a block's walk over the
 // keys.  Each leaves O, m and l of its keys in shared memory (the idle Q and K/V
 // slots); each then brings a share of the rows to their common reference, adds the
 // parts up out of the cluster's distributed shared memory, divides and stores.
+//
+// Measured with masks: documents of 9,001 + 5,097 rows x 14 heads over 2 K/V heads
+// 653 us, 1,174 TFLOP/s on the pairs that are seen; of 4,584, 82, 2,292 and 701 rows
+// x 8 heads 134 - 141 us (800 TFLOP/s: 240 blocks of uneven length on 148 SMs); two
+// block prefixes over 7,660 rows, 8 over 2 heads, 130 us; 82 rows x 1 head 12 us,
+// launch and one block's latency.
 #pragma once
 
 #include "common.cuh"

@@ -20,6 +20,10 @@
 // `parts`, whose fp32 sums go to the workspace and are added in order by a third
 // kernel (9,001 + 5,097 rows, 14 heads over 2 K/V heads: 222 walks of up to 777 steps).
 //
+// Measured: that case 2.11 ms for the main kernel, 1,270 TFLOP/s of products done and
+// 909 of the five that a single walk would need; adding its parts 16 us.  1,127 causal
+// rows x 8 heads 19.5 us, three or four steps of each walk after another.
+//
 // dkdv works on S^T = K Q^T and dP^T = V dO^T (keys on the 128 TMEM lanes), so
 // that P^T and dS^T are, rounded to bf16 in place, the A operands of
 // dV += P^T dO and dK += dS^T Q straight from tensor memory; dq works on S and dP

@@ -19,6 +19,10 @@
 // of the weight gradient stay in the threads' registers over all rows that a
 // group walks and leave once as a partial row; a second kernel adds the
 // partials in a fixed order, so results do not depend on scheduling.
+//
+// Measured at 28,196 x 5,376 bf16 (a copy runs at 6.47 TB/s): forward 105 us, 5.8 TB/s;
+// layer norm's gradients 143 us, 6.3 TB/s, and 5 us for the partials; AdaLN's 172 us,
+// 5.3 TB/s (4,584 rows 35 us), 9 us for the sorting and 6 us for the partials.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -410,8 +414,8 @@ __global__ void __launch_bounds__(G > THREADS ? G : THREADS) layernorm_backward_
 // at a time.  One more warp copies rows into a ring of shared memory (bulk copies),
 // so reads from HBM go on while the block reduces and writes, and every pass reads
 // the rows from there, so that a thread's registers hold its parameters and column
-// sums for all rows.  A block is bound by the latency of its reductions and by
-// instruction issue; R rows share one reduction.
+// sums for all rows.  A block is bound by the latency of its reductions; R rows share
+// one reduction, and two blocks per SM hide each other's.
 constexpr int MAX_SLOTS = 4;
 constexpr unsigned long long RING_DRAIN_NS = 2000000000ull;
 
@@ -853,7 +857,8 @@ __global__ void __launch_bounds__(64 * 16) norm_reduce_kernel(const float* __res
 // may lie anywhere.  Rows are first put in the order of their entries (stable,
 // so sums do not depend on scheduling): blocks of SORT_ROWS rows count their
 // entries, then every block finds where its rows of each entry begin and places
-// them.  Rows whose entry is out of range go to one more bucket at the end.
+// them.  Rows whose entry is out of range go to one more bucket at the end.  Latency
+// alone: 2.3 and 6.5 us at 28,196 rows.
 constexpr int SORT_ROWS = 1024;
 constexpr int MAX_ENTRIES = 8192;      // the counts of one block in shared memory
 
@@ -1016,7 +1021,9 @@ __global__ void __launch_bounds__(G > THREADS ? G : THREADS) adaln_backward_kern
 // and find its statistics, and G threads with CH chunks each turn rows into dx and
 // column sums, with the entry's weights in registers while it lasts.  No step needs a
 // barrier of the block: a row's statistics are shuffles of one warp, and rows pass
-// from warp to warp by one mbarrier each way.
+// from warp to warp by one mbarrier each way.  (With the block's barriers instead, as
+// in the layer norm above, 28,196 x 5,376 took 218 us and not 172.)  What bounds it is
+// how many rows are on their way from memory while S of the ring's rows are read.
 constexpr int ADALN_SLOTS = 10;
 
 struct RowTerms {            // dx = (dy w) rstd + x b + c, xhat = x rstd + shift

@@ -167,8 +167,9 @@ struct GroupedRope {
 // row are those of both tensors in a row, so a lane still meets the same pairs
 // in every item.  The rotation back (the gradient) is the same kernel with a
 // table of negated frequencies.  B items per lane are in flight: 14 (8 chunk pairs)
-// for wide rows; 4 (2) and twice the blocks per SM for rows of few heads, whose time
-// is the latency of the trigonometry.
+// for wide rows (28,196 rows x 84 heads 194 - 201 us, 6.0 - 6.3 TB/s: HBM); 4 (2) and
+// twice the blocks per SM for rows of few heads, whose time is the latency of the
+// trigonometry (4,584 rows x 10 heads 8.0 us, 2.9 TB/s).
 template <int LAYOUT, int B, int CTAS_PER_SM>
 __global__ void __launch_bounds__(ROPE_THREADS, CTAS_PER_SM) rope_grouped_kernel(
     const GroupedRope p, const float* __restrict__ coords, long long n_rows, const RopeTable tab) {
