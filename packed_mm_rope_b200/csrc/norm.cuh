@@ -21,8 +21,8 @@
 // partials in a fixed order, so results do not depend on scheduling.
 //
 // Measured at 28,196 x 5,376 bf16 (a copy runs at 6.47 TB/s): forward 105 us, 5.8 TB/s;
-// layer norm's gradients 143 us, 6.3 TB/s, and 5 us for the partials; AdaLN's 172 us,
-// 5.3 TB/s (4,584 rows 35 us), 9 us for the sorting and 6 us for the partials.
+// layer norm's gradients 143 us, 6.3 TB/s, and 5 us for the partials; AdaLN's 158 us,
+// 5.8 TB/s (4,584 rows 35 us), 9 us for the sorting and 6 us for the partials.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -1022,13 +1022,29 @@ __global__ void __launch_bounds__(G > THREADS ? G : THREADS) adaln_backward_kern
 // column sums, with the entry's weights in registers while it lasts.  No step needs a
 // barrier of the block: a row's statistics are shuffles of one warp, and rows pass
 // from warp to warp by one mbarrier each way.  (With the block's barriers instead, as
-// in the layer norm above, 28,196 x 5,376 took 218 us and not 172.)  What bounds it is
+// in the layer norm above, 28,196 x 5,376 took 218 us and not 158.)  What bounds it is
 // how many rows are on their way from memory while S of the ring's rows are read.
 constexpr int ADALN_SLOTS = 10;
 
 struct RowTerms {            // dx = (dy w) rstd + x b + c, xhat = x rstd + shift
   float rstd, shift, b, c;
 };
+
+// Table entries: read again for every row, to stay in the L1 cache.
+__device__ __forceinline__ float4 load_kept(const float* p) {
+  float4 v;
+  asm volatile("ld.global.nc.L1::evict_last.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p));
+  return v;
+}
+// Results: not to displace them there (28,196 x 5,376 172 -> 166 us, and room for a
+// larger ring).
+__device__ __forceinline__ void store_past_l1(__nv_bfloat16* p, const Chunk<__nv_bfloat16>& c) {
+  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(c.w[0]), "r"(c.w[1]),
+               "r"(c.w[2]), "r"(c.w[3])
+               : "memory");
+}
 
 // Terms of a row in shared memory by one warp; lane 0 holds the result.
 __device__ __forceinline__ RowTerms adaln_row_terms(const uint8_t* x, const uint8_t* dy, const float* scale, int chunks,
@@ -1050,8 +1066,7 @@ __device__ __forceinline__ RowTerms adaln_row_terms(const uint8_t* x, const uint
 #pragma unroll 2
   for (int c = lane; c < chunks; c += 32) {
     const Chunk<T> ux = ring_chunk<T>(x, c), ud = ring_chunk<T>(dy, c);
-    const float4 w0 = __ldg(reinterpret_cast<const float4*>(scale) + 2 * c);
-    const float4 w1 = __ldg(reinterpret_cast<const float4*>(scale) + 2 * c + 1);
+    const float4 w0 = load_kept(scale + 8 * c), w1 = load_kept(scale + 8 * c + 4);
     const float2 w[4] = {{w0.x, w0.y}, {w0.z, w0.w}, {w1.x, w1.y}, {w1.z, w1.w}};
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -1189,7 +1204,7 @@ __global__ void __launch_bounds__(G + 32 * (S + 1), 1) adaln_backward_ring_kerne
           db[k][m] = __fadd2_rn(db[k][m], d);
           set_pair(o, m, __ffma2_rn(__fmul2_rn(d, w[k][m]), rs, __ffma2_rn(xv, b2, c0)));
         }
-        store_chunk<T, true>(out, 8 * c, hidden, o);
+        store_past_l1(out + 8 * c, o);
       }
     }
     ring.release(at);

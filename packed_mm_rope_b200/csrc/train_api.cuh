@@ -209,10 +209,11 @@ h3_status with_adaln_ring(int hidden, F f) {
 }
 
 // Warps that find the terms of rows, and the ring's size: what it leaves of an SM's 256 KB
-// caches the table entry that these warps read.  28,196 x 5,376: 4, 5, 6, 7 warps with 150 KB
-// 184, 172, 172, 173 us; 6 warps with 129, 150, 172 KB 179, 172, 177 us.
+// caches the table entry that these warps read.  28,196 x 5,376: 4, 5, 6, 7 warps (with
+// 150 KB) 184, 172, 172, 173 us; 6 warps with 129, 150, 172, 194, 215 KB, results stored past
+// that cache, 175, 166, 161, 158, 212 us.
 constexpr int kAdalnWarps = 6;
-constexpr uint64_t kAdalnSmem = 160u << 10;
+constexpr uint64_t kAdalnSmem = 200u << 10;
 
 struct AdalnWork {
   long long groups, per;               // row groups, sorted positions per group
