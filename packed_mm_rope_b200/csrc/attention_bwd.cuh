@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(256, 3) prep_kernel(const __grid_constant__ Pr
                                                       int n_q, int n_k, int n_heads, int n_qt, long long o_stride,
                                                       long long do_stride, float2* __restrict__ stat,
                                                       int2* __restrict__ rng, int4* __restrict__ hull) {
+  begin_after_predecessor(o, dout, lse, ranges);
   const int tile = blockIdx.x, head = blockIdx.y, batch = blockIdx.z;
   const int sub = threadIdx.x & 15, first = tile * BM + (threadIdx.x >> 4);
   const long long bh = static_cast<long long>(batch) * n_heads + head;
@@ -951,6 +952,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 backward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                 const __grid_constant__ Params p) {
+  begin_after_predecessor();
   extern __shared__ uint8_t smem_raw[];
   const unsigned n_dkdv = static_cast<unsigned>(p.n_kt) * p.parts * p.n_kv_heads * p.batch;
   unsigned i = blockIdx.x;
@@ -970,6 +972,7 @@ backward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 
 // dV and dK of split walks: the parts' sums in order, four columns per thread.
 __global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ Params p) {
+  begin_after_predecessor();
   const long long tile_size = static_cast<long long>(2) * BN * HD;
   const long long tiles = static_cast<long long>(p.batch) * p.n_kv_heads * p.n_kt;
   const long long n = tiles * (tile_size / 4);

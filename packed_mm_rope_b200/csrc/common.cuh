@@ -179,6 +179,17 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
 // ------------------------------------------- clusters, distributed smem ----
 
 // All threads of all CTAs of the cluster; what was written before is seen after.
+// Begin of a kernel that is launched while the one before it in the stream may still
+// run: lets the next such kernel be set up in turn, then waits until the one before
+// has ended and its writes can be seen.  The pointers are laundered so that no load
+// through them, read-only ones included, is moved above the wait.
+template <typename... T>
+__device__ __forceinline__ void begin_after_predecessor(T&... pointers) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  ([](auto& q) { asm volatile("" : "+l"(q)); }(pointers), ...);
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");

@@ -232,6 +232,7 @@ template <typename T, typename P, bool VEC, int G, int CH>
 __global__ void __launch_bounds__(G > THREADS ? G : THREADS) layernorm_kernel(
     const T* x, T* y, const P* __restrict__ weight, const P* __restrict__ bias, float* __restrict__ mean_out,
     float* __restrict__ rstd_out, long long n_rows, int hidden, long long x_stride, long long y_stride, float eps) {
+  begin_after_predecessor(x, weight, bias);
   constexpr int BLOCK = G > THREADS ? G : THREADS;
   constexpr int GROUPS = BLOCK / G;
   __shared__ float buf[GROUPS][2][1][G / 32];
@@ -385,6 +386,7 @@ __global__ void __launch_bounds__(G > THREADS ? G : THREADS) layernorm_backward_
     const T* dy, const T* x, const float* __restrict__ mean, const float* __restrict__ rstd,
     const P* __restrict__ weight, T* dx, float* __restrict__ partials, long long n_rows, int hidden,
     long long dy_stride, long long x_stride, long long dx_stride) {
+  begin_after_predecessor(dy, x, mean, rstd, weight);
   constexpr int BLOCK = G > THREADS ? G : THREADS;
   constexpr int GROUPS = BLOCK / G;
   __shared__ float buf[GROUPS][2][2][G / 32];
@@ -615,6 +617,7 @@ __global__ void __launch_bounds__(G + 32, MINB) layernorm_ring_kernel(
     const T* x, T* y, const P* __restrict__ weight, const P* __restrict__ bias, float* __restrict__ mean_out,
     float* __restrict__ rstd_out, long long n_rows, int hidden, long long x_stride, long long y_stride, float eps,
     int slots, unsigned long long limit, int err_slot) {
+  begin_after_predecessor(x, weight, bias);
   extern __shared__ __align__(128) uint8_t rows[];
   __shared__ uint64_t bars[2 * MAX_SLOTS];
   __shared__ uint32_t abort_word;
@@ -747,6 +750,7 @@ __global__ void __launch_bounds__(G + 32, MINB) layernorm_backward_ring_kernel(
     const T* dy, const T* x, const float* __restrict__ mean, const float* __restrict__ rstd,
     const P* __restrict__ weight, T* dx, float* __restrict__ partials, long long n_rows, int hidden,
     long long dy_stride, long long x_stride, long long dx_stride, int slots, unsigned long long limit, int err_slot) {
+  begin_after_predecessor(dy, x, mean, rstd, weight);
   extern __shared__ __align__(128) uint8_t rows[];
   __shared__ uint64_t bars[2 * MAX_SLOTS];
   __shared__ uint32_t abort_word;
@@ -845,6 +849,7 @@ __device__ __forceinline__ void reduce_partials(const float* __restrict__ partia
 template <typename P>
 __global__ void __launch_bounds__(64 * 16) norm_reduce_kernel(const float* __restrict__ partials, int n_partials,
                                                                 int hidden, P* dweight, P* dbias) {
+  begin_after_predecessor(partials);
   P* out = blockIdx.y == 0 ? dweight : dbias;
   if (out == nullptr) return;
   reduce_partials<16, 1>(partials, 0, n_partials, blockIdx.y, hidden,
@@ -872,6 +877,7 @@ __global__ void __launch_bounds__(SORT_ROWS) adaln_count_kernel(const int32_t* _
                                                                 const int32_t* __restrict__ tags, int n_entries,
                                                                 long long n_rows, int* __restrict__ hist,
                                                                 int err_slot) {
+  begin_after_predecessor(ts, tags);
   extern __shared__ int counts[];
   for (int e = threadIdx.x; e <= n_entries; e += SORT_ROWS) counts[e] = 0;
   __syncthreads();
@@ -892,6 +898,7 @@ __global__ void __launch_bounds__(SORT_ROWS) adaln_place_kernel(const int32_t* _
                                                                 long long n_rows, const int* __restrict__ hist,
                                                                 int n_blocks, int2* __restrict__ order,
                                                                 int* __restrict__ starts) {
+  begin_after_predecessor(ts, tags, hist);
   extern __shared__ int base[];            // [n_entries + 1]: where this block's rows of the entry go
   __shared__ int warp_total[SORT_ROWS / 32];
   __shared__ int carry;
@@ -956,6 +963,7 @@ __global__ void __launch_bounds__(G > THREADS ? G : THREADS) adaln_backward_kern
     const __nv_bfloat16* dy, const __nv_bfloat16* x, const float* __restrict__ table, const int2* __restrict__ order,
     __nv_bfloat16* dx, float* __restrict__ partials, int n_entries, long long n_rows, long long per, int hidden,
     long long dy_stride, long long x_stride, long long dx_stride, float eps) {
+  begin_after_predecessor(dy, x, table, order);
   using T = __nv_bfloat16;
   constexpr int BLOCK = G > THREADS ? G : THREADS;
   constexpr int GROUPS = BLOCK / G;
@@ -1098,6 +1106,7 @@ __global__ void __launch_bounds__(G + 32 * (S + 1), 1) adaln_backward_ring_kerne
     __nv_bfloat16* dx, float* __restrict__ partials, int n_entries, long long n_rows, long long per, int hidden,
     long long dy_stride, long long x_stride, long long dx_stride, float eps, int slots, unsigned long long limit,
     int err_slot) {
+  begin_after_predecessor(dy, x, table, order);
   using T = __nv_bfloat16;
   extern __shared__ __align__(128) uint8_t rows[];
   __shared__ uint64_t bars[3 * ADALN_SLOTS];
@@ -1218,6 +1227,7 @@ template <int ROWS>
 __global__ void __launch_bounds__(64 * ROWS) adaln_reduce_kernel(const float* __restrict__ partials,
                                                                  const int* __restrict__ starts, long long per,
                                                                  int hidden, float* __restrict__ dtable) {
+  begin_after_predecessor(partials, starts);
   const int e = blockIdx.y >> 1, half = blockIdx.y & 1;
   const long long a = starts[e], b = starts[e + 1];
   const long long c0 = a / per, c1 = b > a ? (b - 1) / per + 1 : c0;   // groups with rows of entry e

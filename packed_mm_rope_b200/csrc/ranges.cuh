@@ -17,6 +17,7 @@ namespace h3 {
 __global__ void __launch_bounds__(256) key_ranges_kernel(const int32_t* __restrict__ starts,
                                                          const int32_t* __restrict__ prefix, int n_docs, int n_rows,
                                                          int mode, int2* __restrict__ ranges, int err_slot) {
+  begin_after_predecessor(starts, prefix);
   const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
   const long long tid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   // a table that does not ascend inside [0, n_rows] is an input fault; its rows

@@ -173,6 +173,7 @@ struct GroupedRope {
 template <int LAYOUT, int B, int CTAS_PER_SM>
 __global__ void __launch_bounds__(ROPE_THREADS, CTAS_PER_SM) rope_grouped_kernel(
     const GroupedRope p, const float* __restrict__ coords, long long n_rows, const RopeTable tab) {
+  begin_after_predecessor(coords);
   constexpr int IPH = LAYOUT == 0 ? 16 : 8;        // work items per head
   constexpr int PPI = LAYOUT == 0 ? 4 : 8;         // rotary pairs per item
   const int lane = threadIdx.x & 31;

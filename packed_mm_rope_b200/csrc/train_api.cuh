@@ -5,7 +5,23 @@
 
 namespace {
 
-h3_status launched() { return cudaGetLastError() == cudaSuccess ? H3_OK : H3_ERR_CUDA; }
+// Launches a kernel that begins with begin_after_predecessor(): it may be set up while
+// the kernel before it in the stream still runs (about 2 us per launch), and reads and
+// writes nothing until that one has ended.
+template <typename... P, typename... A>
+h3_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? H3_OK : H3_ERR_CUDA;
+}
 
 inline uint64_t up256(uint64_t b) { return (b + 255u) & ~uint64_t(255u); }
 
@@ -173,8 +189,7 @@ h3_status launch_ring(const RingPlan& plan, int threads, cudaStream_t s, Args...
       return H3_ERR_CUDA;
     done[dev].store(epoch);
   }
-  Kernel<<<static_cast<unsigned>(plan.blocks), threads, plan.smem, s>>>(args...);
-  return launched();
+  return launch(Kernel, dim3(static_cast<unsigned>(plan.blocks)), threads, plan.smem, s, args...);
 }
 
 // Blocks of the plain backward row kernels (a partial row per group of each).
@@ -326,10 +341,9 @@ h3_status h3_build_key_ranges(const int32_t* d_doc_starts, const int32_t* d_pref
   if (reinterpret_cast<uintptr_t>(d_ranges) & 7u) return H3_ERR_UNSUPPORTED;
   const long long need = (std::max<long long>(n_rows, n_docs + 1LL) + 255) / 256;
   const int grid = static_cast<int>(std::min<long long>(need, 8LL * sm_count()));
-  h3::key_ranges_kernel<<<grid, 256, 0, as_stream(stream)>>>(d_doc_starts, d_prefix, n_docs, static_cast<int>(n_rows),
+  return launch(h3::key_ranges_kernel, dim3(grid), 256, 0, as_stream(stream), d_doc_starts, d_prefix, n_docs, static_cast<int>(n_rows),
                                                              mode, reinterpret_cast<int2*>(d_ranges),
                                                              error_slot(stream));
-  return launched();
 }
 
 h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v, void* d_o, float* d_lse,
@@ -375,12 +389,14 @@ h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v,
   cfg.blockDim = dim3(h3::attn::THREADS);
   cfg.dynamicSmemBytes = h3::attn::MASKED_SMEM_BYTES;
   cfg.stream = as_stream(stream);
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = static_cast<unsigned>(p.parts);
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = p.parts > 1 ? 1 : 0;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // as launch()
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = static_cast<unsigned>(p.parts);
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = p.parts > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, h3::attn::attention_kernel<true>, tq, tk, tv, p) == cudaSuccess ? H3_OK : H3_ERR_CUDA;
 }
 
@@ -472,13 +488,11 @@ h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const 
                                     st->v,
                                     p.group,
                                     p.scale_log2};
-  h3::attn_bwd::prep_kernel<<<dim3(w.n_qt, heads, batch), 256, 0, s>>>(
-      in, static_cast<const __nv_bfloat16*>(d_o), static_cast<const __nv_bfloat16*>(d_do), d_lse,
+  h3_status rc = launch(h3::attn_bwd::prep_kernel, dim3(w.n_qt, heads, batch), 256, 0, s, in, static_cast<const __nv_bfloat16*>(d_o), static_cast<const __nv_bfloat16*>(d_do), d_lse,
       reinterpret_cast<const int2*>(d_ranges), p.n_q, p.n_k, p.n_heads, w.n_qt, st->o, st->dout, stat, rng, hull);
-  h3::attn_bwd::backward_kernel<<<static_cast<unsigned>(blocks), h3::attn_bwd::THREADS, h3::attn_bwd::SMEM_BYTES, s>>>(
-      tq, tk, tv, tdo, p);
-  if (w.parts > 1) h3::attn_bwd::sum_parts_kernel<<<8 * sm_count(), 256, 0, s>>>(p);
-  return launched();
+  if (rc == H3_OK) rc = launch(h3::attn_bwd::backward_kernel, dim3(static_cast<unsigned>(blocks)), h3::attn_bwd::THREADS, h3::attn_bwd::SMEM_BYTES, s, tq, tk, tv, tdo, p);
+  if (rc == H3_OK && w.parts > 1) rc = launch(h3::attn_bwd::sum_parts_kernel, dim3(8 * sm_count()), 256, 0, s, p);
+  return rc;
 }
 
 h3_status h3_mmrope_rotate(const void* d_q, const void* d_k, void* d_q_out, void* d_k_out, const float* d_coords,
@@ -521,8 +535,7 @@ h3_status h3_mmrope_rotate(const void* d_q, const void* d_k, void* d_q_out, void
   const long long nblk = (n_rows + warps_per_cta - 1) / warps_per_cta;
   auto go = [&](auto kernel, int ctas) {
     const long long grid = std::min<long long>(nblk, 2LL * ctas * sm_count());
-    kernel<<<static_cast<unsigned>(grid), h3::ROPE_THREADS, 0, as_stream(stream)>>>(p, d_coords, n_rows, tab);
-    return launched();
+    return launch(kernel, dim3(static_cast<unsigned>(grid)), h3::ROPE_THREADS, 0, as_stream(stream), p, d_coords, n_rows, tab);
   };
   // up to 16 heads a lane has at most 8 chunks of a row
   if (n_heads + n_kv_heads <= 16)
@@ -568,11 +581,9 @@ h3_status h3_layernorm(const void* d_x, void* d_y, const void* d_weight, const v
       using S = decltype(shape);
       const long long grid = std::min<long long>((n_rows + S::GROUPS - 1) / S::GROUPS, 16LL * sms);
       auto go = [&](auto kernel) {
-        kernel<<<static_cast<unsigned>(grid), S::BLOCK, 0, as_stream(stream)>>>(
-            static_cast<const T*>(d_x), static_cast<T*>(d_y), static_cast<const P*>(d_weight),
+        return launch(kernel, dim3(static_cast<unsigned>(grid)), S::BLOCK, 0, as_stream(stream), static_cast<const T*>(d_x), static_cast<T*>(d_y), static_cast<const P*>(d_weight),
             static_cast<const P*>(d_bias), d_mean, d_rstd, static_cast<long long>(n_rows), hidden, x_row_stride,
             y_row_stride, eps);
-        return launched();
       };
       if constexpr (S::ALIGNED)
         if (vec) return go(h3::norm::layernorm_kernel<T, P, true, S::G, S::CH>);
@@ -630,11 +641,9 @@ h3_status h3_layernorm_backward(const void* d_dy, const void* d_x, const float* 
         const long long grid = backward_blocks<S>(n_rows);
         groups = grid * S::GROUPS;
         auto go = [&](auto kernel) {
-          kernel<<<static_cast<unsigned>(grid), S::BLOCK, 0, as_stream(stream)>>>(
-              static_cast<const T*>(d_dy), static_cast<const T*>(d_x), d_mean, d_rstd, static_cast<const P*>(d_weight),
+          return launch(kernel, dim3(static_cast<unsigned>(grid)), S::BLOCK, 0, as_stream(stream), static_cast<const T*>(d_dy), static_cast<const T*>(d_x), d_mean, d_rstd, static_cast<const P*>(d_weight),
               static_cast<T*>(d_dx), partials, static_cast<long long>(n_rows), hidden, dy_row_stride, x_row_stride,
               dx_row_stride);
-          return launched();
         };
         if constexpr (S::ALIGNED)
           if (vec) return go(h3::norm::layernorm_backward_kernel<T, P, true, S::G, S::CH>);
@@ -642,9 +651,7 @@ h3_status h3_layernorm_backward(const void* d_dy, const void* d_x, const float* 
       });
     }
     if (st != H3_OK || !params) return st;
-    h3::norm::norm_reduce_kernel<P><<<dim3((hidden + 63) / 64, 2), 64 * 16, 0, as_stream(stream)>>>(
-        partials, static_cast<int>(groups), hidden, static_cast<P*>(d_dweight), static_cast<P*>(d_dbias));
-    return launched();
+    return launch(h3::norm::norm_reduce_kernel<P>, dim3((hidden + 63) / 64, 2), 64 * 16, 0, as_stream(stream), partials, static_cast<int>(groups), hidden, static_cast<P*>(d_dweight), static_cast<P*>(d_dbias));
   });
 }
 
@@ -685,11 +692,10 @@ h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const in
   int* hist = reinterpret_cast<int*>(base + w.hist);
   float* partials = reinterpret_cast<float*>(base + w.partials);
   const size_t smem = (static_cast<size_t>(n_entries) + 1u) * sizeof(int);
-  h3::norm::adaln_count_kernel<<<w.blocks, h3::norm::SORT_ROWS, smem, s>>>(d_timestep_index, d_token_tag, n_entries,
+  h3_status st = launch(h3::norm::adaln_count_kernel, dim3(w.blocks), h3::norm::SORT_ROWS, smem, s, d_timestep_index, d_token_tag, n_entries,
                                                                            n_rows, hist, error_slot(stream));
-  h3::norm::adaln_place_kernel<<<w.blocks, h3::norm::SORT_ROWS, smem, s>>>(d_timestep_index, d_token_tag, n_entries,
+  if (st == H3_OK) st = launch(h3::norm::adaln_place_kernel, dim3(w.blocks), h3::norm::SORT_ROWS, smem, s, d_timestep_index, d_token_tag, n_entries,
                                                                            n_rows, hist, w.blocks, order, starts);
-  h3_status st = launched();
   if (st != H3_OK) return st;
   if (ring_takes(hidden))
     st = with_adaln_ring(hidden, [&](auto shape) {
@@ -709,11 +715,9 @@ h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const in
     st = with_backward_shape(hidden, [&](auto shape) {
       using S = decltype(shape);
       if constexpr (S::G == 32) {            // up to 1,024 elements
-        h3::norm::adaln_backward_kernel<S::G, S::CH><<<static_cast<unsigned>(w.groups / S::GROUPS), S::BLOCK, 0, s>>>(
-            static_cast<const __nv_bfloat16*>(d_dy), static_cast<const __nv_bfloat16*>(d_x), d_table, order,
+        return launch(h3::norm::adaln_backward_kernel<S::G, S::CH>, dim3(static_cast<unsigned>(w.groups / S::GROUPS)), S::BLOCK, 0, s, static_cast<const __nv_bfloat16*>(d_dy), static_cast<const __nv_bfloat16*>(d_x), d_table, order,
             static_cast<__nv_bfloat16*>(d_dx), partials, n_entries, n_rows, w.per, hidden, dy_row_stride, x_row_stride,
             dx_row_stride, eps);
-        return launched();
       } else {
         return H3_ERR_UNSUPPORTED;
       }
@@ -722,10 +726,8 @@ h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const in
   // many partial rows per entry are added by 16 rows of threads, few by 2
   const dim3 rgrid((hidden + 255) / 256, 2 * n_entries);
   if (w.groups >= 8LL * n_entries)
-    h3::norm::adaln_reduce_kernel<16><<<rgrid, 64 * 16, 0, s>>>(partials, starts, w.per, hidden, d_dtable);
-  else
-    h3::norm::adaln_reduce_kernel<2><<<rgrid, 64 * 2, 0, s>>>(partials, starts, w.per, hidden, d_dtable);
-  return launched();
+    return launch(h3::norm::adaln_reduce_kernel<16>, rgrid, 64 * 16, 0, s, partials, starts, w.per, hidden, d_dtable);
+  return launch(h3::norm::adaln_reduce_kernel<2>, rgrid, 64 * 2, 0, s, partials, starts, w.per, hidden, d_dtable);
 }
 
 }  // extern "C"

@@ -227,6 +227,53 @@ def test_calls_at_once_on_two_streams(h3):
         assert h3.h3_check_device_error(s.cuda_stream) == h3.H3_OK
 
 
+def test_calls_behind_other_work(h3):
+    """Inputs written just before by fills, copies, torch kernels, another stream or another call, eagerly and in a
+    captured graph with branches: each call waits for what precedes it."""
+    n, c = 1200, 1280
+    src = [randn(40 + i, n, c) for i in range(2)]
+    x, dy = torch.empty_like(src[0]), torch.empty_like(src[0])
+    level, tag = (torch.arange(n, device="cuda") % 7).int(), (torch.arange(n, device="cuda") % 3).int()
+    table, zero = torch.empty(21, 2, c, device="cuda"), torch.zeros(21, 2, c, device="cuda")
+    side = torch.cuda.Stream()
+
+    def run():
+        x.zero_()
+        table.copy_(zero)
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            dy.zero_()
+            dy.add_(src[1])
+            b = h3.layer_norm(dy)[0]
+        x.copy_(src[0])
+        table.add_(0.25)
+        here.wait_stream(side)
+        dx, dt = h3.adaln_modulate_backward(dy, x, level, tag, table)
+        y, mean, rstd = h3.layer_norm(dx, out=dx)      # in place behind the call that wrote it
+        g = h3.layer_norm_backward(b, y, mean, rstd, dx=b)
+        q = y.view(n, 10, 128)
+        qr, _ = h3.mmrope_rotate(q, None, coords, q_out=q)
+        r = h3.build_key_ranges(starts, n, "prefix_causal")
+        lse = torch.empty(10, n, device="cuda")
+        o = h3.masked_attention(qr, qr, qr, r, lse=lse)
+        return (dt, *g, o, *h3.masked_attention_backward(o, qr, qr, qr, o, lse, r))
+
+    coords, starts = randn(44, n, 3, dtype=torch.float32), starts_of([700, 3, 497])
+    torch.cuda.synchronize()
+    want = [t.clone() for t in run()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(want, run()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(20):
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert h3.h3_check_device_error() == h3.H3_OK
+
+
 def test_single_rows_and_heads_of_larger_tensors(h3):
     """Sizes of one: their strides say nothing."""
     q, k, v = randn(1, 3, 5, 4, 128), randn(2, 3, 5, 2, 128), randn(3, 3, 5, 2, 128)
