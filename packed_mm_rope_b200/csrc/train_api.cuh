@@ -20,7 +20,9 @@ h3_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cuda
   cfg.stream = s;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? H3_OK : H3_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess) return H3_OK;
+  cudaGetLastError();
+  return H3_ERR_CUDA;
 }
 
 inline uint64_t up256(uint64_t b) { return (b + 255u) & ~uint64_t(255u); }
@@ -54,7 +56,8 @@ bool overlap(const RowSpan& a, const RowSpan& b) {
   if (a0 >= end(b) || b0 >= end(a)) return false;
   const int64_t sa = (a.rows == 1 ? b.stride : a.stride) * a.size, sb = (b.rows == 1 ? a.stride : b.stride) * b.size;
   if (sa != sb || sa == 0) return true;
-  const int64_t apart = a0 <= b0 ? static_cast<int64_t>((b0 - a0) % sa) : (sa - static_cast<int64_t>((a0 - b0) % sa)) % sa;
+  const int64_t apart =
+      a0 <= b0 ? static_cast<int64_t>((b0 - a0) % sa) : (sa - static_cast<int64_t>((a0 - b0) % sa)) % sa;
   return apart < a.width * a.size || sa - apart < b.width * b.size;
 }
 
@@ -165,7 +168,7 @@ struct RingPlan {
 };
 
 RingPlan ring_plan(int64_t n_rows, size_t row_bytes, int tensors, int ctas, std::initializer_list<int> choices) {
-  const uint64_t budget = kRingSmem / ctas - 3072u;
+  const uint64_t budget = kRingSmem / ctas - (3u << 10);
   RingPlan p{1, 1, 0, 0};
   for (int r : choices)
     if (n_rows >= 2LL * r * ctas * kRingSms && 2u * r * tensors * row_bytes <= budget) p.rows = std::max(p.rows, r);
@@ -341,9 +344,8 @@ h3_status h3_build_key_ranges(const int32_t* d_doc_starts, const int32_t* d_pref
   if (reinterpret_cast<uintptr_t>(d_ranges) & 7u) return H3_ERR_UNSUPPORTED;
   const long long need = (std::max<long long>(n_rows, n_docs + 1LL) + 255) / 256;
   const int grid = static_cast<int>(std::min<long long>(need, 8LL * sm_count()));
-  return launch(h3::key_ranges_kernel, dim3(grid), 256, 0, as_stream(stream), d_doc_starts, d_prefix, n_docs, static_cast<int>(n_rows),
-                                                             mode, reinterpret_cast<int2*>(d_ranges),
-                                                             error_slot(stream));
+  return launch(h3::key_ranges_kernel, dim3(grid), 256, 0, as_stream(stream), d_doc_starts, d_prefix, n_docs,
+                static_cast<int>(n_rows), mode, reinterpret_cast<int2*>(d_ranges), error_slot(stream));
 }
 
 h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v, void* d_o, float* d_lse,
@@ -488,10 +490,15 @@ h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const 
                                     st->v,
                                     p.group,
                                     p.scale_log2};
-  h3_status rc = launch(h3::attn_bwd::prep_kernel, dim3(w.n_qt, heads, batch), 256, 0, s, in, static_cast<const __nv_bfloat16*>(d_o), static_cast<const __nv_bfloat16*>(d_do), d_lse,
-      reinterpret_cast<const int2*>(d_ranges), p.n_q, p.n_k, p.n_heads, w.n_qt, st->o, st->dout, stat, rng, hull);
-  if (rc == H3_OK) rc = launch(h3::attn_bwd::backward_kernel, dim3(static_cast<unsigned>(blocks)), h3::attn_bwd::THREADS, h3::attn_bwd::SMEM_BYTES, s, tq, tk, tv, tdo, p);
-  if (rc == H3_OK && w.parts > 1) rc = launch(h3::attn_bwd::sum_parts_kernel, dim3(8 * sm_count()), 256, 0, s, p);
+  h3_status rc = launch(h3::attn_bwd::prep_kernel, dim3(w.n_qt, heads, batch), 256, 0, s, in,
+                        static_cast<const __nv_bfloat16*>(d_o), static_cast<const __nv_bfloat16*>(d_do), d_lse,
+                        reinterpret_cast<const int2*>(d_ranges), p.n_q, p.n_k, p.n_heads, w.n_qt, st->o, st->dout, stat,
+                        rng, hull);
+  if (rc == H3_OK)
+    rc = launch(h3::attn_bwd::backward_kernel, dim3(static_cast<unsigned>(blocks)), h3::attn_bwd::THREADS,
+                h3::attn_bwd::SMEM_BYTES, s, tq, tk, tv, tdo, p);
+  if (rc == H3_OK && w.parts > 1)
+    rc = launch(h3::attn_bwd::sum_parts_kernel, dim3(8 * sm_count()), 256, 0, s, p);
   return rc;
 }
 
@@ -535,7 +542,8 @@ h3_status h3_mmrope_rotate(const void* d_q, const void* d_k, void* d_q_out, void
   const long long nblk = (n_rows + warps_per_cta - 1) / warps_per_cta;
   auto go = [&](auto kernel, int ctas) {
     const long long grid = std::min<long long>(nblk, 2LL * ctas * sm_count());
-    return launch(kernel, dim3(static_cast<unsigned>(grid)), h3::ROPE_THREADS, 0, as_stream(stream), p, d_coords, n_rows, tab);
+    return launch(kernel, dim3(static_cast<unsigned>(grid)), h3::ROPE_THREADS, 0, as_stream(stream), p, d_coords,
+                  n_rows, tab);
   };
   // up to 16 heads a lane has at most 8 chunks of a row
   if (n_heads + n_kv_heads <= 16)
@@ -581,9 +589,9 @@ h3_status h3_layernorm(const void* d_x, void* d_y, const void* d_weight, const v
       using S = decltype(shape);
       const long long grid = std::min<long long>((n_rows + S::GROUPS - 1) / S::GROUPS, 16LL * sms);
       auto go = [&](auto kernel) {
-        return launch(kernel, dim3(static_cast<unsigned>(grid)), S::BLOCK, 0, as_stream(stream), static_cast<const T*>(d_x), static_cast<T*>(d_y), static_cast<const P*>(d_weight),
-            static_cast<const P*>(d_bias), d_mean, d_rstd, static_cast<long long>(n_rows), hidden, x_row_stride,
-            y_row_stride, eps);
+        return launch(kernel, dim3(static_cast<unsigned>(grid)), S::BLOCK, 0, as_stream(stream),
+                      static_cast<const T*>(d_x), static_cast<T*>(d_y), static_cast<const P*>(d_weight),
+                      static_cast<const P*>(d_bias), d_mean, d_rstd, n_rows, hidden, x_row_stride, y_row_stride, eps);
       };
       if constexpr (S::ALIGNED)
         if (vec) return go(h3::norm::layernorm_kernel<T, P, true, S::G, S::CH>);
@@ -641,9 +649,10 @@ h3_status h3_layernorm_backward(const void* d_dy, const void* d_x, const float* 
         const long long grid = backward_blocks<S>(n_rows);
         groups = grid * S::GROUPS;
         auto go = [&](auto kernel) {
-          return launch(kernel, dim3(static_cast<unsigned>(grid)), S::BLOCK, 0, as_stream(stream), static_cast<const T*>(d_dy), static_cast<const T*>(d_x), d_mean, d_rstd, static_cast<const P*>(d_weight),
-              static_cast<T*>(d_dx), partials, static_cast<long long>(n_rows), hidden, dy_row_stride, x_row_stride,
-              dx_row_stride);
+          return launch(kernel, dim3(static_cast<unsigned>(grid)), S::BLOCK, 0, as_stream(stream),
+                        static_cast<const T*>(d_dy), static_cast<const T*>(d_x), d_mean, d_rstd,
+                        static_cast<const P*>(d_weight), static_cast<T*>(d_dx), partials, n_rows, hidden, dy_row_stride,
+                        x_row_stride, dx_row_stride);
         };
         if constexpr (S::ALIGNED)
           if (vec) return go(h3::norm::layernorm_backward_kernel<T, P, true, S::G, S::CH>);
@@ -651,7 +660,8 @@ h3_status h3_layernorm_backward(const void* d_dy, const void* d_x, const float* 
       });
     }
     if (st != H3_OK || !params) return st;
-    return launch(h3::norm::norm_reduce_kernel<P>, dim3((hidden + 63) / 64, 2), 64 * 16, 0, as_stream(stream), partials, static_cast<int>(groups), hidden, static_cast<P*>(d_dweight), static_cast<P*>(d_dbias));
+    return launch(h3::norm::norm_reduce_kernel<P>, dim3((hidden + 63) / 64, 2), 64 * 16, 0, as_stream(stream), partials,
+                  static_cast<int>(groups), hidden, static_cast<P*>(d_dweight), static_cast<P*>(d_dbias));
   });
 }
 
@@ -692,10 +702,11 @@ h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const in
   int* hist = reinterpret_cast<int*>(base + w.hist);
   float* partials = reinterpret_cast<float*>(base + w.partials);
   const size_t smem = (static_cast<size_t>(n_entries) + 1u) * sizeof(int);
-  h3_status st = launch(h3::norm::adaln_count_kernel, dim3(w.blocks), h3::norm::SORT_ROWS, smem, s, d_timestep_index, d_token_tag, n_entries,
-                                                                           n_rows, hist, error_slot(stream));
-  if (st == H3_OK) st = launch(h3::norm::adaln_place_kernel, dim3(w.blocks), h3::norm::SORT_ROWS, smem, s, d_timestep_index, d_token_tag, n_entries,
-                                                                           n_rows, hist, w.blocks, order, starts);
+  h3_status st = launch(h3::norm::adaln_count_kernel, dim3(w.blocks), h3::norm::SORT_ROWS, smem, s, d_timestep_index,
+                        d_token_tag, n_entries, n_rows, hist, error_slot(stream));
+  if (st == H3_OK)
+    st = launch(h3::norm::adaln_place_kernel, dim3(w.blocks), h3::norm::SORT_ROWS, smem, s, d_timestep_index,
+                d_token_tag, n_entries, n_rows, hist, w.blocks, order, starts);
   if (st != H3_OK) return st;
   if (ring_takes(hidden))
     st = with_adaln_ring(hidden, [&](auto shape) {
@@ -715,9 +726,10 @@ h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const in
     st = with_backward_shape(hidden, [&](auto shape) {
       using S = decltype(shape);
       if constexpr (S::G == 32) {            // up to 1,024 elements
-        return launch(h3::norm::adaln_backward_kernel<S::G, S::CH>, dim3(static_cast<unsigned>(w.groups / S::GROUPS)), S::BLOCK, 0, s, static_cast<const __nv_bfloat16*>(d_dy), static_cast<const __nv_bfloat16*>(d_x), d_table, order,
-            static_cast<__nv_bfloat16*>(d_dx), partials, n_entries, n_rows, w.per, hidden, dy_row_stride, x_row_stride,
-            dx_row_stride, eps);
+        return launch(h3::norm::adaln_backward_kernel<S::G, S::CH>, dim3(static_cast<unsigned>(w.groups / S::GROUPS)),
+                      S::BLOCK, 0, s, static_cast<const __nv_bfloat16*>(d_dy), static_cast<const __nv_bfloat16*>(d_x),
+                      d_table, order, static_cast<__nv_bfloat16*>(d_dx), partials, n_entries, n_rows, w.per, hidden,
+                      dy_row_stride, x_row_stride, dx_row_stride, eps);
       } else {
         return H3_ERR_UNSUPPORTED;
       }
