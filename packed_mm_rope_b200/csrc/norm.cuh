@@ -490,6 +490,14 @@ struct BlockSum {
   static constexpr int PER = 32 / WP;              // values that the lanes add up at once
   static constexpr int SIZE = 2 * M * WP;
 
+  // Where in a set a lane finds its partial of values g PER .. g PER + PER - 1, or -1:
+  // with fewer values than lanes to add them up, or a padded number of warps, the
+  // others would read beyond the set, into the one that the next sum is written to.
+  static __host__ __device__ constexpr int source(int g, int lane) {
+    const int value = g * PER + lane / WP, warp = lane % WP;
+    return value < N && warp < W ? value * WP + warp : -1;
+  }
+
   static __device__ __forceinline__ bool sum(float (&v)[N], float* buf, int& parity, bool fail) {
     const int lane = threadIdx.x & 31;
     float a[M];
@@ -520,7 +528,8 @@ struct BlockSum {
         : "memory");
 #pragma unroll
     for (int g = 0; g < (N + PER - 1) / PER; ++g) {
-      float s = (lane & (WP - 1)) < W ? set[g * 32 + lane] : 0.f;
+      const int from = source(g, lane);
+      float s = from >= 0 ? set[from] : 0.f;
 #pragma unroll
       for (int o = WP / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
 #pragma unroll
