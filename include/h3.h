@@ -147,13 +147,15 @@ int32_t h3_version(void);
  * counterpart; it is plumbing.  Checks that `device` exists and has compute
  * capability 10.0 (the kernels are built for sm_100a only) and that the
  * kernels load on it, then does once what every other call otherwise does
- * lazily on first use: the shared-memory opt-ins of the kernels, the lookup of
- * the driver's tensor-map encoder, the host-buffer pipeline's two streams and
- * events, the address of the no-allocation scratch; and clears the device's
- * error words.  Allocates no device memory at run time (loading the kernels
- * on the device commits the module's static arrays, among them the 64 MiB
- * no-allocation scratch).  The calling thread's current device is left as it
- * was.  Calling it again is harmless.
+ * lazily on first use: the shared-memory opt-ins of the attention kernels, the
+ * lookup of the driver's tensor-map encoder, the host-buffer pipeline's two
+ * streams and events, the address of the no-allocation scratch; and clears the
+ * device's error words.  (The kernels of the layer norm and of the AdaLN
+ * gradients, one per type and range of row lengths, opt in when each is first
+ * used; stream capture allows it.)  Allocates no device memory at run time
+ * (loading the kernels on the device commits the module's static arrays, among
+ * them the 64 MiB no-allocation scratch).  The calling thread's current device
+ * is left as it was.  Calling it again is harmless.
  * Errors: H3_ERR_INVALID_ARG (no such device), H3_ERR_UNSUPPORTED (another
  * architecture, or the kernels do not load), H3_ERR_CUDA.
  */

@@ -28,13 +28,22 @@ constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;   // 2 s per wait
 constexpr uint64_t kDrainLimitNs = 2000000000ull;
 std::atomic<uint64_t> g_wait_limit_ns{kDefaultWaitLimitNs};
 
+// Whether a runtime call succeeded.  Its failure becomes the library call's status, so it
+// does not stay behind as this thread's last error, which a later call would report as its own.
+inline bool cuda_ok(cudaError_t e) {
+  if (e == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 // One-time set-up of the current device, kept until h3_shutdown: the
-// shared-memory opt-ins of the kernels that need more than 48 KB (function
-// attributes are per device) and the SM count.
+// shared-memory opt-ins of the attention kernels, which need more than 48 KB
+// (function attributes are per device), and the SM count.  The layer norm and
+// AdaLN gradient kernels, of which there are many, opt in as they are first used.
 struct DeviceState {
   bool ready = false;
   int sms = 148;
@@ -46,19 +55,19 @@ std::atomic<uint32_t> g_attr_epoch{1};   // raised by h3_shutdown: kernel attrib
 
 const DeviceState* device_state() {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  if (!cuda_ok(cudaGetDevice(&dev)) || dev < 0 || dev >= 64) return nullptr;
   std::lock_guard<std::mutex> lock(g_state_mu);
   DeviceState& st = g_states[dev];
   if (!st.ready) {
-    if (cudaFuncSetAttribute(h3::attn::attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(h3::attn::SMEM_BYTES)) != cudaSuccess ||
-        cudaFuncSetAttribute(h3::attn::attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(h3::attn::MASKED_SMEM_BYTES)) != cudaSuccess ||
-        cudaFuncSetAttribute(h3::attn_bwd::backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(h3::attn_bwd::SMEM_BYTES)) != cudaSuccess)
+    auto opt_in = [](auto kernel, uint32_t bytes) {
+      return cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)));
+    };
+    if (!opt_in(h3::attn::attention_kernel<false>, h3::attn::SMEM_BYTES) ||
+        !opt_in(h3::attn::attention_kernel<true>, h3::attn::MASKED_SMEM_BYTES) ||
+        !opt_in(h3::attn_bwd::backward_kernel, h3::attn_bwd::SMEM_BYTES))
       return nullptr;
     int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0) st.sms = n;
+    if (cuda_ok(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) && n > 0) st.sms = n;
     st.ready = true;
   }
   return &st;
@@ -79,7 +88,7 @@ int g_slots_used[64];
 
 int error_slot(void* stream) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (!cuda_ok(cudaGetDevice(&dev)) || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(g_slot_mu);
   for (int i = 1; i <= g_slots_used[dev]; ++i)
     if (g_slot_stream[dev][i] == stream) return i;
@@ -100,7 +109,7 @@ EncodeTiledFn encode_tiled() {
   std::call_once(once, [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+    if (cuda_ok(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q)) &&
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<EncodeTiledFn>(p);
   });
@@ -390,14 +399,14 @@ HostPipe* host_pipe() {
   std::mutex& mu = g_pipes_mu;
   HostPipe* pipes = g_pipes;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  if (!cuda_ok(cudaGetDevice(&dev)) || dev < 0 || dev >= 64) return nullptr;
   std::lock_guard<std::mutex> lock(mu);
   HostPipe& hp = pipes[dev];
   if (!hp.ok) {
-    bool made = cudaStreamCreateWithFlags(&hp.h2d, cudaStreamNonBlocking) == cudaSuccess &&
-                cudaStreamCreateWithFlags(&hp.d2h, cudaStreamNonBlocking) == cudaSuccess;
+    bool made = cuda_ok(cudaStreamCreateWithFlags(&hp.h2d, cudaStreamNonBlocking)) &&
+                cuda_ok(cudaStreamCreateWithFlags(&hp.d2h, cudaStreamNonBlocking));
     for (auto& e : hp.ev)
-      made = made && cudaEventCreateWithFlags(&e, cudaEventDisableTiming) == cudaSuccess;
+      made = made && cuda_ok(cudaEventCreateWithFlags(&e, cudaEventDisableTiming));
     if (!made) {   // release whatever was created; the next call tries again
       for (auto& e : hp.ev)
         if (e != nullptr) cudaEventDestroy(e), e = nullptr;
@@ -419,7 +428,7 @@ void release_host_pipes() {
     HostPipe& hp = g_pipes[dev];
     if (!hp.ok) continue;
     std::lock_guard<std::mutex> q(hp.enqueue);
-    if (cudaSetDevice(dev) != cudaSuccess) continue;
+    if (!cuda_ok(cudaSetDevice(dev))) continue;
     cudaStreamSynchronize(hp.h2d);
     cudaStreamSynchronize(hp.d2h);
     for (auto& e : hp.ev) {
@@ -507,23 +516,22 @@ h3_status h3_packed_mmrope_attention_host(const h3_segment* segs, int32_t nseg, 
   cudaEvent_t* ev_in = hp->ev;
   cudaEvent_t* ev_out = hp->ev + HostPipe::kMaxChunks;
   cudaEvent_t ev_start = hp->ev[2 * HostPipe::kMaxChunks], ev_end = hp->ev[2 * HostPipe::kMaxChunks + 1];
-  auto ck = [](cudaError_t e) { return e == cudaSuccess; };
   // After a failure with copies already queued: order `stream` after both copy
   // streams, so that a caller who synchronises `stream` and then frees its
   // host buffers cannot race a copy still in flight.
   auto fail = [&](h3_status status) {
-    if (ck(cudaEventRecord(ev_end, hp->h2d))) cudaStreamWaitEvent(s, ev_end, 0);
-    if (ck(cudaEventRecord(ev_start, hp->d2h))) cudaStreamWaitEvent(s, ev_start, 0);
+    if (cuda_ok(cudaEventRecord(ev_end, hp->h2d))) cuda_ok(cudaStreamWaitEvent(s, ev_end, 0));
+    if (cuda_ok(cudaEventRecord(ev_start, hp->d2h))) cuda_ok(cudaStreamWaitEvent(s, ev_start, 0));
     return status;
   };
 
   // both copy streams start after the work already queued on `stream`
-  if (!ck(cudaEventRecord(ev_start, s)) || !ck(cudaStreamWaitEvent(hp->h2d, ev_start, 0)) ||
-      !ck(cudaStreamWaitEvent(hp->d2h, ev_start, 0)))
+  if (!cuda_ok(cudaEventRecord(ev_start, s)) || !cuda_ok(cudaStreamWaitEvent(hp->h2d, ev_start, 0)) ||
+      !cuda_ok(cudaStreamWaitEvent(hp->d2h, ev_start, 0)))
     return H3_ERR_CUDA;
   // coordinates (after the permutation is on the device)
   if (h_perm != nullptr) {
-    if (!ck(cudaMemcpyAsync(dperm, h_perm, static_cast<size_t>(n_rows) * 4, cudaMemcpyHostToDevice, s)))
+    if (!cuda_ok(cudaMemcpyAsync(dperm, h_perm, static_cast<size_t>(n_rows) * 4, cudaMemcpyHostToDevice, s)))
       return fail(H3_ERR_CUDA);
   }
   st = h3_build_coords(segs, nseg, h_perm ? dperm : nullptr, n_rows, dcoords, stream);
@@ -535,11 +543,11 @@ h3_status h3_packed_mmrope_attention_host(const h3_segment* segs, int32_t nseg, 
     for (int x = 0; x < 3; ++x) {
       const uint8_t* src = static_cast<const uint8_t*>(x == 0 ? h_q : x == 1 ? h_k : h_v) + off;
       uint8_t* dst = (x == 0 ? dq : x == 1 ? dk : dv) + off;
-      if (!ck(cudaMemcpy2DAsync(dst, row_bytes, src, row_bytes, width, static_cast<size_t>(n_rows),
-                                cudaMemcpyHostToDevice, hp->h2d)))
+      if (!cuda_ok(cudaMemcpy2DAsync(dst, row_bytes, src, row_bytes, width, static_cast<size_t>(n_rows),
+                                     cudaMemcpyHostToDevice, hp->h2d)))
         return fail(H3_ERR_CUDA);
     }
-    if (!ck(cudaEventRecord(ev_in[c], hp->h2d)) || !ck(cudaStreamWaitEvent(s, ev_in[c], 0)))
+    if (!cuda_ok(cudaEventRecord(ev_in[c], hp->h2d)) || !cuda_ok(cudaStreamWaitEvent(s, ev_in[c], 0)))
       return fail(H3_ERR_CUDA);
     // rotate this chunk's Q and K in place, then attend over all rows for its heads
     st = h3_mmrope_qk(dq + off, dk + off, dq + off, dk + off, dcoords, n_rows, nh,
@@ -548,14 +556,14 @@ h3_status h3_packed_mmrope_attention_host(const h3_segment* segs, int32_t nseg, 
     st = h3_packed_attention(dq + off, dk + off, dv + off, d_o + off, nullptr, nullptr, nullptr, 1, n_rows, nh, 128,
                              static_cast<int64_t>(n_heads) * 128, 0.f, stream);
     if (st != H3_OK) return fail(st);
-    if (!ck(cudaEventRecord(ev_out[c], s)) || !ck(cudaStreamWaitEvent(hp->d2h, ev_out[c], 0)))
+    if (!cuda_ok(cudaEventRecord(ev_out[c], s)) || !cuda_ok(cudaStreamWaitEvent(hp->d2h, ev_out[c], 0)))
       return fail(H3_ERR_CUDA);
-    if (!ck(cudaMemcpy2DAsync(static_cast<uint8_t*>(h_o) + off, row_bytes, d_o + off, row_bytes, width,
-                              static_cast<size_t>(n_rows), cudaMemcpyDeviceToHost, hp->d2h)))
+    if (!cuda_ok(cudaMemcpy2DAsync(static_cast<uint8_t*>(h_o) + off, row_bytes, d_o + off, row_bytes, width,
+                                   static_cast<size_t>(n_rows), cudaMemcpyDeviceToHost, hp->d2h)))
       return fail(H3_ERR_CUDA);
   }
   // `stream` is ordered after the last copy out (and, through it, all others)
-  if (!ck(cudaEventRecord(ev_end, hp->d2h)) || !ck(cudaStreamWaitEvent(s, ev_end, 0))) return fail(H3_ERR_CUDA);
+  if (!cuda_ok(cudaEventRecord(ev_end, hp->d2h)) || !cuda_ok(cudaStreamWaitEvent(s, ev_end, 0))) return fail(H3_ERR_CUDA);
   return H3_OK;
 }
 
@@ -579,11 +587,11 @@ void* g_scratch_addr[64];
 // fails.  A device reset moves the array, hence h3_shutdown before any reset.
 void* noalloc_scratch() {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  if (!cuda_ok(cudaGetDevice(&dev)) || dev < 0 || dev >= 64) return nullptr;
   std::lock_guard<std::mutex> lock(g_scratch_mu);
   if (g_scratch_addr[dev] == nullptr) {
     void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess) return nullptr;
+    if (!cuda_ok(cudaGetSymbolAddress(&p, g_noalloc_scratch))) return nullptr;
     g_scratch_addr[dev] = p;
   }
   return g_scratch_addr[dev];
@@ -622,11 +630,11 @@ h3_status h3_packed_mmrope_attention_host_noalloc(const h3_segment* segs, int32_
 
   // everything in order on `stream`: copies in, coords, rope, attention, copy out
   if (h_perm != nullptr &&
-      cudaMemcpyAsync(dperm, h_perm, static_cast<size_t>(n_rows) * 4, cudaMemcpyHostToDevice, s) != cudaSuccess)
+      !cuda_ok(cudaMemcpyAsync(dperm, h_perm, static_cast<size_t>(n_rows) * 4, cudaMemcpyHostToDevice, s)))
     return H3_ERR_CUDA;
-  if (cudaMemcpyAsync(dq, h_q, bytes, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-      cudaMemcpyAsync(dk, h_k, bytes, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-      cudaMemcpyAsync(dv, h_v, bytes, cudaMemcpyHostToDevice, s) != cudaSuccess)
+  if (!cuda_ok(cudaMemcpyAsync(dq, h_q, bytes, cudaMemcpyHostToDevice, s)) ||
+      !cuda_ok(cudaMemcpyAsync(dk, h_k, bytes, cudaMemcpyHostToDevice, s)) ||
+      !cuda_ok(cudaMemcpyAsync(dv, h_v, bytes, cudaMemcpyHostToDevice, s)))
     return H3_ERR_CUDA;
   h3_status st = h3_build_coords(segs, nseg, h_perm ? dperm : nullptr, n_rows, dcoords, stream);
   if (st != H3_OK) return st;
@@ -634,7 +642,7 @@ h3_status h3_packed_mmrope_attention_host_noalloc(const h3_segment* segs, int32_
   if (st != H3_OK) return st;
   st = h3_packed_attention(dq, dk, dv, d_o, nullptr, nullptr, nullptr, 1, n_rows, n_heads, 128, rs, 0.f, stream);
   if (st != H3_OK) return st;
-  if (cudaMemcpyAsync(h_o, d_o, bytes, cudaMemcpyDeviceToHost, s) != cudaSuccess) return H3_ERR_CUDA;
+  if (!cuda_ok(cudaMemcpyAsync(h_o, d_o, bytes, cudaMemcpyDeviceToHost, s))) return H3_ERR_CUDA;
   return H3_OK;
 }
 
@@ -642,10 +650,10 @@ h3_status h3_check_device_error(void* stream) {
   // this stream's word, taken by a kernel ordered after the work already on it
   const int slot = error_slot(stream);
   h3::take_error_word<<<1, 1, 0, as_stream(stream)>>>(slot);
-  if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(as_stream(stream)) != cudaSuccess)
+  if (cudaGetLastError() != cudaSuccess || !cuda_ok(cudaStreamSynchronize(as_stream(stream))))
     return H3_ERR_CUDA;
   unsigned int word = 0;
-  if (cudaMemcpyFromSymbol(&word, h3::g_error_snapshot, sizeof(word), sizeof(word) * slot) != cudaSuccess)
+  if (!cuda_ok(cudaMemcpyFromSymbol(&word, h3::g_error_snapshot, sizeof(word), sizeof(word) * slot)))
     return H3_ERR_CUDA;
   if (word & h3::DEVERR_TIMEOUT) return H3_ERR_TIMEOUT;
   if (word & h3::DEVERR_INPUT) return H3_ERR_DEVICE_INPUT;
@@ -661,7 +669,7 @@ namespace {
 // Restores the calling thread's current device on scope exit.
 struct DeviceGuard {
   int saved = -1;
-  DeviceGuard() { if (cudaGetDevice(&saved) != cudaSuccess) saved = -1; }
+  DeviceGuard() { if (!cuda_ok(cudaGetDevice(&saved))) saved = -1; }
   ~DeviceGuard() { if (saved >= 0) cudaSetDevice(saved); }
 };
 
@@ -671,22 +679,22 @@ extern "C" {
 
 h3_status h3_init(int32_t device) {
   int count = 0;
-  if (cudaGetDeviceCount(&count) != cudaSuccess) return H3_ERR_CUDA;
+  if (!cuda_ok(cudaGetDeviceCount(&count))) return H3_ERR_CUDA;
   if (device < 0 || device >= count || device >= 64) return H3_ERR_INVALID_ARG;
   int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess)
+  if (!cuda_ok(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device)) ||
+      !cuda_ok(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device)))
     return H3_ERR_CUDA;
   if (major != 10 || minor != 0) return H3_ERR_UNSUPPORTED;   // the kernels are built for sm_100a only
   DeviceGuard guard;
-  if (cudaSetDevice(device) != cudaSuccess) return H3_ERR_CUDA;
+  if (!cuda_ok(cudaSetDevice(device))) return H3_ERR_CUDA;
   cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, h3::attn::attention_kernel<false>) != cudaSuccess) return H3_ERR_UNSUPPORTED;
+  if (!cuda_ok(cudaFuncGetAttributes(&fa, h3::attn::attention_kernel<false>))) return H3_ERR_UNSUPPORTED;
   if (encode_tiled() == nullptr || device_state() == nullptr || host_pipe() == nullptr ||
       noalloc_scratch() == nullptr)
     return H3_ERR_CUDA;
   static const unsigned int zeros[h3::ERR_SLOTS] = {};
-  if (cudaMemcpyToSymbol(h3::g_error_words, zeros, sizeof(zeros)) != cudaSuccess) return H3_ERR_CUDA;
+  if (!cuda_ok(cudaMemcpyToSymbol(h3::g_error_words, zeros, sizeof(zeros)))) return H3_ERR_CUDA;
   return H3_OK;
 }
 

@@ -20,9 +20,7 @@ h3_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cuda
   cfg.stream = s;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess) return H3_OK;
-  cudaGetLastError();
-  return H3_ERR_CUDA;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...)) ? H3_OK : H3_ERR_CUDA;
 }
 
 inline uint64_t up256(uint64_t b) { return (b + 255u) & ~uint64_t(255u); }
@@ -184,11 +182,10 @@ h3_status launch_ring(const RingPlan& plan, int threads, cudaStream_t s, Args...
   // the opt-in to more than 48 KB of shared memory, once per kernel and device until h3_shutdown
   static std::atomic<uint32_t> done[64];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return H3_ERR_CUDA;
+  if (!cuda_ok(cudaGetDevice(&dev)) || dev < 0 || dev >= 64) return H3_ERR_CUDA;
   const uint32_t epoch = g_attr_epoch.load();
   if (done[dev].load() != epoch) {
-    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingSmem)) !=
-        cudaSuccess)
+    if (!cuda_ok(cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingSmem))))
       return H3_ERR_CUDA;
     done[dev].store(epoch);
   }
@@ -399,7 +396,7 @@ h3_status h3_masked_attention(const void* d_q, const void* d_k, const void* d_v,
   attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = p.parts > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, h3::attn::attention_kernel<true>, tq, tk, tv, p) == cudaSuccess ? H3_OK : H3_ERR_CUDA;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, h3::attn::attention_kernel<true>, tq, tk, tv, p)) ? H3_OK : H3_ERR_CUDA;
 }
 
 uint64_t h3_masked_attention_backward_workspace_bytes(const h3_attn_shape* a) {
@@ -434,8 +431,8 @@ h3_status h3_masked_attention_backward(const void* d_do, const void* d_q, const 
   cudaStream_t s = as_stream(stream);
   if (!queries) {                          // no row reads the keys
     const size_t rows = static_cast<size_t>(a->batch) * a->n_k, width = static_cast<size_t>(a->n_kv_heads) * 256u;
-    return cudaMemset2DAsync(d_dk, static_cast<size_t>(st->dk) * 2u, 0, width, rows, s) == cudaSuccess &&
-                   cudaMemset2DAsync(d_dv, static_cast<size_t>(st->dv) * 2u, 0, width, rows, s) == cudaSuccess
+    return cuda_ok(cudaMemset2DAsync(d_dk, static_cast<size_t>(st->dk) * 2u, 0, width, rows, s)) &&
+                   cuda_ok(cudaMemset2DAsync(d_dv, static_cast<size_t>(st->dv) * 2u, 0, width, rows, s))
                ? H3_OK
                : H3_ERR_CUDA;
   }
@@ -692,7 +689,7 @@ h3_status h3_adaln_modulate_backward(const void* d_dy, const void* d_x, const in
     return H3_ERR_INVALID_ARG;
   cudaStream_t s = as_stream(stream);
   if (n_rows == 0)
-    return cudaMemsetAsync(d_dtable, 0, static_cast<size_t>(n_entries) * 2u * hidden * 4u, s) == cudaSuccess
+    return cuda_ok(cudaMemsetAsync(d_dtable, 0, static_cast<size_t>(n_entries) * 2u * hidden * 4u, s))
                ? H3_OK
                : H3_ERR_CUDA;
   const AdalnWork w = adaln_work(n_rows, hidden, n_entries);
