@@ -5,7 +5,8 @@
 The library is one translation unit (csrc/h3.cu includes the kernels), linked
 against the static CUDA runtime; the driver's tensor-map encoder is looked up
 at run time, so no libcuda link is needed.  _tensors.so (csrc/binding.cpp) is a
-Python module over the library's C ABI, linked against it and PyTorch.
+Python module over the library's C ABI, linked against it and PyTorch; where there
+is no PyTorch with CUDA to build it against, the library is built alone.
 """
 from __future__ import annotations
 
@@ -62,18 +63,38 @@ def _run(cmd: list, target: str, verbose: bool) -> None:
         sys.stdout.write(r.stderr)
 
 
+def _cxx():
+    return shutil.which("g++") or shutil.which("c++")
+
+
+def binding_lacks() -> str | None:
+    """What the tensor binding would need and is not there, or None."""
+    try:
+        import torch
+    except ImportError:
+        return "PyTorch"
+    if torch.version.cuda is None:
+        return "a PyTorch with CUDA"
+    if _cxx() is None:
+        return "a C++ compiler"
+    if not os.path.exists(os.path.join(sysconfig.get_path("include"), "Python.h")):
+        return "the Python headers"
+    return None
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Build _tensors.so; raises RuntimeError where that cannot be done."""
     if not force and up_to_date(BINDING):
         return BINDING
+    lacks = binding_lacks()
+    if lacks is not None:
+        raise RuntimeError(f"{os.path.basename(BINDING)} cannot be built without {lacks}")
     import torch
     from torch.utils import cpp_extension
-    cxx = shutil.which("g++") or shutil.which("c++")
-    if cxx is None:
-        raise RuntimeError("no C++ compiler found")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     include = [sysconfig.get_path("include"), *cpp_extension.include_paths(), os.path.join(cuda, "include")]
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG",
+    cmd = [_cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", "-DNDEBUG",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     for path in include:
         cmd += ["-isystem", path]
@@ -84,9 +105,19 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Build libh3.so and, where it can be built, the tensor binding; returns the library's path.
+
+    A user of the C ABI needs no PyTorch: without one the binding is left out, with a line on stderr, and
+    the Python calls that go through it raise ImportError.
+    """
     if force or not up_to_date():
         _run([nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), os.path.join(CSRC, "h3.cu")], LIB, verbose)
-    build_binding(force, verbose)
+    if force or not up_to_date(BINDING):
+        lacks = binding_lacks()
+        if lacks is not None:
+            sys.stderr.write(f"{os.path.basename(BINDING)} left out: no {lacks.removeprefix('a ')}\n")
+            return LIB
+        build_binding(force, verbose)
     return LIB
 
 
