@@ -1067,19 +1067,25 @@ __device__ __forceinline__ void store_past_l1(__nv_bfloat16* p, const Chunk<__nv
 __device__ __forceinline__ RowTerms adaln_row_terms(const uint8_t* x, const uint8_t* dy, const float* scale, int chunks,
                                                     float inv_n, float eps, int lane) {
   using T = __nv_bfloat16;
-  float2 s = make_float2(0.f, 0.f);
+  // four sums side by side: a lane has up to 32 chunks of four pairs, and one chain of 128
+  // additions would be off by up to that many roundings (mean of 8,192 elements)
+  auto add_up = [](const float2 (&v)[4]) {
+    const float2 t = __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(v[2], v[3]));
+    return t.x + t.y;
+  };
+  float2 s[4] = {};
 #pragma unroll 4
   for (int c = lane; c < chunks; c += 32) {
     const Chunk<T> u = ring_chunk<T>(x, c);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) s = __fadd2_rn(s, pair_of(u, m));
+    for (int m = 0; m < 4; ++m) s[m] = __fadd2_rn(s[m], pair_of(u, m));
   }
-  float mean = s.x + s.y;
+  float mean = add_up(s);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
   mean *= inv_n;
   const float2 nm = make_float2(-mean, -mean);
-  float2 a0 = make_float2(0.f, 0.f), a1 = a0, a2 = a0;   // (x - mean)^2, g, g (x - mean)
+  float2 a0[4] = {}, a1[4] = {}, a2[4] = {};       // (x - mean)^2, g, g (x - mean)
 #pragma unroll 2
   for (int c = lane; c < chunks; c += 32) {
     const Chunk<T> ux = ring_chunk<T>(x, c), ud = ring_chunk<T>(dy, c);
@@ -1089,12 +1095,12 @@ __device__ __forceinline__ RowTerms adaln_row_terms(const uint8_t* x, const uint
     for (int m = 0; m < 4; ++m) {
       const float2 xc = __fadd2_rn(pair_of(ux, m), nm), d = pair_of(ud, m);
       const float2 g = __ffma2_rn(d, w[m], d);
-      a0 = __ffma2_rn(xc, xc, a0);
-      a1 = __fadd2_rn(a1, g);
-      a2 = __ffma2_rn(g, xc, a2);
+      a0[m] = __ffma2_rn(xc, xc, a0[m]);
+      a1[m] = __fadd2_rn(a1[m], g);
+      a2[m] = __ffma2_rn(g, xc, a2[m]);
     }
   }
-  float var = a0.x + a0.y, sg = a1.x + a1.y, sgx = a2.x + a2.y;
+  float var = add_up(a0), sg = add_up(a1), sgx = add_up(a2);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     var += __shfl_xor_sync(0xffffffffu, var, o);
