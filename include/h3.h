@@ -600,6 +600,8 @@ h3_status h3_check_device_error(void* stream);
  * Limit, in nanoseconds of device global time, of every bounded wait inside
  * the attention, layer norm and AdaLN gradient kernels (process-wide; default
  * 2e9 = 2 s).  0 restores the default.  Used by tests to force the timeout path.
+ * A wait looks several times before it looks at the clock, so what comes within
+ * microseconds may be waited for under a shorter limit.
  */
 h3_status h3_set_wait_limit_ns(uint64_t ns);
 

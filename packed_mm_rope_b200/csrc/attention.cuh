@@ -143,6 +143,13 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, r);
 }
 
+// The same for a walk's last product (one wait per block), short limits included.
+__device__ __forceinline__ bool warp_wait_exact(uint32_t bar, uint32_t parity, volatile uint32_t* abort,
+                                                uint64_t limit, int err_slot) {
+  const bool r = mbar_wait_exact(bar, parity, abort, limit, err_slot);
+  return __all_sync(0xffffffffu, r);
+}
+
 struct Params {
   int n_rows;
   int n_heads;
@@ -867,7 +874,8 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
 
     // epilogue: O / l -> bf16 -> global; optional log-sum-exp
-    if (ok && warp_wait(bar_o_full(wg), 0, abort_flag, limit, eslot)) {
+    if (ok && (MASKED ? warp_wait_exact(bar_o_full(wg), 0, abort_flag, limit, eslot)
+                      : warp_wait(bar_o_full(wg), 0, abort_flag, limit, eslot))) {
       tc_fence_after();
       // row sums over the four threads of each row
       l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);

@@ -67,6 +67,7 @@ using attn::any_nonfinite;
 using attn::zero_nonfinite;
 using attn::mma_wait;
 using attn::warp_wait;
+using attn::warp_wait_exact;
 
 constexpr int WARPS = 16;                     // element-wise warps
 constexpr int W_PROD = WARPS;
@@ -664,7 +665,7 @@ __device__ __forceinline__ void dkdv_block(const CUtensorMap& tm_q, const CUtens
       for (int r = 0; r < 16; ++r) pk[r] = pack_bf16x2(x[2 * r], x[2 * r + 1]);
       publish(t_dp, pk, bar_ds, lane);
     }
-    if (ok && warp_wait(bar_out, 0, abort_flag, limit, eslot)) {
+    if (ok && warp_wait_exact(bar_out, 0, abort_flag, limit, eslot)) {
       tc_fence_after();
       const long long r0 = static_cast<long long>(batch) * p.n_k;
       const int col = kvh * HD + 64 * half;
@@ -925,7 +926,7 @@ __device__ __forceinline__ void dq_block(const CUtensorMap& tm_q, const CUtensor
       for (int r = 0; r < 16; ++r) pk[r] = pack_bf16x2(x[2 * r], x[2 * r + 1]);
       publish(t_s, pk, bar_ds, lane);
     }
-    if (ok && warp_wait(bar_out, 0, abort_flag, limit, eslot)) {
+    if (ok && warp_wait_exact(bar_out, 0, abort_flag, limit, eslot)) {
       tc_fence_after();
       uint32_t v[32];
       load_acc(tmem + lb + TMEM_DQ + 64 * half, v);

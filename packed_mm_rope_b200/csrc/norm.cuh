@@ -448,7 +448,7 @@ struct Ring {
   }
   // Consumers: whether the step has landed (bounded wait); its slot is free again.
   __device__ __forceinline__ bool wait(RingAt at) const {
-    return mbar_wait_bounded(full + 8u * at.slot, at.phase, abort, limit, err_slot);
+    return mbar_wait_exact(full + 8u * at.slot, at.phase, abort, limit, err_slot);
   }
   __device__ __forceinline__ void release(RingAt at) const {
     __syncwarp();
@@ -461,7 +461,7 @@ struct Ring {
     RingAt at;
     int issued = 0;
     for (; issued < count; ++issued, at.next(slots)) {
-      if (issued >= slots && !mbar_wait_bounded(empty + 8u * at.slot, at.phase ^ 1u, abort, limit, err_slot)) break;
+      if (issued >= slots && !mbar_wait_exact(empty + 8u * at.slot, at.phase ^ 1u, abort, limit, err_slot)) break;
       const uint32_t bar = full + 8u * at.slot, to = data + at.slot * slot_bytes;
       const int n = rows(issued);
       mbar_arrive_expect_tx(bar, n * TENSORS * row_bytes);
@@ -1160,7 +1160,8 @@ __global__ void __launch_bounds__(G + 32 * (S + 1), 1) adaln_backward_ring_kerne
       if (i >= slots && !__all_sync(0xffffffffu, mbar_wait_bounded(ring.empty + 8u * at.slot, at.phase ^ 1u, &abort_word,
                                                                    limit, err_slot)))
         break;
-      if (!__all_sync(0xffffffffu, ring.wait(at))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(ring.full + 8u * at.slot, at.phase, &abort_word, limit, err_slot)))
+        break;
       const uint8_t* in = rows + at.slot * ring.slot_bytes;
       if (e < n_entries) {
         const RowTerms r =
