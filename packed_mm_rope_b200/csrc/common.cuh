@@ -194,9 +194,8 @@ __device__ __forceinline__ bool mbar_wait_exact(uint32_t bar, uint32_t parity, v
   return false;
 }
 
-// ------------------------------------------- clusters, distributed smem ----
+// ---------------------------------------------------------- launches ----
 
-// All threads of all CTAs of the cluster; what was written before is seen after.
 // Begin of a kernel that is launched while the one before it in the stream may still
 // run: lets the next such kernel be set up in turn, then waits until the one before
 // has ended and its writes can be seen.  The pointers are laundered so that no load
@@ -208,6 +207,9 @@ __device__ __forceinline__ void begin_after_predecessor(T&... pointers) {
   ([](auto& q) { asm volatile("" : "+l"(q)); }(pointers), ...);
 }
 
+// ------------------------------------------- clusters, distributed smem ----
+
+// All threads of all CTAs of the cluster; what was written before is seen after.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");

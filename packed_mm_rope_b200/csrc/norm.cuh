@@ -10,14 +10,17 @@
 // AdaLN is the same norm with w = 1 + scale[e], b = shift[e] gathered per row,
 // so its table gradient is dw, db summed over the rows of each entry e.
 //
-// All of it is HBM-bound: every row is read once (x, and dy backward), held in
-// registers as it was stored (16-byte chunks of 8 elements, two for fp32) and
-// written once.  Statistics and sums are fp32, in two passes over the
-// registers (mean, then squared deviations), so a large mean costs no digits.
-// A row belongs to a group of G threads: one warp for short rows, 128 to 512
-// threads for long ones; thread t holds chunks t, t + G, ...  The column sums
-// of the weight gradient stay in the threads' registers over all rows that a
-// group walks and leave once as a partial row; a second kernel adds the
+// All of it is HBM-bound: every row is read once (x, and dy backward) and written once.
+// Short rows, and rows that are not 16-byte aligned, are held in registers as they
+// were stored (chunks of 8 elements) by a group of G threads: one warp, or 128 to 512
+// threads for long rows; thread t holds chunks t, t + G, ...  Aligned rows of 1,025 to
+// 11,520 elements pass through rings of rows in shared memory instead (below).
+// Statistics and sums are fp32: first the mean, then the squared deviations from it, so
+// the variance loses nothing to a large mean.  xhat does: the mean is rounded to fp32, so
+// it is off by 2^-24 |mean| / deviation, and the ring kernels, which form xhat as
+// x rstd - mean rstd and dx as x B + C, add two or three roundings of that size.
+// The column sums of the weight gradient stay in the threads' registers over all rows
+// that a group walks and leave once as a partial row; a second kernel adds the
 // partials in a fixed order, so results do not depend on scheduling.
 //
 // Measured at 28,196 x 5,376 bf16 (a copy runs at 6.47 TB/s): forward 105 us, 5.8 TB/s;
