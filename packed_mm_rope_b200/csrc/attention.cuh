@@ -81,10 +81,13 @@
 // parts up out of the cluster's distributed shared memory, divides and stores.
 //
 // Measured with masks: documents of 9,001 + 5,097 rows x 14 heads over 2 K/V heads
-// 653 us, 1,174 TFLOP/s on the pairs that are seen; of 4,584, 82, 2,292 and 701 rows
-// x 8 heads 134 - 141 us (800 TFLOP/s: 240 blocks of uneven length on 148 SMs); two
-// block prefixes over 7,660 rows, 8 over 2 heads, 130 us; 82 rows x 1 head 12 us,
-// launch and one block's latency.
+// by itself, at 1,965 MHz, 653 us, 1,174 TFLOP/s on the pairs that are seen; in a loop
+// with its gradients, under the 1 kW power cap at 1,650 MHz, 769 us, 997 TFLOP/s.
+// Documents of 4,584, 82, 2,292 and 701 rows x 8 heads 134 - 141 us (800 TFLOP/s), two
+// block prefixes over 7,660 rows, 8 over 2 heads, 126 - 130 us: their 240 blocks of 6 to
+// 37 and 7 to 32 key tiles leave 46 and 41 steps per SM on average but 60 on the fullest,
+// so a quarter and a third of the SMs' time is idle.  82 rows x 1 head 12 us, launch and
+// one block's latency.
 #pragma once
 
 #include "common.cuh"
@@ -251,10 +254,12 @@ attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // masked: a flat grid, heads fastest, so that the longest walks of all heads come
-  // first and the shortest last.  Under a causal mask the last rows see the most
-  // keys, with documents any may: the end of the sequence whose row sees more leads.
-  // (8,192 causal rows x 8 heads, 256 blocks: heads slowest leaves 1.5 times as long.)
+  // masked: a flat grid, heads fastest, the tiles in the order of the sequence or, if the
+  // last row sees at least as many keys as the first, in the reverse order.  Under a causal
+  // mask that puts the longest walks of all heads first and the shortest last (8,192 causal
+  // rows x 8 heads, 256 blocks: heads slowest leaves 1.5 times as long); with documents it
+  // says nothing about the walks between the ends (two block prefixes of 1,201 / 4,096 and
+  // 880 / 3,564 rows: walks of 28, 7, 32 and 10 key tiles, in that order).
   const int n_tiles = (p.n_rows + 2 * BM - 1) / (2 * BM);
   int head = blockIdx.y, batch = blockIdx.z, tile = blockIdx.x, part = 0;
   if constexpr (MASKED) {

@@ -20,8 +20,10 @@
 // `parts`, whose fp32 sums go to the workspace and are added in order by a third
 // kernel (9,001 + 5,097 rows, 14 heads over 2 K/V heads: 222 walks of up to 777 steps).
 //
-// Measured: that case 2.11 ms for the main kernel, 1,270 TFLOP/s of products done and
-// 909 of the five that a single walk would need; adding its parts 16 us.  1,127 causal
+// Measured: that case by itself, at 1,965 MHz, 2.11 ms for the main kernel, 1,270 TFLOP/s of
+// products done and 909 of the five that a single walk would need; adding its parts 16 us.
+// In a loop with the forward call, under the 1 kW power cap at 1,650 MHz, the whole call
+// takes 2.48 ms, 1,085 and 775 TFLOP/s.  1,127 causal
 // rows x 8 heads 19.5 us, three or four steps of each walk after another.
 //
 // dkdv works on S^T = K Q^T and dP^T = V dO^T (keys on the 128 TMEM lanes), so
@@ -102,8 +104,9 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint4 a, const 
 
 // D of rows with at most this many keys comes from P and dP.  Against 64 bits that
 // takes the error of dQ and dK, which the roundings of dS and of the outputs alone
-// make 1.41 times that of the outputs' rounding, from 1.45 - 1.6 down to 1.44 of it at
-// most (documents of 20 to 2,000 rows, causal and full).
+// make 1.41 times that of the outputs' rounding, from 1.45 - 1.6 down to 1.41 - 1.44 of it
+// (documents of 20 to 2,000 rows, causal and full; up to 1.47 elsewhere.  Measured, not
+// bounds).
 constexpr int SHORT_ROW = 32;
 
 struct PrepInputs {

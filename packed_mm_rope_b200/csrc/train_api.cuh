@@ -305,10 +305,14 @@ AttentionWork attention_work(const h3_attn_shape* a) {
 }
 
 // CTAs that share a block's keys (a cluster): where SMs would stay idle, as many as
-// still run all at once, if each has two key tiles when every row sees every key.
-// (Joining the parts takes about 6 us: 2,304 rows x 8 heads 31 against 40 us.  Halving
-// walks for the sake of balance alone, with one to two blocks per SM, does not pay:
-// 7,660 rows in documents x 8 heads 181 against 158 us.)
+// still run all at once, if each has two key tiles when every row sees every key.  What
+// that gains depends on the walks, shared against not: 18 key tiles x 1 head (8 parts)
+// 21.4 / 39.8 us, x 8 heads (2 parts) 30.6 / 40.5; 9 tiles x 1 (4) 19.0 / 24.8, x 8 (2)
+// 23.6 / 25.3; 6 tiles x 8 (2) 18.3 / 19.8; 4 tiles x 8 (2) 16.9 / 16.6.  Only n_k is known
+// here, so masks may leave less: 95 documents of 80 rows, walks of up to 4 tiles cut in
+// four, 18.3 / 21.0; 30 of 256 rows x 2 heads, walks of 2 tiles cut in two, 16.3 / 14.1.
+// Halving walks for the sake of balance alone, with one to two blocks per SM, does not
+// pay: 7,660 rows in documents x 8 heads 181 against 158 us.
 int attention_parts(uint64_t blocks, int64_t n_k) {
   const int64_t tiles = (n_k + h3::attn::BN - 1) / h3::attn::BN;
   int parts = 1;
